@@ -38,6 +38,8 @@ __all__ = [
     "moe_plan_placement", "moe_workspace_bytes_mapped", "moe_dispatch_layout_mapped", "Placement",
     "moe_dispatch_pack_routed", "moe_routed_expert_stage1", "moe_dispatch_pack_nvfp4",
     "moe_expert_scale_nvfp4", "nvfp4_record_bytes", "mxfp8_record_bytes", "HostPipeline",
+    "MOE_TYPE_F32", "MOE_TYPE_BF16", "moe_balance_loss", "moe_balance_loss_workspace_bytes",
+    "moe_route_backward", "moe_combine_backward",
     "MoePath", "trace_enable", "trace_disable", "trace_reset", "trace_records",
 ]
 
@@ -49,6 +51,8 @@ MOE_ERR_TIMEOUT = 4
 MOE_ERR_CUDA = 5
 MOE_FORMAT_MXFP8 = 1
 MOE_FORMAT_NVFP4 = 2
+MOE_TYPE_F32 = 0
+MOE_TYPE_BF16 = 1
 
 
 def status_bit(code: int) -> int:
@@ -146,6 +150,13 @@ def load_library() -> ctypes.CDLL:
             "moe_permute_to_experts_masked": ([P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32,
                                                i32, i32, P, P, P, P, P, P], ctypes.c_int),
             "moe_expert_scale": ([P, P, P, i32, i32, i32, P, P], ctypes.c_int),
+            "moe_balance_loss_workspace_bytes": ([i32, i32, i32], sz),
+            "moe_balance_loss": ([P, i32, i32, i32, i32, i32, P, P, P, P, P, P, P, P, sz, P, P],
+                                 ctypes.c_int),
+            "moe_route_backward": ([P, i32, i32, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, P],
+                                   ctypes.c_int),
+            "moe_combine_backward": ([P, P, i32, P, P, P, i32, i32, i32, i32, P, P, P, P],
+                                     ctypes.c_int),
             "moe_trace_enable": ([ctypes.c_char_p, i32], ctypes.c_int),
             "moe_trace_disable": ([], None),
             "moe_trace_reset": ([], None),
@@ -193,6 +204,29 @@ def _status_ptr(dev_status):
     if dev_status is None:
         return ctypes.c_void_p(0)
     return _dev(dev_status, "dev_status", (torch.int32,))
+
+
+def _arr(t, name: str, dtypes, shape):
+    """Address of a contiguous CUDA tensor of one of `dtypes` and of `shape` (None: any size)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor (got {t.device})")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _opt(t, name: str, dtypes, shape):
+    return None if t is None else _arr(t, name, dtypes, shape)
+
+
+_I32, _F32, _U8 = (torch.int32,), (torch.float32,), (torch.uint8,)
+_LOGIT_TYPES = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16}
 
 
 def moe_version() -> int:
@@ -700,6 +734,67 @@ def trace_records() -> list[tuple[str, float]]:
         _check(lib.moe_trace_get(i, ctypes.byref(name), ctypes.byref(ms)))
         out.append((name.value.decode(), float(ms.value)))
     return out
+
+
+def moe_balance_loss_workspace_bytes(S: int, T: int, E: int) -> int:
+    return int(load_library().moe_balance_loss_workspace_bytes(S, T, E))
+
+
+def moe_balance_loss(logits, topk_ids, counts, prob_mean, lse, n_valid, losses, ws,
+                     token_mask=None, dev_status=None, stream=None):
+    """Router losses: logits f32 or bf16 [S,T,E], topk_ids i32 [S,T,k], token_mask uint8 [S,T]
+    (None: all valid) -> counts i32 [S,E], prob_mean f32 [S,E], lse f32 [S,T], n_valid i32 [S],
+    losses f32 [2] (balance, z); ws is a uint8 device tensor."""
+    lib = load_library()
+    S, T, E = logits.shape
+    k = topk_ids.shape[-1]
+    _check(lib.moe_balance_loss(
+        _arr(logits, "logits", _LOGIT_TYPES, None), _LOGIT_TYPES[logits.dtype], S, T, E, k,
+        _arr(topk_ids, "topk_ids", _I32, (S, T, k)), _opt(token_mask, "token_mask", _U8, (S, T)),
+        _arr(counts, "counts", _I32, (S, E)), _arr(prob_mean, "prob_mean", _F32, (S, E)),
+        _arr(lse, "lse", _F32, (S, T)), _arr(n_valid, "n_valid", _I32, (S,)),
+        _arr(losses, "losses", _F32, (2,)), _arr(ws, "ws", _U8, None), ws.numel(),
+        _opt(dev_status, "dev_status", _I32, None), _stream(stream)))
+
+
+def moe_route_backward(logits, topk_ids, topk_w, d_topk_w, lse, counts, n_valid, d_losses,
+                       d_logits, token_mask=None, dev_status=None, stream=None):
+    """Gradient in the logits [S,T,E] (f32 or bf16) of the routing weights (topk_w, d_topk_w f32
+    [S,T,k], both or neither None) and of the two losses (d_losses f32 [2] with what
+    moe_balance_loss wrote, or None) -> d_logits of the logits' type."""
+    lib = load_library()
+    S, T, E = d_logits.shape
+    if topk_ids is None and topk_w is not None:
+        raise ValueError("topk_ids: needed with topk_w")
+    k = topk_ids.shape[-1] if topk_ids is not None else 1
+    if d_losses is not None and topk_ids is None:
+        raise ValueError("topk_ids: needed with d_losses (k enters the balance loss)")
+    if d_losses is None:
+        logits = lse = counts = n_valid = None
+    _check(lib.moe_route_backward(
+        _opt(logits, "logits", (d_logits.dtype,), (S, T, E)), _LOGIT_TYPES.get(d_logits.dtype, -1),
+        S, T, E, k, _opt(topk_ids, "topk_ids", _I32, (S, T, k)),
+        _opt(topk_w, "topk_w", _F32, (S, T, k)), _opt(d_topk_w, "d_topk_w", _F32, (S, T, k)),
+        _opt(lse, "lse", _F32, (S, T)), _opt(counts, "counts", _I32, (S, E)),
+        _opt(n_valid, "n_valid", _I32, (S,)), _opt(d_losses, "d_losses", _F32, (2,)),
+        _opt(token_mask, "token_mask", _U8, (S, T)),
+        _arr(d_logits, "d_logits", _LOGIT_TYPES, None), _opt(dev_status, "dev_status", _I32, None),
+        _stream(stream)))
+
+
+def moe_combine_backward(d_out, y, pair_row, topk_w, d_y, d_topk_w, recv_pair=None,
+                         dev_status=None, stream=None):
+    """Gradient of moe_combine: d_out bf16 [S,T,H], y bf16 [y_rows,H] -> d_y bf16 [y_rows,H],
+    d_topk_w f32 [S,T,k]; rows with recv_pair i32 [y_rows] < 0 are set to zero."""
+    lib = load_library()
+    S, T, H = d_out.shape
+    rows, k = y.shape[0], pair_row.shape[-1]
+    _check(lib.moe_combine_backward(
+        _arr(d_out, "d_out", _BF16_TYPES, None), _arr(y, "y", _BF16_TYPES, (rows, H)), rows,
+        _arr(pair_row, "pair_row", _I32, (S, T, k)), _arr(topk_w, "topk_w", _F32, (S, T, k)),
+        _opt(recv_pair, "recv_pair", _I32, (rows,)), S, T, k, H,
+        _arr(d_y, "d_y", _BF16_TYPES, (rows, H)), _arr(d_topk_w, "d_topk_w", _F32, (S, T, k)),
+        _opt(dev_status, "dev_status", _I32, None), _stream(stream)))
 
 
 class MoePath:

@@ -912,4 +912,102 @@ moe_status_t moe_expert_scale_nvfp4(const uint8_t *recv_q, const int32_t *expert
                        __func__);
 }
 
+size_t moe_balance_loss_workspace_bytes(int S, int T, int E)
+{
+    if (check_sizes("moe_balance_loss_workspace_bytes", S, T, 1, E, 1) != MOE_OK) return 0;
+    return balance_loss_ws_bytes(S, T, E);
+}
+
+moe_status_t moe_balance_loss(const void *logits, int logits_type, int S, int T, int E, int k,
+                              const int32_t *topk_ids, const uint8_t *token_mask, int32_t *counts,
+                              float *prob_mean, float *lse, int32_t *n_valid, float *losses,
+                              void *ws, size_t ws_bytes, uint32_t *dev_status, cudaStream_t stream)
+{
+    MOE_CALL_RANGE();
+    moe_status_t st = check_sizes(__func__, S, T, k, E, 1);
+    if (st != MOE_OK) return st;
+    REQUIRE(logits_type == MOE_TYPE_F32 || logits_type == MOE_TYPE_BF16,
+            "%s: logits_type=%d is neither MOE_TYPE_F32 nor MOE_TYPE_BF16", __func__, logits_type);
+    REQUIRE(S <= 65535, "%s: S=%d must be <= 65535", __func__, S);
+    const int64_t NT = (int64_t)S * T;
+    REQUIRE_ARR(logits, NT * E, logits_type == MOE_TYPE_F32 ? 4 : 2);
+    REQUIRE_ARR(topk_ids, NT * k, 4);
+    REQUIRE_ARR(counts, (int64_t)S * E, 4);
+    REQUIRE_ARR(prob_mean, (int64_t)S * E, 4);
+    REQUIRE_ARR(lse, NT, 4);
+    REQUIRE_ARR(n_valid, S, 4);
+    REQUIRE_ARR(losses, 2, 4);
+    REQUIRE_STATUS(dev_status);
+    const size_t need = balance_loss_ws_bytes(S, T, E);
+    REQUIRE_ARR(ws, need, 256);
+    REQUIRE(ws_bytes >= need, "%s: ws_bytes=%zu < required %zu", __func__, ws_bytes, need);
+    return cuda_status(launch_balance_loss(logits, logits_type, topk_ids, token_mask, S, T, E, k,
+                                           counts, prob_mean, lse, n_valid, losses, ws, dev_status,
+                                           stream),
+                       __func__);
+}
+
+moe_status_t moe_route_backward(const void *logits, int logits_type, int S, int T, int E, int k,
+                                const int32_t *topk_ids, const float *topk_w,
+                                const float *d_topk_w, const float *lse, const int32_t *counts,
+                                const int32_t *n_valid, const float *d_losses,
+                                const uint8_t *token_mask, void *d_logits, uint32_t *dev_status,
+                                cudaStream_t stream)
+{
+    MOE_CALL_RANGE();
+    moe_status_t st = check_sizes(__func__, S, T, k, E, 1);
+    if (st != MOE_OK) return st;
+    REQUIRE(logits_type == MOE_TYPE_F32 || logits_type == MOE_TYPE_BF16,
+            "%s: logits_type=%d is neither MOE_TYPE_F32 nor MOE_TYPE_BF16", __func__, logits_type);
+    const int64_t NT = (int64_t)S * T;
+    REQUIRE(NT == 0 || (topk_w != nullptr) == (d_topk_w != nullptr),
+            "%s: `topk_w` and `d_topk_w` come together or not at all", __func__);
+    REQUIRE(NT == 0 || topk_w || d_losses, "%s: no gradient comes in: `d_topk_w` and `d_losses` are null",
+            __func__);
+    const int width = logits_type == MOE_TYPE_F32 ? 4 : 2;
+    if (topk_w) {
+        REQUIRE_ARR(topk_ids, NT * k, 4);
+        REQUIRE_ARR(topk_w, NT * k, 4);
+        REQUIRE_ARR(d_topk_w, NT * k, 4);
+    }
+    if (d_losses) {
+        REQUIRE_ARR(logits, NT * E, width);
+        REQUIRE_ARR(lse, NT, 4);
+        REQUIRE_ARR(counts, (int64_t)S * E, 4);
+        REQUIRE_ARR(n_valid, S, 4);
+        REQUIRE_ARR(d_losses, 2, 4);
+    }
+    REQUIRE_ARR(d_logits, NT * E, width);
+    REQUIRE_STATUS(dev_status);
+    return cuda_status(launch_route_backward(logits, logits_type, topk_ids, topk_w, d_topk_w, lse,
+                                             counts, n_valid, d_losses, token_mask, S, T, E, k,
+                                             d_logits, dev_status, stream),
+                       __func__);
+}
+
+moe_status_t moe_combine_backward(const uint16_t *d_out, const uint16_t *y, int y_rows,
+                                  const int32_t *pair_row, const float *topk_w,
+                                  const int32_t *recv_pair, int S, int T, int k, int H,
+                                  uint16_t *d_y, float *d_topk_w, uint32_t *dev_status,
+                                  cudaStream_t stream)
+{
+    MOE_CALL_RANGE();
+    moe_status_t st = check_sizes(__func__, S, T, k, k, 1);
+    if (st != MOE_OK) return st;
+    REQUIRE(H >= 8 && H % 8 == 0, "%s: H=%d must be a positive multiple of 8", __func__, H);
+    REQUIRE(y_rows >= 0, "%s: y_rows=%d must be >= 0", __func__, y_rows);
+    const int64_t NT = (int64_t)S * T;
+    REQUIRE_ARR(d_out, NT * H, 16);
+    REQUIRE_ARR(y, (int64_t)y_rows * H, 16);
+    REQUIRE_ARR(pair_row, NT * k, 4);
+    REQUIRE_ARR(topk_w, NT * k, 4);
+    REQUIRE(aligned(recv_pair, 4), "%s: `recv_pair` is not 4-byte aligned", __func__);
+    REQUIRE_ARR(d_y, (int64_t)y_rows * H, 16);
+    REQUIRE_ARR(d_topk_w, NT * k, 4);
+    REQUIRE_STATUS(dev_status);
+    return cuda_status(launch_combine_backward(d_out, y, y_rows, pair_row, topk_w, recv_pair, NT, k,
+                                               H, d_y, d_topk_w, dev_status, stream),
+                       __func__);
+}
+
 }  // extern "C"

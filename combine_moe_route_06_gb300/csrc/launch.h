@@ -202,4 +202,21 @@ cudaError_t launch_expert_scale(const uint16_t *recv, const int32_t *expert_offs
                                 const float *scale, int E, int H, int cap_recv, uint16_t *y,
                                 cudaStream_t st);
 
+// Training side of the router and the combine (router_loss.cu, combine_backward.cu).
+size_t balance_loss_ws_bytes(int S, int T, int E);
+cudaError_t launch_balance_loss(const void *logits, int type, const int32_t *ids,
+                                const uint8_t *mask, int S, int T, int E, int k, int32_t *counts,
+                                float *prob_mean, float *lse, int32_t *n_valid, float *losses,
+                                void *ws, uint32_t *dev_status, cudaStream_t st);
+cudaError_t launch_route_backward(const void *logits, int type, const int32_t *ids, const float *w,
+                                  const float *dw, const float *lse, const int32_t *counts,
+                                  const int32_t *n_valid, const float *d_losses,
+                                  const uint8_t *mask, int S, int T, int E, int k, void *d_logits,
+                                  uint32_t *dev_status, cudaStream_t st);
+cudaError_t launch_combine_backward(const uint16_t *d_out, const uint16_t *y, int y_rows,
+                                    const int32_t *pair_row, const float *w,
+                                    const int32_t *recv_pair, int64_t N, int k, int H,
+                                    uint16_t *d_y, float *d_w, uint32_t *dev_status,
+                                    cudaStream_t st);
+
 }  // namespace moe

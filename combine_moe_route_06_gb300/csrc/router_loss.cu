@@ -1,0 +1,455 @@
+// router_loss.cu -- the router's training side: balance and z loss with
+// per-expert counts, and the gradient of both and of the routing weights.
+//
+// For source s with valid tokens V (n = |V|), p_t = softmax(l_t), lse_t =
+// log sum exp l_t:
+//   c_e = picks of expert e by tokens of V,  P_e = (1/n) sum_{t in V} p_te
+//   balance = (1/S) sum_s E/(k n) sum_e c_e P_e,  z = (1/S) sum_s (1/n) sum_t lse_t^2
+// and, with d0, d1 the losses' gradients, A_e = d0 E/(k S n^2) c_e, g_j the
+// gradient of routing weight j (softmax over the chosen logits):
+//   dl_te = p_te (A_e - sum_i A_i p_ti + 2 d1 lse_t / (S n))
+//           + [e = id_j] w_j (g_j - sum_i w_i g_i)
+// The picks are constants of the gradient (a count has none).
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "launch.h"
+#include "trace.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kRlThreads = 256;
+constexpr int kRlWarps = kRlThreads / 32;
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void store_as(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_as(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int off = 16; off; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
+    return v;
+}
+
+// Workspace of one call: per source and CTA the sums of the probabilities, the
+// pick counts, the sum of lse^2 and the number of valid tokens.
+struct LossWs {
+    float *prob;      // [S][B][E]
+    int32_t *picks;   // [S][B][E]
+    float *z;         // [S][B]
+    int32_t *valid;   // [S][B]
+};
+
+// CTAs per source: at least 16 rows each, and about two per SM over all sources.
+int loss_ctas(int S, int T)
+{
+    const int by_rows = (T + 15) / 16;
+    const int by_grid = S >= 304 ? 1 : 304 / S;
+    const int b = by_rows < by_grid ? by_rows : by_grid;
+    return b < 1 ? 1 : b;
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+LossWs carve(void *ws, int S, int B, int E)
+{
+    char *p = (char *)ws;
+    LossWs w;
+    w.prob = (float *)p;
+    p += align256((size_t)S * B * E * 4);
+    w.picks = (int32_t *)p;
+    p += align256((size_t)S * B * E * 4);
+    w.z = (float *)p;
+    p += align256((size_t)S * B * 4);
+    w.valid = (int32_t *)p;
+    return w;
+}
+
+// One warp per token: the row in registers, its softmax added to the lane's
+// column sums; the CTA's sums go to the workspace.
+template <typename L, int VPL>
+__global__ void __launch_bounds__(kRlThreads) k_balance_part(
+    const L *__restrict__ logits, const int32_t *__restrict__ ids,
+    const uint8_t *__restrict__ mask, int T, int E, int k, float *__restrict__ lse, LossWs ws,
+    uint32_t *dev_status)
+{
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ float sm[];              // [warps][E] sums, then [E] picks
+    int32_t *picks = (int32_t *)(sm + kRlWarps * E);
+    __shared__ float zsum[kRlWarps];
+    __shared__ int nsum[kRlWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int s = blockIdx.y, b = blockIdx.x, B = gridDim.x;
+    for (int e = threadIdx.x; e < E; e += kRlThreads) picks[e] = 0;
+    __syncthreads();
+
+    float acc[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; i++) acc[i] = 0.f;
+    float z = 0.f;
+    int n = 0;
+    bool bad_id = false;
+    for (int t = b * kRlWarps + warp; t < T; t += B * kRlWarps) {
+        const int64_t row = (int64_t)s * T + t;
+        if (mask && mask[row] == 0) {
+            if (lane == 0) lse[row] = 0.f;
+            continue;
+        }
+        n++;
+        if (lane < k) {
+            const int id = __ldg(ids + row * k + lane);
+            if (id >= E) bad_id = true;
+            else if (id >= 0) atomicAdd(&picks[id], 1);
+        }
+        const L *src = logits + row * E;
+        float v[VPL];
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < VPL; i++) {
+            const int e = lane + 32 * i;
+            v[i] = e < E ? to_float(src[e]) : -INFINITY;
+            top = fmaxf(top, v[i]);
+        }
+        top = warp_max(top);
+        const float base = top == -INFINITY ? 0.f : top;   // a row of -inf: all terms 0
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPL; i++) {
+            v[i] = expf(v[i] - base);
+            sum += v[i];
+        }
+        sum = warp_sum(sum);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int i = 0; i < VPL; i++) acc[i] = fmaf(v[i], inv, acc[i]);
+        const float l = base + logf(sum);
+        if (sum != 0.f) z = fmaf(l, l, z);
+        if (lane == 0) lse[row] = l;
+    }
+    if (bad_id) flag_status(dev_status, MOE_ERR_BAD_EXPERT_ID);
+#pragma unroll
+    for (int i = 0; i < VPL; i++) {
+        const int e = lane + 32 * i;
+        if (e < E) sm[warp * E + e] = acc[i];
+    }
+    if (lane == 0) {
+        zsum[warp] = z;
+        nsum[warp] = n;
+    }
+    __syncthreads();
+    const int64_t at = (int64_t)s * B + b;
+    for (int e = threadIdx.x; e < E; e += kRlThreads) {
+        float p = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRlWarps; w++) p += sm[w * E + e];
+        ws.prob[at * E + e] = p;
+        ws.picks[at * E + e] = picks[e];
+    }
+    if (threadIdx.x == 0) {
+        float zt = 0.f;
+        int nt = 0;
+        for (int w = 0; w < kRlWarps; w++) {
+            zt += zsum[w];
+            nt += nsum[w];
+        }
+        ws.z[at] = zt;
+        ws.valid[at] = nt;
+    }
+}
+
+// Sums the CTAs' parts in their order, source after source.
+__global__ void __launch_bounds__(1024) k_balance_finish(LossWs ws, int S, int B, int E, int k,
+                                                         int32_t *__restrict__ counts,
+                                                         float *__restrict__ prob_mean,
+                                                         int32_t *__restrict__ n_valid,
+                                                         float *__restrict__ losses)
+{
+    pdl_wait();
+    pdl_trigger();
+    __shared__ float part[32];
+    __shared__ int n_sh;
+    __shared__ float z_sh;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float balance = 0.f, z = 0.f;   // thread 0's
+    for (int s = 0; s < S; s++) {
+        if (warp == 0) {
+            int n = 0;
+            float zs = 0.f;
+            for (int b = lane; b < B; b += 32) {
+                n += ws.valid[(int64_t)s * B + b];
+                zs += ws.z[(int64_t)s * B + b];
+            }
+            n = __reduce_add_sync(kFull, n);
+            zs = warp_sum(zs);
+            if (lane == 0) {
+                n_sh = n;
+                z_sh = zs;
+            }
+        }
+        __syncthreads();
+        const int n = n_sh;
+        const float inv = n > 0 ? 1.f / (float)n : 0.f;
+        float dot = 0.f;
+        for (int e = threadIdx.x; e < E; e += 1024) {
+            float p = 0.f;
+            int c = 0;
+            for (int b = 0; b < B; b++) {
+                p += ws.prob[((int64_t)s * B + b) * E + e];
+                c += ws.picks[((int64_t)s * B + b) * E + e];
+            }
+            p *= inv;
+            counts[(int64_t)s * E + e] = c;
+            prob_mean[(int64_t)s * E + e] = p;
+            dot = fmaf((float)c, p, dot);
+        }
+        dot = warp_sum(dot);
+        if (lane == 0) part[warp] = dot;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            float d = 0.f;
+            for (int w = 0; w < 32; w++) d += part[w];
+            balance += d * inv * ((float)E / (float)k);
+            z += z_sh * inv;
+            n_valid[s] = n;
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        losses[0] = balance / (float)S;
+        losses[1] = z / (float)S;
+    }
+}
+
+// One warp per token.  With LOSS the dense part is computed from the logits and
+// the saved lse, else it is zero; the chosen experts' entries are then stored
+// once more with the routing weights' part added (a warp barrier orders the
+// two stores of an element).
+template <typename L, int VPL, bool LOSS>
+__global__ void __launch_bounds__(kRlThreads) k_route_backward(
+    const L *__restrict__ logits, const int32_t *__restrict__ ids, const float *__restrict__ w,
+    const float *__restrict__ dw, const float *__restrict__ lse, const int32_t *__restrict__ counts,
+    const int32_t *__restrict__ n_valid, const float *__restrict__ d_losses,
+    const uint8_t *__restrict__ mask, int S, int T, int E, int k, L *__restrict__ out,
+    uint32_t *dev_status)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t N = (int64_t)S * T;
+    const int64_t stride = (int64_t)gridDim.x * kRlWarps;
+    bool bad_id = false;
+    for (int64_t row = (int64_t)blockIdx.x * kRlWarps + (threadIdx.x >> 5); row < N;
+         row += stride) {
+        L *dst = out + row * E;
+        if (mask && mask[row] == 0) {
+#pragma unroll
+            for (int i = 0; i < VPL; i++) {
+                const int e = lane + 32 * i;
+                if (e < E) store_as(dst + e, 0.f);
+            }
+            continue;
+        }
+        const int s = (int)(row / T);
+        int id = -1;
+        float g = 0.f;
+        if (w) {
+            float wj = 0.f, gj = 0.f;
+            if (lane < k) {
+                id = __ldg(ids + row * k + lane);
+                wj = __ldg(w + row * k + lane);
+                gj = __ldg(dw + row * k + lane);
+                if (id >= E) bad_id = true;
+                if (id < 0 || id >= E) {
+                    id = -1;
+                    wj = 0.f;
+                    gj = 0.f;
+                }
+            }
+            const float dot = warp_sum(wj * gj);
+            g = wj * (gj - dot);
+        }
+        if constexpr (LOSS) {
+            const float n = fmaxf((float)__ldg(n_valid + s), 1.f);
+            const float per = 1.f / ((float)S * n);
+            const float lead = __ldg(d_losses) * ((float)E / (float)k) * per / n;
+            const float l = __ldg(lse + row);
+            const bool empty = l == -INFINITY;     // a row of -inf has no gradient
+            const float zc = empty ? 0.f : 2.f * __ldg(d_losses + 1) * per * l;
+            const L *src = logits + row * E;
+            const int32_t *c = counts + (int64_t)s * E;
+            // the softmax again from the row: exp(l - lse) would carry the rounding of lse
+            float p[VPL], a[VPL];
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < VPL; i++) {
+                const int e = lane + 32 * i;
+                p[i] = e < E ? to_float(src[e]) : -INFINITY;
+                a[i] = e < E ? lead * (float)__ldg(c + e) : 0.f;
+                top = fmaxf(top, p[i]);
+            }
+            top = warp_max(top);
+            const float base = top == -INFINITY ? 0.f : top;
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < VPL; i++) {
+                p[i] = expf(p[i] - base);
+                sum += p[i];
+            }
+            sum = warp_sum(sum);
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            float dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < VPL; i++) {
+                p[i] *= inv;
+                dot = fmaf(a[i], p[i], dot);
+            }
+            const float back = zc - warp_sum(dot);
+            float chosen = 0.f;
+            if (id >= 0) {
+                const float q = expf(to_float(src[id]) - base) * inv;
+                chosen = q * (lead * (float)__ldg(c + id) + back);
+            }
+#pragma unroll
+            for (int i = 0; i < VPL; i++) {
+                const int e = lane + 32 * i;
+                if (e < E) store_as(dst + e, p[i] * (a[i] + back));
+            }
+            if (w) {
+                for (int j = 0; j < k; j++) {      // picks of the same expert add up
+                    const int ij = __shfl_sync(kFull, id, j);
+                    const float gj = __shfl_sync(kFull, g, j);
+                    if (ij == id) chosen += gj;
+                }
+                __syncwarp();
+                if (id >= 0) store_as(dst + id, chosen);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; i++) {
+                const int e = lane + 32 * i;
+                if (e < E) store_as(dst + e, 0.f);
+            }
+            if (w) {
+                float chosen = 0.f;
+                for (int j = 0; j < k; j++) {
+                    const int ij = __shfl_sync(kFull, id, j);
+                    const float gj = __shfl_sync(kFull, g, j);
+                    if (ij == id) chosen += gj;
+                }
+                __syncwarp();
+                if (id >= 0) store_as(dst + id, chosen);
+            }
+        }
+    }
+    if (bad_id) flag_status(dev_status, MOE_ERR_BAD_EXPERT_ID);
+}
+
+// VPL: logits per lane, the smallest instance that holds E.
+#define MOE_VPL_CASES(E, CALL)          \
+    do {                                \
+        const int vpl_ = ((E) + 31) / 32; \
+        if (vpl_ <= 1) { CALL(1); }     \
+        else if (vpl_ <= 2) { CALL(2); } \
+        else if (vpl_ <= 4) { CALL(4); } \
+        else if (vpl_ <= 8) { CALL(8); } \
+        else if (vpl_ <= 12) { CALL(12); } \
+        else if (vpl_ <= 16) { CALL(16); } \
+        else if (vpl_ <= 24) { CALL(24); } \
+        else { CALL(32); }              \
+    } while (0)
+
+template <typename L>
+cudaError_t balance_part(const L *logits, const int32_t *ids, const uint8_t *mask, int S, int T,
+                         int E, int k, int B, float *lse, LossWs ws, uint32_t *dev_status,
+                         cudaStream_t st)
+{
+    const size_t smem = (size_t)(kRlWarps + 1) * E * 4;
+    cudaError_t err = cudaSuccess;
+#define CALL(V)                                                                               \
+    MOE_TRACED_LAUNCH("k_balance_part", st,                                                   \
+        err = launch_pdl(k_balance_part<L, V>, dim3(B, S), dim3(kRlThreads), smem, st, logits, \
+                         ids, mask, T, E, k, lse, ws, dev_status))
+    MOE_VPL_CASES(E, CALL);
+#undef CALL
+    return err;
+}
+
+template <typename L>
+cudaError_t route_backward(const L *logits, const int32_t *ids, const float *w, const float *dw,
+                           const float *lse, const int32_t *counts, const int32_t *n_valid,
+                           const float *d_losses, const uint8_t *mask, int S, int T, int E, int k,
+                           L *out, uint32_t *dev_status, cudaStream_t st)
+{
+    const int64_t N = (int64_t)S * T;
+    const int64_t want = (N + kRlWarps - 1) / kRlWarps;
+    cudaError_t err = cudaSuccess;
+#define CALL2(V, LOSS)                                                                          \
+    do {                                                                                        \
+        const int64_t fit = resident_grid((const void *)k_route_backward<L, V, LOSS>, kRlThreads, 0); \
+        const int64_t grid = fit > 0 && want > fit ? fit : want;                                \
+        MOE_TRACED_LAUNCH("k_route_backward", st,                                               \
+            err = launch_pdl(k_route_backward<L, V, LOSS>, dim3((unsigned)grid), dim3(kRlThreads), \
+                             0, st, logits, ids, w, dw, lse, counts, n_valid, d_losses, mask, S, T, \
+                             E, k, out, dev_status));                                           \
+    } while (0)
+#define CALL(V) if (d_losses) CALL2(V, true); else CALL2(V, false)
+    MOE_VPL_CASES(E, CALL);
+#undef CALL
+#undef CALL2
+    return err;
+}
+
+}  // namespace
+
+size_t balance_loss_ws_bytes(int S, int T, int E)
+{
+    const int B = loss_ctas(S, T);
+    return 2 * align256((size_t)S * B * E * 4) + 2 * align256((size_t)S * B * 4);
+}
+
+cudaError_t launch_balance_loss(const void *logits, int type, const int32_t *ids,
+                                const uint8_t *mask, int S, int T, int E, int k, int32_t *counts,
+                                float *prob_mean, float *lse, int32_t *n_valid, float *losses,
+                                void *ws, uint32_t *dev_status, cudaStream_t st)
+{
+    const int B = loss_ctas(S, T);
+    const LossWs w = carve(ws, S, B, E);
+    cudaError_t err = type == MOE_TYPE_BF16
+                          ? balance_part((const __nv_bfloat16 *)logits, ids, mask, S, T, E, k, B,
+                                         lse, w, dev_status, st)
+                          : balance_part((const float *)logits, ids, mask, S, T, E, k, B, lse, w,
+                                         dev_status, st);
+    if (err != cudaSuccess) return err;
+    MOE_TRACED_LAUNCH("k_balance_finish", st,
+        err = launch_pdl(k_balance_finish, dim3(1), dim3(1024), 0, st, w, S, B, E, k, counts,
+                         prob_mean, n_valid, losses));
+    return err;
+}
+
+cudaError_t launch_route_backward(const void *logits, int type, const int32_t *ids, const float *w,
+                                  const float *dw, const float *lse, const int32_t *counts,
+                                  const int32_t *n_valid, const float *d_losses,
+                                  const uint8_t *mask, int S, int T, int E, int k, void *d_logits,
+                                  uint32_t *dev_status, cudaStream_t st)
+{
+    if ((int64_t)S * T == 0) return cudaSuccess;
+    if (type == MOE_TYPE_BF16)
+        return route_backward((const __nv_bfloat16 *)logits, ids, w, dw, lse, counts, n_valid,
+                              d_losses, mask, S, T, E, k, (__nv_bfloat16 *)d_logits, dev_status, st);
+    return route_backward((const float *)logits, ids, w, dw, lse, counts, n_valid, d_losses, mask,
+                          S, T, E, k, (float *)d_logits, dev_status, st);
+}
+
+}  // namespace moe

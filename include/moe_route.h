@@ -30,6 +30,13 @@
  *   moe_dispatch_layout_mapped      hot ones ("Beyond One GPU", section 6)
  *   moe_dispatch_layout_static      the layout for callers that cannot allocate
  *   moe_expert_scale(_mxfp8/_nvfp4) stand-in experts for tests and benchmarks
+ *
+ * The training direction of the path, declared after the forward calls:
+ *   moe_balance_loss                balance and z loss, per-expert counts
+ *   moe_route_backward              gradient of the routing weights and losses
+ *   moe_combine_backward            gradient of the weighted combine
+ * (the gradient of dispatch is moe_combine with weights of one).
+ *
  *   moe_trace_*                     optional CUDA-event timing of launches
  *   moe_dispatch_layout_kernels,    kernels one call enqueues for given sizes
  *   moe_permute_to_experts_kernels  (for counting launches per step)
@@ -104,6 +111,10 @@ typedef enum {
 /* Row formats of moe_dispatch_quantized. */
 #define MOE_FORMAT_MXFP8 1
 #define MOE_FORMAT_NVFP4 2
+
+/* Element types of the router logits in the training calls. */
+#define MOE_TYPE_F32 0
+#define MOE_TYPE_BF16 1
 
 /* Library version as MAJOR*10000 + MINOR*100 + PATCH. */
 int moe_version(void);
@@ -697,6 +708,82 @@ moe_status_t moe_expert_scale_mxfp8(const uint8_t *recv_q, const int32_t *expert
 moe_status_t moe_expert_scale_nvfp4(const uint8_t *recv_q, const int32_t *expert_offsets,
                                     const float *scale, int E, int H, float global_scale,
                                     int cap_recv, uint16_t *y, cudaStream_t stream);
+
+/*
+ * Balance loss, z loss and per-expert counts of a router, source by source.
+ * A source is what is balanced: S sequences of T tokens balance each sequence
+ * by itself, S = 1 the whole batch.  With V_s the valid tokens of source s,
+ * n_s their number, p = softmax over all E logits, lse = log sum exp:
+ *   counts[s][e]    = #{(t, j) : t in V_s, topk_ids[s][t][j] == e}
+ *   prob_mean[s][e] = (1 / n_s) sum over t in V_s of p[s][t][e]
+ *   losses[0] = (1/S) sum_s E / (k n_s) sum_e counts[s][e] prob_mean[s][e]
+ *   losses[1] = (1/S) sum_s (1 / n_s) sum over t in V_s of lse[s][t]^2
+ * losses[0] is 1 for a router that spreads its picks or its probabilities
+ * evenly.  A source without valid tokens adds 0 to both.  The losses carry no
+ * coefficients: those go into d_losses of moe_route_backward.
+ *   logits     [S][T][E] of logits_type (MOE_TYPE_F32 or MOE_TYPE_BF16).  -inf
+ *              is a probability of 0; a row of -inf alone has lse -inf, counts
+ *              among the valid tokens and adds nothing else.
+ *   topk_ids   [S][T][k] int32; ids < 0 are not counted, ids >= E are skipped
+ *              and flag MOE_ERR_BAD_EXPERT_ID.
+ *   token_mask [S][T] uint8 or NULL: tokens with 0 are not valid.  Nothing of
+ *              theirs is read (their logits may hold anything), lse is 0.
+ *   counts, prob_mean [S][E]; lse [S][T] float32; n_valid [S] int32;
+ *   losses [2] float32, all out, kept for moe_route_backward.
+ *   ws         moe_balance_loss_workspace_bytes(S, T, E) bytes, 256-byte aligned.
+ * Sums are in fp32 in a fixed order.  S <= 65535.
+ */
+size_t moe_balance_loss_workspace_bytes(int S, int T, int E);
+moe_status_t moe_balance_loss(const void *logits, int logits_type, int S, int T, int E, int k,
+                              const int32_t *topk_ids, const uint8_t *token_mask, int32_t *counts,
+                              float *prob_mean, float *lse, int32_t *n_valid, float *losses,
+                              void *ws, size_t ws_bytes, uint32_t *dev_status,
+                              cudaStream_t stream);
+
+/*
+ * Gradient in the router logits of the routing weights (moe_route_topk's
+ * softmax over the chosen logits) and of both losses, in one pass:
+ *   d_logits[s][t][e] = p_e (A_e - sum_i A_i p_i) + (2 d_losses[1] / (S n_s)) lse p_e
+ *                       + sum over j with topk_ids == e of w_j (g_j - sum_i w_i g_i)
+ * with A_e = d_losses[0] E counts[s][e] / (k S n_s^2), w = topk_w, g = d_topk_w;
+ * the picks are constants.  Computed in fp32, rounded once to logits_type.
+ *   topk_w, d_topk_w [S][T][k] float32, both or neither (NULL: no gradient
+ *              comes through the weights; topk_ids may then be NULL).
+ *   d_losses   [2] float32 or NULL (no gradient comes through the losses; logits,
+ *              lse, counts and n_valid may then be NULL).
+ *   lse, counts, n_valid  as moe_balance_loss wrote them, for the same token_mask.
+ *   token_mask as there; tokens with 0 get a zero row, nothing of theirs is read.
+ *   d_logits   [S][T][E] of logits_type out, apart from the inputs.
+ *   ids < 0 carry no gradient; ids >= E neither, and flag MOE_ERR_BAD_EXPERT_ID.
+ */
+moe_status_t moe_route_backward(const void *logits, int logits_type, int S, int T, int E, int k,
+                                const int32_t *topk_ids, const float *topk_w,
+                                const float *d_topk_w, const float *lse, const int32_t *counts,
+                                const int32_t *n_valid, const float *d_losses,
+                                const uint8_t *token_mask, void *d_logits, uint32_t *dev_status,
+                                cudaStream_t stream);
+
+/*
+ * Gradient of moe_combine in the expert rows and in the routing weights: for
+ * every pair with 0 <= pair_row < y_rows
+ *   d_y[row]          = bf16_rne(topk_w[s][t][j] * float(d_out[s][t]))
+ *   d_topk_w[s][t][j] = sum over h of float(y[row][h]) * float(d_out[s][t][h]), fp32
+ * and d_topk_w = 0 for every other pair (pair_row >= y_rows also flags
+ * MOE_ERR_INVALID_ARG).  No two pairs share a row (moe_permute_to_experts and
+ * the masked layout give every pair its own).
+ *   d_out, y   [S][T][H], [y_rows][H] bf16 in; pair_row, topk_w as moe_combine.
+ *   recv_pair  [y_rows] int32 or NULL: rows of d_y with recv_pair < 0 (padding)
+ *              are set to zero; with NULL they are not written.
+ *   d_y        [y_rows][H] bf16 out, apart from the inputs; d_topk_w [S][T][k] out.
+ * With one receiving partition this is that partition's part; the d_topk_w of
+ * all partitions add up.  The gradient of dispatch (one row copied to several)
+ * is moe_combine of the rows' gradients with weights of one.
+ */
+moe_status_t moe_combine_backward(const uint16_t *d_out, const uint16_t *y, int y_rows,
+                                  const int32_t *pair_row, const float *topk_w,
+                                  const int32_t *recv_pair, int S, int T, int k, int H,
+                                  uint16_t *d_y, float *d_topk_w, uint32_t *dev_status,
+                                  cudaStream_t stream);
 
 /*
  * Per-kernel timing (tracing aid; off by default).  While enabled, every
