@@ -39,7 +39,8 @@ __all__ = [
     "moe_dispatch_pack_routed", "moe_routed_expert_stage1", "moe_dispatch_pack_nvfp4",
     "moe_expert_scale_nvfp4", "nvfp4_record_bytes", "mxfp8_record_bytes", "HostPipeline",
     "MOE_TYPE_F32", "MOE_TYPE_BF16", "moe_balance_loss", "moe_balance_loss_workspace_bytes",
-    "moe_route_backward", "moe_combine_backward",
+    "moe_route_backward", "moe_combine_backward", "moe_w4_bytes", "moe_w4_pack",
+    "moe_expert_product_w4", "moe_expert_product_w4_workspace_bytes",
     "MoePath", "trace_enable", "trace_disable", "trace_reset", "trace_records",
 ]
 
@@ -157,6 +158,11 @@ def load_library() -> ctypes.CDLL:
                                    ctypes.c_int),
             "moe_combine_backward": ([P, P, i32, P, P, P, i32, i32, i32, i32, P, P, P, P],
                                      ctypes.c_int),
+            "moe_w4_bytes": ([i32, i32, i32, i32], sz),
+            "moe_w4_pack": ([P, P, i32, i32, i32, i32, P, sz, P], ctypes.c_int),
+            "moe_expert_product_w4_workspace_bytes": ([i32, i32, i32, i32], sz),
+            "moe_expert_product_w4": ([P, i32, P, P, i32, P, P, i32, i32, i32, i32, P, P, sz, P, P],
+                                      ctypes.c_int),
             "moe_trace_enable": ([ctypes.c_char_p, i32], ctypes.c_int),
             "moe_trace_disable": ([], None),
             "moe_trace_reset": ([], None),
@@ -794,6 +800,49 @@ def moe_combine_backward(d_out, y, pair_row, topk_w, d_y, d_topk_w, recv_pair=No
         _arr(pair_row, "pair_row", _I32, (S, T, k)), _arr(topk_w, "topk_w", _F32, (S, T, k)),
         _opt(recv_pair, "recv_pair", _I32, (rows,)), S, T, k, H,
         _arr(d_y, "d_y", _BF16_TYPES, (rows, H)), _arr(d_topk_w, "d_topk_w", _F32, (S, T, k)),
+        _opt(dev_status, "dev_status", _I32, None), _stream(stream)))
+
+
+def moe_w4_bytes(E: int, N: int, K: int, gated: bool = False) -> int:
+    """Bytes of E experts' packed 4-bit weights with N outputs over K columns."""
+    n = int(load_library().moe_w4_bytes(E, N, K, int(gated)))
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, load_library().moe_last_error_message().decode())
+    return n
+
+
+def moe_w4_pack(codes, scales, w4, gated=False, stream=None):
+    """codes uint8 [E,rows,K/2] (E2M1, first value in the low nibble), scales uint8 [E,rows,K/16]
+    (E4M3), rows = N or for gated weights 2N (gate, then up) -> w4 uint8 [moe_w4_bytes]."""
+    lib = load_library()
+    E, rows, half = codes.shape
+    if gated and rows % 2:
+        raise ValueError(f"codes: gated weights have an even number of rows, got {rows}")
+    N, K = rows // 2 if gated else rows, 2 * half
+    _check(lib.moe_w4_pack(_arr(codes, "codes", _U8, None),
+                           _arr(scales, "scales", _U8, (E, rows, K // 16)), E, N, K, int(gated),
+                           _arr(w4, "w4", _U8, None), w4.numel(), _stream(stream)))
+
+
+def moe_expert_product_w4_workspace_bytes(a_rows: int, E: int, N: int, K: int) -> int:
+    return int(load_library().moe_expert_product_w4_workspace_bytes(a_rows, E, N, K))
+
+
+def moe_expert_product_w4(a, w4, w_factor, y, ws, expert_offsets=None, masked_counts=None,
+                          block_rows=0, gated=False, dev_status=None, stream=None):
+    """a bf16 [rows,K] times every expert's packed 4-bit weights -> y bf16 [rows,N]; the experts'
+    rows by expert_offsets i32 [E+1] or by masked_counts i32 [E] with block_rows; w_factor f32 [E]."""
+    lib = load_library()
+    rows, K = a.shape
+    N, E = y.shape[-1], w_factor.shape[0]
+    if w4.numel() < moe_w4_bytes(E, N, K, gated):
+        raise ValueError(f"w4: {w4.numel()} bytes are not the packed weights of E={E}, N={N}, K={K}, "
+                         f"gated={gated}")
+    _check(lib.moe_expert_product_w4(
+        _arr(a, "a", _BF16_TYPES, None), rows, _opt(expert_offsets, "expert_offsets", _I32, (E + 1,)),
+        _opt(masked_counts, "masked_counts", _I32, (E,)), block_rows, _arr(w4, "w4", _U8, None),
+        _arr(w_factor, "w_factor", _F32, (E,)), E, N, K, int(gated),
+        _arr(y, "y", _BF16_TYPES, (rows, N)), _arr(ws, "ws", _U8, None), ws.numel(),
         _opt(dev_status, "dev_status", _I32, None), _stream(stream)))
 
 

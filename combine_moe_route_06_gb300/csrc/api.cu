@@ -12,6 +12,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "w4.cuh"
 
 namespace {
 // One NVTX range per library call (host side: argument checks and enqueue), so a
@@ -1007,6 +1008,83 @@ moe_status_t moe_combine_backward(const uint16_t *d_out, const uint16_t *y, int 
     REQUIRE_STATUS(dev_status);
     return cuda_status(launch_combine_backward(d_out, y, y_rows, pair_row, topk_w, recv_pair, NT, k,
                                                H, d_y, d_topk_w, dev_status, stream),
+                       __func__);
+}
+
+static moe_status_t check_w4(const char *fn, int E, int N, int K, int gated)
+{
+    REQUIRE(E >= 1 && E <= kMaxE, "%s: E=%d must be in [1, %d]", fn, E, kMaxE);
+    REQUIRE(N >= 8 && N % 8 == 0 && N <= (1 << 20), "%s: N=%d must be a multiple of 8 in [8, 2^20]",
+            fn, N);
+    REQUIRE(K >= 16 && K % 16 == 0 && K <= (1 << 20),
+            "%s: K=%d must be a multiple of 16 in [16, 2^20]", fn, K);
+    REQUIRE(gated == 0 || gated == 1, "%s: gated=%d must be 0 or 1", fn, gated);
+    REQUIRE((int64_t)E * w4_tiles(N, gated) * w4_chunks(K) < ((int64_t)1 << 31),
+            "%s: E=%d experts of %d x %d weights are too many", fn, E, N, K);
+    return MOE_OK;
+}
+
+size_t moe_w4_bytes(int E, int N, int K, int gated)
+{
+    if (check_w4("moe_w4_bytes", E, N, K, gated) != MOE_OK) return 0;
+    return w4_bytes(E, N, K, gated != 0);
+}
+
+moe_status_t moe_w4_pack(const uint8_t *codes, const uint8_t *scales, int E, int N, int K,
+                         int gated, uint8_t *w4, size_t w4_size, cudaStream_t stream)
+{
+    MOE_CALL_RANGE();
+    moe_status_t st = check_w4(__func__, E, N, K, gated);
+    if (st != MOE_OK) return st;
+    REQUIRE_ARR(codes, 1, 8);
+    REQUIRE_ARR(scales, 1, 1);
+    REQUIRE_ARR(w4, 1, 16);
+    const size_t need = w4_bytes(E, N, K, gated != 0);
+    REQUIRE(w4_size >= need, "%s: w4_size=%zu < required %zu", __func__, w4_size, need);
+    return cuda_status(launch_w4_pack(codes, scales, E, N, K, gated != 0, w4, stream), __func__);
+}
+
+size_t moe_expert_product_w4_workspace_bytes(int a_rows, int E, int N, int K)
+{
+    if (check_w4("moe_expert_product_w4_workspace_bytes", E, N, K, 0) != MOE_OK) return 0;
+    if (a_rows < 0) {
+        fail(MOE_ERR_INVALID_ARG, "moe_expert_product_w4_workspace_bytes: a_rows=%d must be >= 0",
+             a_rows);
+        return 0;
+    }
+    return expert_w4_ws_bytes(a_rows, E, N, K);
+}
+
+moe_status_t moe_expert_product_w4(const uint16_t *a, int a_rows, const int32_t *expert_offsets,
+                                   const int32_t *masked_counts, int block_rows,
+                                   const uint8_t *w4, const float *w_factor, int E, int N, int K,
+                                   int gated, uint16_t *y, void *ws, size_t ws_bytes,
+                                   uint32_t *dev_status, cudaStream_t stream)
+{
+    MOE_CALL_RANGE();
+    moe_status_t st = check_w4(__func__, E, N, K, gated);
+    if (st != MOE_OK) return st;
+    REQUIRE(a_rows >= 0, "%s: a_rows=%d must be >= 0", __func__, a_rows);
+    REQUIRE((expert_offsets != nullptr) != (masked_counts != nullptr),
+            "%s: give `expert_offsets` or `masked_counts`, not both", __func__);
+    if (masked_counts) {
+        REQUIRE(block_rows >= 1, "%s: block_rows=%d must be >= 1", __func__, block_rows);
+        REQUIRE((int64_t)E * block_rows <= a_rows, "%s: a_rows=%d < E * block_rows=%lld", __func__,
+                a_rows, (long long)E * block_rows);
+        REQUIRE_ARR(masked_counts, E, 4);
+    } else {
+        REQUIRE_ARR(expert_offsets, E + 1, 4);
+    }
+    REQUIRE_ARR(a, (int64_t)a_rows * K, 16);
+    REQUIRE_ARR(w4, 1, 16);
+    REQUIRE_ARR(w_factor, E, 4);
+    REQUIRE_ARR(y, (int64_t)a_rows * N, 16);
+    REQUIRE_STATUS(dev_status);
+    const size_t need = expert_w4_ws_bytes(a_rows, E, N, K);
+    REQUIRE_ARR(ws, need, 256);
+    REQUIRE(ws_bytes >= need, "%s: ws_bytes=%zu < required %zu", __func__, ws_bytes, need);
+    return cuda_status(launch_expert_w4(a, a_rows, expert_offsets, masked_counts, block_rows, w4,
+                                        w_factor, E, N, K, gated != 0, y, ws, dev_status, stream),
                        __func__);
 }
 

@@ -219,4 +219,14 @@ cudaError_t launch_combine_backward(const uint16_t *d_out, const uint16_t *y, in
                                     uint16_t *d_y, float *d_w, uint32_t *dev_status,
                                     cudaStream_t st);
 
+// The experts' products with 4-bit weights (expert_w4.cu).
+size_t w4_bytes(int E, int N, int K, bool gated);
+cudaError_t launch_w4_pack(const uint8_t *codes, const uint8_t *scales, int E, int N, int K,
+                           bool gated, uint8_t *w4, cudaStream_t st);
+size_t expert_w4_ws_bytes(int a_rows, int E, int N, int K);
+cudaError_t launch_expert_w4(const uint16_t *a, int a_rows, const int32_t *offsets,
+                             const int32_t *counts, int block_rows, const uint8_t *w4,
+                             const float *factor, int E, int N, int K, bool gated, uint16_t *y,
+                             void *ws, uint32_t *dev_status, cudaStream_t st);
+
 }  // namespace moe

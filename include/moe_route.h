@@ -31,6 +31,11 @@
  *   moe_dispatch_layout_static      the layout for callers that cannot allocate
  *   moe_expert_scale(_mxfp8/_nvfp4) stand-in experts for tests and benchmarks
  *
+ * The experts' products of the serving path:
+ *   moe_w4_pack                     4-bit weights into the library's layout, once
+ *   moe_expert_product_w4           rows of every expert times its 4-bit weights,
+ *                                   plain or silu(gate) * up
+ *
  * The training direction of the path, declared after the forward calls:
  *   moe_balance_loss                balance and z loss, per-expert counts
  *   moe_route_backward              gradient of the routing weights and losses
@@ -708,6 +713,51 @@ moe_status_t moe_expert_scale_mxfp8(const uint8_t *recv_q, const int32_t *expert
 moe_status_t moe_expert_scale_nvfp4(const uint8_t *recv_q, const int32_t *expert_offsets,
                                     const float *scale, int E, int H, float global_scale,
                                     int cap_recv, uint16_t *y, cudaStream_t stream);
+
+/*
+ * 4-bit expert weights.  A weight is code * scale * factor: an E2M1 code, the
+ * E4M3 scale of its group of 16 consecutive columns, and one fp32 factor per
+ * expert (NVFP4, the encoding of moe_dispatch_pack_nvfp4 with the factor in the
+ * place of its global_scale).  moe_w4_pack lays the weights of E experts out
+ * for moe_expert_product_w4; a caller does it once, when it loads them.
+ *   codes   [E][rows][K/2] uint8 in, 8-byte aligned, element 2i in the low nibble.
+ *   scales  [E][rows][K/16] uint8 (E4M3) in.
+ *           rows = N, or 2N for gated weights: the N gate rows, then the N up rows.
+ *   w4      moe_w4_bytes(E, N, K, gated) bytes out, 16-byte aligned: 9/16 byte a
+ *           weight, N and K rounded up to the 128 x 128 blocks of the layout
+ *           (64 outputs by 128 columns for gated weights).
+ * N a multiple of 8, K a multiple of 16, 1 <= E <= 1024.
+ */
+size_t moe_w4_bytes(int E, int N, int K, int gated);
+moe_status_t moe_w4_pack(const uint8_t *codes, const uint8_t *scales, int E, int N, int K,
+                         int gated, uint8_t *w4, size_t w4_size, cudaStream_t stream);
+
+/*
+ * The experts' products over the receive layouts.  For every row r of expert e:
+ *   gated 0:  y[r][n] = bf16_rne( sum_k a[r][k] W_e[n][k] ),              n < N
+ *   gated 1:  y[r][n] = bf16_rne( silu(sum_k a[r][k] W_e[n][k])
+ *                                 * sum_k a[r][k] W_e[N + n][k] )
+ * with silu(v) = v / (1 + exp(-v)), sums in fp32 and one rounding at the end.
+ *   a        [a_rows][K] bf16 in, y [a_rows][N] bf16 out, apart from each other.
+ *   expert_offsets  [E+1] int32: expert e's rows are [offsets[e], offsets[e+1])
+ *            (moe_permute_to_experts; for one partition its slice of the E+1
+ *            offsets serves, the weights being that partition's), or
+ *   masked_counts   [E] int32 with block_rows: expert e's rows are the first
+ *            masked_counts[e] of block e (moe_permute_to_experts_masked).
+ *            The other of the two is NULL.
+ *   w4       packed weights of the same E, N, K and gated; w_factor [E] float32.
+ *   ws       moe_expert_product_w4_workspace_bytes(a_rows, E, N, K) bytes,
+ *            256-byte aligned.
+ * Rows of y outside the experts' rows are not written.  Row ranges that leave
+ * [0, a_rows) are cut to it and flag MOE_ERR_INVALID_ARG.  A NaN or infinity in
+ * a row of `a` reaches only that row of y.
+ */
+size_t moe_expert_product_w4_workspace_bytes(int a_rows, int E, int N, int K);
+moe_status_t moe_expert_product_w4(const uint16_t *a, int a_rows, const int32_t *expert_offsets,
+                                   const int32_t *masked_counts, int block_rows,
+                                   const uint8_t *w4, const float *w_factor, int E, int N, int K,
+                                   int gated, uint16_t *y, void *ws, size_t ws_bytes,
+                                   uint32_t *dev_status, cudaStream_t stream);
 
 /*
  * Balance loss, z loss and per-expert counts of a router, source by source.
