@@ -190,13 +190,13 @@ __global__ void __launch_bounds__(kRowsThreads) k_w4_rows(
 
 // ---------------------------------------------------------------- the product
 
-constexpr int kDecodeWarps = 8;                     // decode the weights, then the epilogue
+constexpr int kAStages = 4;                         // decoded blocks in tensor memory
+constexpr int kDecodeWarps = 4 * kAStages;          // decode the weights, then the epilogue
 constexpr int kMmThreads = (kDecodeWarps + 3) * 32; // + weight loads, row loads, MMA
 constexpr int kMaxRowsTile = 128;                   // rows of `a` per tile
 constexpr int kWStages = 11;                        // 9 KiB weight blocks in flight
 constexpr int kXBytes = 96 * 1024;                  // ring of row operands
 constexpr int kXStagesMax = 12;
-constexpr int kAStages = 4;                         // decoded blocks in tensor memory
 constexpr int kAColumns = kW4Chunk / 2;             // 64 columns a block
 constexpr int kTmemColumns = 512;                   // 128 of sums, 4 x 64 of weights
 constexpr int kGroupBytes = kW4Chunk / 64 * 1024;   // an 8-row group's chunk: 2 KiB
@@ -208,7 +208,7 @@ struct MmShared {
     uint64_t sums_full;
     int64_t before[kMaxE + 1];       // row tiles of the experts before e
     int start[kMaxE], count[kMaxE];
-    float up[2][8][kW4Tile / 2];     // gated epilogue: up factors on their way to the gate's warps
+    float up[kAStages][8][kW4Tile / 2];   // gated epilogue: up factors on their way to the gate's warps
     uint32_t tmem;
     int most;                        // largest row tile, in 8-row groups
     int last;                        // this CTA arrived last at a cut tile
@@ -294,14 +294,14 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
         sh.dead = 0;
         for (int i = 0; i < kWStages; i++) {
             mbar_init(&sh.w_full[i], 1);
-            mbar_init(&sh.w_empty[i], kDecodeWarps);
+            mbar_init(&sh.w_empty[i], 4);
         }
         for (int i = 0; i < kXStagesMax; i++) {
             mbar_init(&sh.x_full[i], 1);
             mbar_init(&sh.x_empty[i], 1);
         }
         for (int i = 0; i < kAStages; i++) {
-            mbar_init(&sh.a_full[i], kDecodeWarps);
+            mbar_init(&sh.a_full[i], 4);
             mbar_init(&sh.a_empty[i], 1);
         }
         mbar_init(&sh.sums_full, 1);
@@ -446,58 +446,68 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
             }
         }
     } else {
-        // ---- decode: a warp has 32 rows (its quarter of the tensor-memory lanes) and half of
-        // a block's columns; then the same warps finish the tile
-        const int quarter = warp & 3, half = warp >> 2;
+        // ---- decode: team t of four warps (one per quarter of the tensor-memory lanes, a row
+        // a lane) has every kAStages-th chunk and A stage t; then the same warps finish the tile
+        const int quarter = warp & 3, team = warp >> 2;
         const int row = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        int sw = 0, sa = 0;
+        const uint32_t a_at = tmem + lanes + kMaxRowsTile + team * kAColumns;
+        int sw = team;               // stage of the team's next chunk
         uint32_t pw = 0, pa = 0, psum = 0;
+        uint32_t mine = team, seen = 0;      // that chunk's number; chunks of the past segments
         bool ok = true;
         pdl_wait();
         while (ok && walk.next(g)) {
-            for (int c = g.c0; c < g.c1; c++) {
+            seen += g.c1 - g.c0;
+            for (; mine < seen; mine += kAStages) {
                 if (!(ok = mbar_wait(&sh.w_full[sw], pw, dead))) break;
                 const uint8_t *block = wring + sw * kW4BlockBytes;
-                const uint4 q0 = *(const uint4 *)(block + ((2 * half) * kW4Tile + row) * 16);
-                const uint4 q1 = *(const uint4 *)(block + ((2 * half + 1) * kW4Tile + row) * 16);
-                const uint32_t sc = *(const uint32_t *)(block + kW4CodeBytes + row * 8 + half * 4);
+                uint4 q[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++) q[j] = *(const uint4 *)(block + (j * kW4Tile + row) * 16);
+                const uint2 sc = *(const uint2 *)(block + kW4CodeBytes + row * 8);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.w_empty[sw]);
-                const uint32_t word[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-                const uint32_t s01 = e4m3x2_to_half2(sc), s23 = e4m3x2_to_half2(sc >> 16);
-                const uint32_t group_scale[4] = {__byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232),
-                                                 __byte_perm(s23, 0, 0x1010), __byte_perm(s23, 0, 0x3232)};
-                uint32_t out[32];
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    uint32_t h[4];
-                    e2m1x8_to_half2(word[i], h);
-#pragma unroll
-                    for (int p = 0; p < 4; p++) out[4 * i + p] = mul_half2(h[p], group_scale[i >> 1]);
+                sw += kAStages;
+                if (sw >= kWStages) {
+                    sw -= kWStages;
+                    pw ^= 1;
                 }
-                if (!(ok = mbar_wait(&sh.a_empty[sa], pa ^ 1, dead))) break;
+                if (!(ok = mbar_wait(&sh.a_empty[team], pa ^ 1, dead))) break;
+                pa ^= 1;
                 tmem_fence_after();
-                tmem_store32(tmem + lanes + kMaxRowsTile + sa * kAColumns + half * 32, out);
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const uint32_t s4 = h ? sc.y : sc.x;
+                    const uint32_t s01 = e4m3x2_to_half2(s4), s23 = e4m3x2_to_half2(s4 >> 16);
+                    const uint32_t group_scale[4] = {
+                        __byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232),
+                        __byte_perm(s23, 0, 0x1010), __byte_perm(s23, 0, 0x3232)};
+                    const uint32_t word[8] = {q[2 * h].x,     q[2 * h].y,     q[2 * h].z,
+                                              q[2 * h].w,     q[2 * h + 1].x, q[2 * h + 1].y,
+                                              q[2 * h + 1].z, q[2 * h + 1].w};
+                    uint32_t out[32];
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        uint32_t half2s[4];
+                        e2m1x8_to_half2(word[i], half2s);
+#pragma unroll
+                        for (int p = 0; p < 4; p++)
+                            out[4 * i + p] = mul_half2(half2s[p], group_scale[i >> 1]);
+                    }
+                    tmem_store32(a_at + h * 32, out);
+                }
                 tmem_wait_st();
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.a_full[sa]);
-                if (++sw == kWStages) {
-                    sw = 0;
-                    pw ^= 1;
-                }
-                if (++sa == kAStages) {
-                    sa = 0;
-                    pa ^= 1;
-                }
+                if (lane == 0) mbar_arrive(&sh.a_full[team]);
             }
             if (!ok || !(ok = mbar_wait(&sh.sums_full, psum, dead))) break;
             psum ^= 1;
             tmem_fence_after();
 
-            // ---- epilogue: a thread has one weight row, eight rows of `a` at a time (the two
-            // halves of the warps take turns)
+            // ---- epilogue: a thread has one weight row, eight rows of `a` at a time, the teams
+            // in turn
             const int blocks = (g.rows + 7) / 8;
             bool sum_parts = false;
             int first = 0, parts = 1;
@@ -506,7 +516,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
                 first = owner(total, B, task0);
                 parts = owner(total, B, task0 + chunks - 1) - first + 1;
                 float *slot = partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * (kMaxRowsTile * kW4Tile);
-                for (int cb = half; cb < blocks; cb += 2) {
+                for (int cb = team; cb < blocks; cb += kAStages) {
                     float v[8];
                     tmem_load8(tmem + lanes + cb * 8, v);
 #pragma unroll
@@ -529,7 +539,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
             const int per = w4_outputs_per_tile(gated);
             const int n = g.tile * per + row % per;
             __nv_bfloat16 *dst = y + (int64_t)(sh.start[g.e] + g.row0) * N + n;
-            for (int cb = half; cb < blocks; cb += 2) {
+            for (int cb = team; cb < blocks; cb += kAStages) {
                 float v[8];
                 if (sum_parts) {
 #pragma unroll
@@ -548,15 +558,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
                 for (int j = 0; j < 8; j++)
                     v[j] = v[j] * __ldcg(row_scale + scale0 + cb * 8 + j) * f;
                 if (gated) {
-                    named_barrier(2 + half, kDecodeWarps * 16);     // the last turn's reads are over
+                    named_barrier(2 + team, 128);     // the last turn's reads are over
                     if (row >= per)
 #pragma unroll
-                        for (int j = 0; j < 8; j++) sh.up[half][j][row - per] = v[j];
-                    named_barrier(2 + half, kDecodeWarps * 16);
+                        for (int j = 0; j < 8; j++) sh.up[team][j][row - per] = v[j];
+                    named_barrier(2 + team, 128);
                     if (row < per)
 #pragma unroll
                         for (int j = 0; j < 8; j++)
-                            v[j] = v[j] / (1.f + __expf(-v[j])) * sh.up[half][j][row];
+                            v[j] = v[j] / (1.f + __expf(-v[j])) * sh.up[team][j][row];
                 }
                 if (row < per && n < N)
 #pragma unroll
