@@ -1075,6 +1075,10 @@ moe_status_t moe_expert_product_w4(const uint16_t *a, int a_rows, const int32_t 
     } else {
         REQUIRE_ARR(expert_offsets, E + 1, 4);
     }
+    // the chunks of the call are numbered in 32 bits
+    REQUIRE(((int64_t)a_rows / 128 + 1 + E) * w4_tiles(N, gated) * w4_chunks(K) < ((int64_t)1 << 31),
+            "%s: a_rows=%d rows of K=%d by N=%d outputs are too many for one call", __func__, a_rows,
+            K, N);
     REQUIRE_ARR(a, (int64_t)a_rows * K, 16);
     REQUIRE_ARR(w4, 1, 16);
     REQUIRE_ARR(w_factor, E, 4);

@@ -87,11 +87,13 @@ __host__ __device__ __forceinline__ int64_t row_groups(int a_rows, int E)
 constexpr int kRowsThreads = 128;
 constexpr int kRowsHeld = 4;        // 16-byte vectors of a row that a thread keeps
 
-// Operand layout of the rows: group g, 64-column atom t at ((g * atoms) + t) * 1024
-// bytes; in an atom row r % 8 has 128 bytes, its 16-byte pieces XOR-ed by r % 8.
-__device__ __forceinline__ int4 *row_piece(uint8_t *x16, int64_t group, int r8, int atoms, int u)
+// Operand layout of the rows: chunk c of group g at (c * groups + g) * 2048 bytes,
+// so a tile's rows are one bulk copy per chunk; in each of its two 64-column
+// atoms row r % 8 has 128 bytes, their 16-byte pieces XOR-ed by r % 8.
+__device__ __forceinline__ int4 *row_piece(uint8_t *x16, int64_t groups, int64_t group, int r8, int u)
 {
-    return (int4 *)(x16 + (group * atoms + (u >> 3)) * 1024 + r8 * 128 + (((u & 7) ^ r8) << 4));
+    return (int4 *)(x16 + ((u >> 4) * groups + group) * 2048 + (u >> 3 & 1) * 1024 + r8 * 128 +
+                    (((u & 7) ^ r8) << 4));
 }
 
 __device__ __forceinline__ uint32_t abs_max_bits(int4 v)
@@ -128,7 +130,8 @@ __global__ void __launch_bounds__(kRowsThreads) k_w4_rows(
     const int tid = threadIdx.x, lane = tid & 31;
     if (blockIdx.x == 0)
         for (int i = tid; i < n_arrivals; i += kRowsThreads) arrivals[i] = 0;
-    const int V = K / 8, atoms = 2 * w4_chunks(K);
+    const int V = K / 8, padded = 16 * w4_chunks(K);
+    const int64_t groups = row_groups(a_rows, E);
     for (int r = blockIdx.x; r < a_rows; r += gridDim.x) {
         // the expert whose run or block holds row r
         int e;
@@ -180,10 +183,10 @@ __global__ void __launch_bounds__(kRowsThreads) k_w4_rows(
 #pragma unroll
         for (int h = 0; h < kRowsHeld; h++) {
             const int v = tid + h * kRowsThreads;
-            if (v < atoms * 8) st_cg(row_piece(x16, group, r8, atoms, v), scale_to_half8(held[h], by));
+            if (v < padded) st_cg(row_piece(x16, groups, group, r8, v), scale_to_half8(held[h], by));
         }
-        for (int v = tid + kRowsHeld * kRowsThreads; v < atoms * 8; v += kRowsThreads)
-            st_cg(row_piece(x16, group, r8, atoms, v),
+        for (int v = tid + kRowsHeld * kRowsThreads; v < padded; v += kRowsThreads)
+            st_cg(row_piece(x16, groups, group, r8, v),
                   v < V ? scale_to_half8(src[v], by) : make_int4(0, 0, 0, 0));
     }
 }
@@ -191,24 +194,28 @@ __global__ void __launch_bounds__(kRowsThreads) k_w4_rows(
 // ---------------------------------------------------------------- the product
 
 constexpr int kAStages = 4;                         // decoded blocks in tensor memory
-constexpr int kDecodeWarps = 4 * kAStages;          // decode the weights, then the epilogue
-constexpr int kMmThreads = (kDecodeWarps + 3) * 32; // + weight loads, row loads, MMA
+constexpr int kDecodeWarps = 4 * kAStages;          // a team of four per decoded block
+constexpr int kEpilogueWarps = 4;
+constexpr int kWarpW = kDecodeWarps + kEpilogueWarps, kWarpX = kWarpW + 1, kWarpMma = kWarpW + 2;
+constexpr int kMmThreads = (kWarpMma + 1) * 32;     // the last three: weight loads, row loads, MMA
 constexpr int kMaxRowsTile = 128;                   // rows of `a` per tile
 constexpr int kWStages = 11;                        // 9 KiB weight blocks in flight
 constexpr int kXBytes = 96 * 1024;                  // ring of row operands
 constexpr int kXStagesMax = 12;
 constexpr int kAColumns = kW4Chunk / 2;             // 64 columns a block
-constexpr int kTmemColumns = 512;                   // 128 of sums, 4 x 64 of weights
+constexpr int kAFirst = 2 * kMaxRowsTile;           // after two tiles of sums
+constexpr int kTmemColumns = kAFirst + kAStages * kAColumns;   // 512: all of it
 constexpr int kGroupBytes = kW4Chunk / 64 * 1024;   // an 8-row group's chunk: 2 KiB
 
 struct MmShared {
     uint64_t w_full[kWStages], w_empty[kWStages];
     uint64_t x_full[kXStagesMax], x_empty[kXStagesMax];
     uint64_t a_full[kAStages], a_empty[kAStages];
-    uint64_t sums_full;
-    int64_t before[kMaxE + 1];       // row tiles of the experts before e
+    uint64_t sums_full[2], sums_empty[2];
+    int before[kMaxE + 1];           // row tiles of the experts before e
     int start[kMaxE], count[kMaxE];
-    float up[kAStages][8][kW4Tile / 2];   // gated epilogue: up factors on their way to the gate's warps
+    float up[8][kW4Tile / 2];        // gated epilogue: up factors on their way to the gate's warps
+    uint64_t done;
     uint32_t tmem;
     int most;                        // largest row tile, in 8-row groups
     int last;                        // this CTA arrived last at a cut tile
@@ -224,23 +231,22 @@ __device__ __forceinline__ int rows_per_tile(int count, int tiles)
 }
 
 struct Segment {
-    int e, tile, row0, rows, n;      // expert, weight tile, rows of `a` in the tile, MMA columns
+    int e, tile, row0, rows;         // expert, weight tile, rows of `a` in the tile
     int c0, c1;                      // chunks of the segment
-    int64_t task;
+    int task;
 };
 
-// The chunks [from, to) of this CTA, one tile after the other.
+// The chunks [at, to) of this CTA, one tile after the other.
 struct Walk {
     const MmShared &sh;
-    int64_t at, to;
+    int at, to;
     int E, tiles, chunks;
     __device__ bool next(Segment &g)
     {
         if (at >= to) return false;
         g.task = at / chunks;
-        g.c0 = (int)(at - g.task * chunks);
-        const int64_t left = to - at;
-        g.c1 = left < chunks - g.c0 ? g.c0 + (int)left : chunks;
+        g.c0 = at - g.task * chunks;
+        g.c1 = min(chunks, g.c0 + to - at);
         at += g.c1 - g.c0;
         int lo = 0, hi = E - 1;      // the last expert with before[e] * tiles <= task
         while (lo < hi) {
@@ -249,27 +255,35 @@ struct Walk {
             else hi = mid - 1;
         }
         g.e = lo;
-        const int64_t local = g.task - sh.before[lo] * tiles;
-        const int nt = (int)(sh.before[lo + 1] - sh.before[lo]);
-        g.tile = (int)(local / nt);
-        const int part = (int)(local - (int64_t)g.tile * nt);
+        const int local = g.task - sh.before[lo] * tiles;
+        const int nt = sh.before[lo + 1] - sh.before[lo];
+        g.tile = local / nt;
         const int count = sh.count[lo], per = rows_per_tile(count, nt);
-        g.row0 = part * per;
+        g.row0 = (local - g.tile * nt) * per;
         g.rows = min(per, count - g.row0);
-        g.n = (g.rows + 15) / 16 * 16;
         return true;
     }
 };
 
 // First chunk of CTA b of B when `total` chunks are cut evenly.
-__device__ __forceinline__ int64_t cut(int64_t total, int b, int B) { return total * b / B; }
+__device__ __forceinline__ int cut(int total, int b, int B) { return (int)((int64_t)total * b / B); }
 // The CTA whose part holds chunk g.
-__device__ __forceinline__ int owner(int64_t total, int B, int64_t g)
+__device__ __forceinline__ int owner(int total, int B, int g)
 {
-    int b = (int)(g * B / total);
+    int b = (int)((int64_t)g * B / total);
     while (cut(total, b + 1, B) <= g) b++;
     while (cut(total, b, B) > g) b--;
     return b;
+}
+
+// After a wait that gave up: waits (with a limit) for the copies in flight, whose
+// barriers are `full`; `next` is the stage to be filled next, in phase `phase`.
+__device__ __forceinline__ void drain(uint64_t *full, int stages, int next, uint32_t phase,
+                                      uint32_t issued)
+{
+    for (int i = 0; i < stages; i++)
+        for (int n = 0; (issued >> i & 1) && n < 100000; n++)
+            if (mbar_try(&full[i], i < next ? phase : phase ^ 1)) break;
 }
 
 __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
@@ -282,13 +296,13 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
     uint8_t *xring = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
     uint8_t *wring = xring + kXBytes;
     MmShared &sh = *(MmShared *)(wring + kWStages * kW4BlockBytes);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(kFull, tid >> 5, 0);
     const int tiles = w4_tiles(N, gated), chunks = w4_chunks(K);
 
     // The row counts are older than k_w4_rows, which has passed its own wait when
     // this kernel starts: they and the weights may be read before pdl_wait.
     pdl_trigger();
-    bool bad = false;
     if (tid == 0) {
         sh.most = 0;
         sh.dead = 0;
@@ -304,244 +318,256 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
             mbar_init(&sh.a_full[i], 4);
             mbar_init(&sh.a_empty[i], 1);
         }
-        mbar_init(&sh.sums_full, 1);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&sh.sums_full[i], 1);
+            mbar_init(&sh.sums_empty[i], kEpilogueWarps);
+        }
+        mbar_init(&sh.done, 1);
         mbar_init_fence();
     }
-    if (warp == kDecodeWarps + 2) tmem_alloc(&sh.tmem, kTmemColumns);
-    __syncthreads();
-    int most = 0;
+    if (warp == kWarpMma) tmem_alloc(&sh.tmem, kTmemColumns);
+    bool bad = false;
     for (int e = tid; e < E; e += kMmThreads) {
         int start, count;
         expert_rows(offsets, counts, block_rows, a_rows, e, start, count, bad);
         sh.start[e] = start;
         sh.count[e] = count;
-        if (count > 0) most = max(most, rows_per_tile(count, tiles_of(count)) / 8);
     }
-    if (most > 0) atomicMax(&sh.most, most);
-    if (bad && blockIdx.x == 0) flag_status(dev_status, MOE_ERR_INVALID_ARG);
     __syncthreads();
     if (warp == 0) {
-        int64_t run = 0;
+        // prefix sums of the experts' row tiles.  Ranges that overlap (offsets that
+        // fall) could hold more rows than there are: those past a_rows are dropped.
+        int tiles_before = 0, most = 0;
+        int64_t rows_before = 0;
         for (int e0 = 0; e0 < E; e0 += 32) {
-            const int n = e0 + lane < E ? tiles_of(sh.count[e0 + lane]) : 0;
-            int64_t inc = n;
+            const int e = e0 + lane;
+            int64_t rows = e < E ? sh.count[e] : 0;
+            const int count = (int)rows;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const int64_t o = __shfl_up_sync(kFull, inc, off);
-                if (lane >= off) inc += o;
+                const int64_t o = __shfl_up_sync(kFull, rows, off);
+                if (lane >= off) rows += o;
             }
-            if (e0 + lane < E) sh.before[e0 + lane] = run + inc - n;
-            run += __shfl_sync(kFull, inc, 31);
+            const bool drop = count > 0 && rows_before + rows > a_rows;
+            if (drop) {
+                sh.count[e] = 0;
+                bad = true;
+            }
+            const int n = drop ? 0 : tiles_of(count);
+            if (n > 0) most = max(most, rows_per_tile(count, n) / 8);
+            const int inc = warp_inclusive_scan(n);
+            if (e < E) sh.before[e] = tiles_before + inc - n;
+            tiles_before += __shfl_sync(kFull, inc, 31);
+            rows_before += __shfl_sync(kFull, rows, 31);
         }
-        if (lane == 0) sh.before[E] = run;
+        most = __reduce_max_sync(kFull, most);
+        if (lane == 0) {
+            sh.before[E] = tiles_before;
+            sh.most = most;
+        }
     }
+    if (bad && blockIdx.x == 0) flag_status(dev_status, MOE_ERR_INVALID_ARG);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
 
     const uint32_t tmem = sh.tmem;
-    const int64_t total = sh.before[E] * tiles * chunks;
+    const int total = sh.before[E] * tiles * chunks;
     // at least a chunk for every CTA that takes part, so each part of a cut tile arrives
-    const int B = total < gridDim.x ? (int)total : gridDim.x;
+    const int B = min(total, (int)gridDim.x);
     const bool idle = (int)blockIdx.x >= B;
     Walk walk{sh, idle ? 0 : cut(total, blockIdx.x, B), idle ? 0 : cut(total, blockIdx.x + 1, B), E,
               tiles, chunks};
-    const int x_stages = min(kXStagesMax, kXBytes / max(1, sh.most * kGroupBytes));
     const int x_stage_bytes = sh.most * kGroupBytes;
+    const int x_stages = min(kXStagesMax, kXBytes / max(1, x_stage_bytes));
+    const bool runs = offsets != nullptr;
     volatile int *dead = &sh.dead;
     Segment g;
+    bool ok = true;
 
-    if (warp == kDecodeWarps) {
+    if (warp == kWarpW) {
         // ---- weight blocks: one bulk copy each
-        if (lane == 0) {
-            int s = 0;
-            uint32_t phase = 0, issued = 0;
-            bool ok = true;
-            while (ok && walk.next(g)) {
-                const uint8_t *src = w4 + (((int64_t)g.e * tiles + g.tile) * chunks + g.c0) *
-                                              (int64_t)kW4BlockBytes;
-                for (int c = g.c0; c < g.c1; c++, src += kW4BlockBytes) {
-                    if (!(ok = mbar_wait(&sh.w_empty[s], phase ^ 1, dead))) break;
+        int s = 0;
+        uint32_t phase = 0, issued = 0;
+        while (ok && walk.next(g)) {
+            const uint8_t *src =
+                w4 + (((int64_t)g.e * tiles + g.tile) * chunks + g.c0) * (int64_t)kW4BlockBytes;
+            for (int c = g.c0; c < g.c1; c++, src += kW4BlockBytes) {
+                if (!(ok = mbar_wait_warp(&sh.w_empty[s], phase ^ 1, dead))) break;
+                if (elect_lane()) {
                     mbar_expect(&sh.w_full[s], kW4BlockBytes);
                     bulk_load(wring + s * kW4BlockBytes, src, kW4BlockBytes, &sh.w_full[s]);
-                    issued |= 1u << s;
-                    if (++s == kWStages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
+                }
+                __syncwarp();
+                issued |= 1u << s;
+                if (++s == kWStages) {
+                    s = 0;
+                    phase ^= 1;
                 }
             }
-            if (!ok)            // no copy is left in flight
-                for (int i = 0; i < kWStages; i++)
-                    if (issued >> i & 1) {
-                        const uint32_t last = i < s ? phase : phase ^ 1;
-                        for (int n = 0; n < 100000 && !mbar_try(&sh.w_full[i], last); n++) {}
-                    }
         }
-    } else if (warp == kDecodeWarps + 1) {
-        // ---- row operands: one bulk copy per 8-row group
-        if (lane == 0) {
-            pdl_wait();
-            const int atoms = 2 * chunks;
-            int s = 0;
-            uint32_t phase = 0, issued = 0;
-            bool ok = true;
-            while (ok && walk.next(g)) {
-                const int64_t group0 =
-                    row_group(offsets != nullptr, sh.start[g.e], block_rows, g.e) + g.row0 / 8;
-                const int groups = (g.rows + 7) / 8;
-                for (int c = g.c0; c < g.c1; c++) {
-                    if (!(ok = mbar_wait(&sh.x_empty[s], phase ^ 1, dead))) break;
-                    mbar_expect(&sh.x_full[s], groups * kGroupBytes);
-                    uint8_t *dst = xring + s * x_stage_bytes;
-                    for (int i = 0; i < groups; i++)
-                        bulk_load(dst + i * kGroupBytes,
-                                  x16 + ((group0 + i) * atoms + 2 * c) * 1024, kGroupBytes,
-                                  &sh.x_full[s]);
-                    issued |= 1u << s;
-                    if (++s == x_stages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
+        if (!ok) drain(sh.w_full, kWStages, s, phase, issued);
+    } else if (warp == kWarpX) {
+        // ---- row operands: one bulk copy per chunk
+        pdl_wait();
+        const int64_t groups = row_groups(a_rows, E);
+        int s = 0;
+        uint32_t phase = 0, issued = 0;
+        while (ok && walk.next(g)) {
+            const int64_t group0 = row_group(runs, sh.start[g.e], block_rows, g.e) + g.row0 / 8;
+            const uint32_t bytes = (g.rows + 7) / 8 * kGroupBytes;
+            for (int c = g.c0; c < g.c1; c++) {
+                if (!(ok = mbar_wait_warp(&sh.x_empty[s], phase ^ 1, dead))) break;
+                if (elect_lane()) {
+                    mbar_expect(&sh.x_full[s], bytes);
+                    bulk_load(xring + s * x_stage_bytes, x16 + (c * groups + group0) * kGroupBytes,
+                              bytes, &sh.x_full[s]);
+                }
+                __syncwarp();
+                issued |= 1u << s;
+                if (++s == x_stages) {
+                    s = 0;
+                    phase ^= 1;
                 }
             }
-            if (!ok)
-                for (int i = 0; i < x_stages; i++)
-                    if (issued >> i & 1) {
-                        const uint32_t last = i < s ? phase : phase ^ 1;
-                        for (int n = 0; n < 100000 && !mbar_try(&sh.x_full[i], last); n++) {}
-                    }
         }
-    } else if (warp == kDecodeWarps + 2) {
-        // ---- MMA: eight steps of 16 columns per chunk, issued by one thread
-        if (lane == 0) {
-            int sx = 0, sa = 0;
-            uint32_t px = 0, pa = 0;
-            bool ok = true;
-            while (ok && walk.next(g)) {
-                const uint32_t word = mma_f16_word(g.n);
-                for (int c = g.c0; c < g.c1; c++) {
-                    if (!(ok = mbar_wait(&sh.x_full[sx], px, dead) &&
-                               mbar_wait(&sh.a_full[sa], pa, dead)))
-                        break;
-                    tmem_fence_after();
-                    const uint32_t a = tmem + kMaxRowsTile + sa * kAColumns;
-                    const uint64_t b = mma_smem_word(smem_addr(xring) + sx * x_stage_bytes, kGroupBytes);
+        if (!ok) drain(sh.x_full, x_stages, s, phase, issued);
+    } else if (warp == kWarpMma) {
+        // ---- MMA: eight steps of 16 columns per chunk, into the two tiles of sums in turn
+        int sx = 0, sa = 0, d = 0;
+        uint32_t px = 0, pa = 0, pd = 0;
+        while (ok && walk.next(g)) {
+            const uint32_t word = mma_f16_word((g.rows + 15) / 16 * 16);
+            if (!(ok = mbar_wait_warp(&sh.sums_empty[d], pd ^ 1, dead))) break;
+            for (int c = g.c0; c < g.c1; c++) {
+                if (!(ok = mbar_wait_warp(&sh.x_full[sx], px, dead) &&
+                           mbar_wait_warp(&sh.a_full[sa], pa, dead)))
+                    break;
+                tmem_fence_after();
+                const uint32_t a = tmem + kAFirst + sa * kAColumns;
+                const uint64_t b = mma_smem_word(smem_addr(xring) + sx * x_stage_bytes, kGroupBytes);
+                if (elect_lane()) {
 #pragma unroll
                     for (int i = 0; i < kW4Chunk / 16; i++)     // 32 bytes a step, 1 KiB an atom
-                        mma_f16(tmem, a + i * 8, b + (uint64_t)((i & 3) * 2 + (i >> 2) * 64), word,
-                                c > g.c0 || i > 0);
+                        mma_f16(tmem + d * kMaxRowsTile, a + i * 8,
+                                b + (uint64_t)((i & 3) * 2 + (i >> 2) * 64), word, c > g.c0 || i > 0);
                     mma_commit(&sh.a_empty[sa]);
                     mma_commit(&sh.x_empty[sx]);
-                    if (++sx == x_stages) {
-                        sx = 0;
-                        px ^= 1;
-                    }
-                    if (++sa == kAStages) {
-                        sa = 0;
-                        pa ^= 1;
-                    }
+                    if (c == g.c1 - 1) mma_commit(&sh.sums_full[d]);
                 }
-                if (ok) mma_commit(&sh.sums_full);
+                __syncwarp();
+                if (++sx == x_stages) {
+                    sx = 0;
+                    px ^= 1;
+                }
+                if (++sa == kAStages) {
+                    sa = 0;
+                    pa ^= 1;
+                }
             }
+            d ^= 1;
+            if (d == 0) pd ^= 1;
         }
-    } else {
+        // the MMAs in flight end before their memory goes
+        if (elect_lane()) mma_commit(&sh.done);
+        __syncwarp();
+        for (int n = 0; n < 100000 && !mbar_try(&sh.done, 0); n++) {}
+    } else if (warp < kDecodeWarps) {
         // ---- decode: team t of four warps (one per quarter of the tensor-memory lanes, a row
-        // a lane) has every kAStages-th chunk and A stage t; then the same warps finish the tile
+        // a lane) has every kAStages-th chunk and A stage t
         const int quarter = warp & 3, team = warp >> 2;
         const int row = quarter * 32 + lane;
-        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const uint32_t a_at = tmem + lanes + kMaxRowsTile + team * kAColumns;
+        const uint32_t a_at =
+            tmem + ((uint32_t)(quarter * 32) << 16) + kAFirst + team * kAColumns;
         int sw = team;               // stage of the team's next chunk
-        uint32_t pw = 0, pa = 0, psum = 0;
-        uint32_t mine = team, seen = 0;      // that chunk's number; chunks of the past segments
-        bool ok = true;
-        pdl_wait();
-        while (ok && walk.next(g)) {
-            seen += g.c1 - g.c0;
-            for (; mine < seen; mine += kAStages) {
-                if (!(ok = mbar_wait(&sh.w_full[sw], pw, dead))) break;
-                const uint8_t *block = wring + sw * kW4BlockBytes;
-                uint4 q[4];
+        uint32_t pw = 0, pa = 0;
+        for (int c = walk.at + team; c < walk.to; c += kAStages) {
+            if (!mbar_wait_warp(&sh.w_full[sw], pw, dead)) break;
+            const uint8_t *block = wring + sw * kW4BlockBytes;
+            uint4 q[4];
 #pragma unroll
-                for (int j = 0; j < 4; j++) q[j] = *(const uint4 *)(block + (j * kW4Tile + row) * 16);
-                const uint2 sc = *(const uint2 *)(block + kW4CodeBytes + row * 8);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.w_empty[sw]);
-                sw += kAStages;
-                if (sw >= kWStages) {
-                    sw -= kWStages;
-                    pw ^= 1;
-                }
-                if (!(ok = mbar_wait(&sh.a_empty[team], pa ^ 1, dead))) break;
-                pa ^= 1;
-                tmem_fence_after();
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const uint32_t s4 = h ? sc.y : sc.x;
-                    const uint32_t s01 = e4m3x2_to_half2(s4), s23 = e4m3x2_to_half2(s4 >> 16);
-                    const uint32_t group_scale[4] = {
-                        __byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232),
-                        __byte_perm(s23, 0, 0x1010), __byte_perm(s23, 0, 0x3232)};
-                    const uint32_t word[8] = {q[2 * h].x,     q[2 * h].y,     q[2 * h].z,
-                                              q[2 * h].w,     q[2 * h + 1].x, q[2 * h + 1].y,
-                                              q[2 * h + 1].z, q[2 * h + 1].w};
-                    uint32_t out[32];
-#pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        uint32_t half2s[4];
-                        e2m1x8_to_half2(word[i], half2s);
-#pragma unroll
-                        for (int p = 0; p < 4; p++)
-                            out[4 * i + p] = mul_half2(half2s[p], group_scale[i >> 1]);
-                    }
-                    tmem_store32(a_at + h * 32, out);
-                }
-                tmem_wait_st();
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.a_full[team]);
+            for (int j = 0; j < 4; j++) q[j] = *(const uint4 *)(block + (j * kW4Tile + row) * 16);
+            const uint2 sc = *(const uint2 *)(block + kW4CodeBytes + row * 8);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.w_empty[sw]);
+            sw += kAStages;
+            if (sw >= kWStages) {
+                sw -= kWStages;
+                pw ^= 1;
             }
-            if (!ok || !(ok = mbar_wait(&sh.sums_full, psum, dead))) break;
-            psum ^= 1;
+            if (!mbar_wait_warp(&sh.a_empty[team], pa ^ 1, dead)) break;
+            pa ^= 1;
             tmem_fence_after();
-
-            // ---- epilogue: a thread has one weight row, eight rows of `a` at a time, the teams
-            // in turn
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const uint32_t s4 = h ? sc.y : sc.x;
+                const uint32_t s01 = e4m3x2_to_half2(s4), s23 = e4m3x2_to_half2(s4 >> 16);
+                const uint32_t group_scale[4] = {
+                    __byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232),
+                    __byte_perm(s23, 0, 0x1010), __byte_perm(s23, 0, 0x3232)};
+                const uint32_t word[8] = {q[2 * h].x,     q[2 * h].y,     q[2 * h].z,
+                                          q[2 * h].w,     q[2 * h + 1].x, q[2 * h + 1].y,
+                                          q[2 * h + 1].z, q[2 * h + 1].w};
+                uint32_t out[32];
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    uint32_t half2s[4];
+                    e2m1x8_to_half2(word[i], half2s);
+#pragma unroll
+                    for (int p = 0; p < 4; p++)
+                        out[4 * i + p] = mul_half2(half2s[p], group_scale[i >> 1]);
+                }
+                tmem_store32(a_at + h * 32, out);
+            }
+            tmem_wait_st();
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.a_full[team]);
+        }
+    } else {
+        // ---- epilogue: a thread has one weight row, eight rows of `a` at a time
+        const int quarter = warp & 3;
+        const int row = quarter * 32 + lane;
+        const int per = w4_outputs_per_tile(gated);
+        int d = 0;
+        uint32_t pd = 0;
+        pdl_wait();
+        while (walk.next(g)) {
+            const float f = __ldg(factor + g.e);
+            const int64_t scale0 =
+                (int64_t)row_group(runs, sh.start[g.e], block_rows, g.e) * 8 + g.row0;
+            const int n = g.tile * per + row % per;
+            __nv_bfloat16 *dst = y + (int64_t)(sh.start[g.e] + g.row0) * N + n;
             const int blocks = (g.rows + 7) / 8;
-            bool sum_parts = false;
             int first = 0, parts = 1;
             if (g.c1 - g.c0 < chunks) {
-                const int64_t task0 = g.task * chunks;
-                first = owner(total, B, task0);
-                parts = owner(total, B, task0 + chunks - 1) - first + 1;
-                float *slot = partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * (kMaxRowsTile * kW4Tile);
-                for (int cb = team; cb < blocks; cb += kAStages) {
+                first = owner(total, B, g.task * chunks);
+                parts = owner(total, B, g.task * chunks + chunks - 1) - first + 1;
+            }
+            const uint32_t sums = tmem + ((uint32_t)(quarter * 32) << 16) + d * kMaxRowsTile;
+            // one answer for the four warps, which meet at barriers below
+            if (!named_all(1, kEpilogueWarps * 32, mbar_wait(&sh.sums_full[d], pd, dead))) break;
+            tmem_fence_after();
+            bool finish = true;
+            if (parts > 1) {
+                float *slot =
+                    partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * (kMaxRowsTile * kW4Tile);
+                for (int cb = 0; cb < blocks; cb++) {
                     float v[8];
-                    tmem_load8(tmem + lanes + cb * 8, v);
+                    tmem_load8(sums + cb * 8, v);
 #pragma unroll
                     for (int j = 0; j < 8; j++) __stcg(slot + (cb * 8 + j) * kW4Tile + row, v[j]);
                 }
                 __threadfence();
-                named_barrier(1, kDecodeWarps * 32);
-                if (tid == 0) sh.last = atomicAdd(arrivals + first, 1) == parts - 1;
-                named_barrier(1, kDecodeWarps * 32);
-                if (!sh.last) {
-                    tmem_fence_before();
-                    continue;
-                }
+                named_barrier(1, kEpilogueWarps * 32);
+                if (quarter == 0 && lane == 0) sh.last = atomicAdd(arrivals + first, 1) == parts - 1;
+                named_barrier(1, kEpilogueWarps * 32);
+                finish = sh.last;
                 __threadfence();
-                sum_parts = true;
             }
-            const float f = __ldg(factor + g.e);
-            const int64_t scale0 =
-                (int64_t)row_group(offsets != nullptr, sh.start[g.e], block_rows, g.e) * 8 + g.row0;
-            const int per = w4_outputs_per_tile(gated);
-            const int n = g.tile * per + row % per;
-            __nv_bfloat16 *dst = y + (int64_t)(sh.start[g.e] + g.row0) * N + n;
-            for (int cb = team; cb < blocks; cb += kAStages) {
+            for (int cb = 0; finish && cb < blocks; cb++) {
                 float v[8];
-                if (sum_parts) {
+                if (parts > 1) {
 #pragma unroll
                     for (int j = 0; j < 8; j++) v[j] = 0.f;
                     for (int p = first; p < first + parts; p++) {
@@ -552,21 +578,21 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
                         for (int j = 0; j < 8; j++) v[j] += __ldcg(slot + (cb * 8 + j) * kW4Tile + row);
                     }
                 } else {
-                    tmem_load8(tmem + lanes + cb * 8, v);
+                    tmem_load8(sums + cb * 8, v);
                 }
 #pragma unroll
                 for (int j = 0; j < 8; j++)
                     v[j] = v[j] * __ldcg(row_scale + scale0 + cb * 8 + j) * f;
                 if (gated) {
-                    named_barrier(2 + team, 128);     // the last turn's reads are over
+                    named_barrier(1, kEpilogueWarps * 32);      // the last block's reads are over
                     if (row >= per)
 #pragma unroll
-                        for (int j = 0; j < 8; j++) sh.up[team][j][row - per] = v[j];
-                    named_barrier(2 + team, 128);
+                        for (int j = 0; j < 8; j++) sh.up[j][row - per] = v[j];
+                    named_barrier(1, kEpilogueWarps * 32);
                     if (row < per)
 #pragma unroll
                         for (int j = 0; j < 8; j++)
-                            v[j] = v[j] / (1.f + __expf(-v[j])) * sh.up[team][j][row];
+                            v[j] = v[j] / (1.f + __expf(-v[j])) * sh.up[j][row];
                 }
                 if (row < per && n < N)
 #pragma unroll
@@ -575,19 +601,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
                             dst[(int64_t)(cb * 8 + j) * N] = __float2bfloat16_rn(v[j]);
             }
             tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.sums_empty[d]);
+            d ^= 1;
+            if (d == 0) pd ^= 1;
         }
     }
     __syncthreads();
-    if (warp == kDecodeWarps + 2) {
-        if (sh.dead) {      // MMAs may still run: wait for them before the memory goes
-            if (lane == 0) {
-                mma_commit(&sh.sums_full);
-                flag_status(dev_status, MOE_ERR_TIMEOUT);
-            }
-            const uint64_t start = global_ns();
-            while (global_ns() - start < 1000000ull) {}
-        }
-        __syncwarp();
+    if (warp == kWarpMma) {
+        if (sh.dead && lane == 0) flag_status(dev_status, MOE_ERR_TIMEOUT);
         tmem_fence_after();
         tmem_free(tmem, kTmemColumns);
     }

@@ -69,6 +69,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
     }
 }
 
+// The same by a whole warp, with one answer for all of its lanes.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *dead)
+{
+    return __all_sync(kFull, mbar_wait(bar, parity, dead));
+}
+
 // Bytes (a multiple of 16, both ends 16-byte aligned) from global to shared
 // memory; the barrier counts them.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
@@ -155,9 +161,31 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar)
                  : "memory");
 }
 
+// One lane of a converged warp, the same for all calls; the compiler keeps what
+// the chosen lane issues in uniform registers.
+__device__ __forceinline__ bool elect_lane()
+{
+    uint32_t chosen;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(chosen));
+    return chosen != 0;
+}
+
 __device__ __forceinline__ void named_barrier(int id, int threads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Barrier `id` of `threads` threads; whether all of them brought true.
+__device__ __forceinline__ bool named_all(int id, int threads, bool mine)
+{
+    uint32_t all;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+                 "barrier.cta.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(all)
+                 : "r"(id), "r"(threads), "r"((uint32_t)mine)
+                 : "memory");
+    return all != 0;
 }
 
 }  // namespace moe
