@@ -87,6 +87,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
 def load_library() -> ctypes.CDLL:
     """Load libmoeroute.so (raises MoeLibraryMissing if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -185,8 +187,10 @@ def _check(rc: int):
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    # the current stream's handle without a Stream object around it (0.3 instead of 2.8 us a call)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 _BF16_TYPES = (torch.bfloat16, torch.int16) + ((torch.uint16,) if hasattr(torch, "uint16") else ())
@@ -214,17 +218,18 @@ def _status_ptr(dev_status):
 
 def _arr(t, name: str, dtypes, shape):
     """Address of a contiguous CUDA tensor of one of `dtypes` and of `shape` (None: any size)."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor (got {t.device})")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
 
 
 def _opt(t, name: str, dtypes, shape):
@@ -835,7 +840,9 @@ def moe_expert_product_w4(a, w4, w_factor, y, ws, expert_offsets=None, masked_co
     lib = load_library()
     rows, K = a.shape
     N, E = y.shape[-1], w_factor.shape[0]
-    if w4.numel() < moe_w4_bytes(E, N, K, gated):
+    # the size of w4 in the layout: blocks of 9,216 bytes, 128 columns by 128 rows (gated: 64 outputs)
+    outputs = 64 if gated else 128
+    if w4.numel() < E * -(-N // outputs) * -(-K // 128) * 9216:
         raise ValueError(f"w4: {w4.numel()} bytes are not the packed weights of E={E}, N={N}, K={K}, "
                          f"gated={gated}")
     _check(lib.moe_expert_product_w4(

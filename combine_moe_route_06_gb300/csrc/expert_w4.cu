@@ -544,6 +544,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
                 first = owner(total, B, g.task * chunks);
                 parts = owner(total, B, g.task * chunks + chunks - 1) - first + 1;
             }
+            float scale[kMaxRowsTile / 32];      // of rows lane, lane + 32, ... of the tile
+#pragma unroll
+            for (int i = 0; i < kMaxRowsTile / 32; i++)
+                scale[i] = lane + 32 * i < g.rows ? __ldcg(row_scale + scale0 + lane + 32 * i) : 0.f;
             const uint32_t sums = tmem + ((uint32_t)(quarter * 32) << 16) + d * kMaxRowsTile;
             // one answer for the four warps, which meet at barriers below
             if (!named_all(1, kEpilogueWarps * 32, mbar_wait(&sh.sums_full[d], pd, dead))) break;
@@ -580,9 +584,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
                 } else {
                     tmem_load8(sums + cb * 8, v);
                 }
+                const float mine = cb < 4 ? scale[0] : cb < 8 ? scale[1] : cb < 12 ? scale[2] : scale[3];
 #pragma unroll
                 for (int j = 0; j < 8; j++)
-                    v[j] = v[j] * __ldcg(row_scale + scale0 + cb * 8 + j) * f;
+                    v[j] = v[j] * __shfl_sync(kFull, mine, (cb & 3) * 8 + j) * f;
                 if (gated) {
                     named_barrier(1, kEpilogueWarps * 32);      // the last block's reads are over
                     if (row >= per)
