@@ -29,6 +29,11 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162f
 __device__ __forceinline__ void store_as(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_as(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
+// exp(d) of a distance d <= 0 from the largest logit.  The error of the fast form
+// grows with |d|, to 2^-22 |d| relative, where the probability is exp(d) small:
+// below 2^-23 of the largest probability.
+__device__ __forceinline__ float exp_below(float d) { return __expf(d); }
+
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
@@ -43,15 +48,20 @@ __device__ __forceinline__ float warp_max(float v)
 }
 
 // Workspace of one call: per source and CTA the sums of the probabilities, the
-// pick counts, the sum of lse^2 and the number of valid tokens.
+// pick counts, the sum of lse^2 and the number of valid tokens; then what the
+// second kernel's CTAs (one per source and 32 experts) hand to the last of them.
 struct LossWs {
-    float *prob;      // [S][B][E]
-    int32_t *picks;   // [S][B][E]
-    float *z;         // [S][B]
-    int32_t *valid;   // [S][B]
+    float *prob;       // [S][B][E]
+    int32_t *picks;    // [S][B][E]
+    float *z;          // [S][B]
+    int32_t *valid;    // [S][B]
+    float *balance;    // [S][ceil(E / 32)]
+    float *z_mean;     // [S]
+    int32_t *arrived;  // [1]
 };
 
-// CTAs per source: at least 16 rows each, and about two per SM over all sources.
+// CTAs per source: two rows a warp where there are few, else about two CTAs per SM
+// over all sources (four took 1.7 us more on 8 x 4,096 x 384 logits: more parts).
 int loss_ctas(int S, int T)
 {
     const int by_rows = (T + 15) / 16;
@@ -59,6 +69,7 @@ int loss_ctas(int S, int T)
     const int b = by_rows < by_grid ? by_rows : by_grid;
     return b < 1 ? 1 : b;
 }
+int loss_blocks(int E) { return (E + 31) / 32; }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -73,6 +84,12 @@ LossWs carve(void *ws, int S, int B, int E)
     w.z = (float *)p;
     p += align256((size_t)S * B * 4);
     w.valid = (int32_t *)p;
+    p += align256((size_t)S * B * 4);
+    w.balance = (float *)p;
+    p += align256((size_t)S * loss_blocks(E) * 4);
+    w.z_mean = (float *)p;
+    p += align256((size_t)S * 4);
+    w.arrived = (int32_t *)p;
     return w;
 }
 
@@ -93,6 +110,7 @@ __global__ void __launch_bounds__(kRlThreads) k_balance_part(
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int s = blockIdx.y, b = blockIdx.x, B = gridDim.x;
     for (int e = threadIdx.x; e < E; e += kRlThreads) picks[e] = 0;
+    if (s == 0 && b == 0 && threadIdx.x == 0) *ws.arrived = 0;
     __syncthreads();
 
     float acc[VPL];
@@ -101,25 +119,46 @@ __global__ void __launch_bounds__(kRlThreads) k_balance_part(
     float z = 0.f;
     int n = 0;
     bool bad_id = false;
-    for (int t = b * kRlWarps + warp; t < T; t += B * kRlWarps) {
+    // the next row's loads are in flight while this one is summed, and the mark of
+    // the row after it, so that rows that are not valid are never loaded
+    struct Row {
+        L v[VPL];
+        int id;
+        bool valid;
+    } next;
+    const int step = B * kRlWarps;
+    auto valid = [&](int64_t t) { return t < T && (mask == nullptr || mask[(int64_t)s * T + t] != 0); };
+    auto load = [&](int64_t t, bool marked, Row &r) {
+        r.valid = marked;
+        r.id = -1;
+        if (!marked) return;
         const int64_t row = (int64_t)s * T + t;
-        if (mask && mask[row] == 0) {
+        if (lane < k) r.id = __ldg(ids + row * k + lane);
+        const L *src = logits + row * E;
+#pragma unroll
+        for (int i = 0; i < VPL; i++)
+            if (lane + 32 * i < E) r.v[i] = src[lane + 32 * i];
+    };
+    const int t0 = b * kRlWarps + warp;
+    load(t0, valid(t0), next);
+    bool marked = valid(t0 + step);
+    for (int64_t t = t0; t < T; t += step) {
+        const Row now = next;
+        load(t + step, marked, next);
+        marked = valid(t + 2 * step);
+        const int64_t row = (int64_t)s * T + t;
+        if (!now.valid) {
             if (lane == 0) lse[row] = 0.f;
             continue;
         }
         n++;
-        if (lane < k) {
-            const int id = __ldg(ids + row * k + lane);
-            if (id >= E) bad_id = true;
-            else if (id >= 0) atomicAdd(&picks[id], 1);
-        }
-        const L *src = logits + row * E;
+        if (now.id >= E) bad_id = true;
+        else if (now.id >= 0) atomicAdd(&picks[now.id], 1);
         float v[VPL];
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < VPL; i++) {
-            const int e = lane + 32 * i;
-            v[i] = e < E ? to_float(src[e]) : -INFINITY;
+            v[i] = lane + 32 * i < E ? to_float(now.v[i]) : -INFINITY;
             top = fmaxf(top, v[i]);
         }
         top = warp_max(top);
@@ -127,7 +166,7 @@ __global__ void __launch_bounds__(kRlThreads) k_balance_part(
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < VPL; i++) {
-            v[i] = expf(v[i] - base);
+            v[i] = exp_below(v[i] - base);
             sum += v[i];
         }
         sum = warp_sum(sum);
@@ -169,64 +208,81 @@ __global__ void __launch_bounds__(kRlThreads) k_balance_part(
     }
 }
 
-// Sums the CTAs' parts in their order, source after source.
-__global__ void __launch_bounds__(1024) k_balance_finish(LossWs ws, int S, int B, int E, int k,
-                                                         int32_t *__restrict__ counts,
-                                                         float *__restrict__ prob_mean,
-                                                         int32_t *__restrict__ n_valid,
-                                                         float *__restrict__ losses)
+// One CTA per source and 32 experts sums the parts in their order; the last CTA
+// to arrive adds the losses up, in order again.
+__global__ void __launch_bounds__(kRlThreads) k_balance_finish(LossWs ws, int S, int B, int E, int k,
+                                                               int32_t *__restrict__ counts,
+                                                               float *__restrict__ prob_mean,
+                                                               int32_t *__restrict__ n_valid,
+                                                               float *__restrict__ losses)
 {
     pdl_wait();
     pdl_trigger();
-    __shared__ float part[32];
+    __shared__ float prob[kRlWarps][32];
+    __shared__ int picks[kRlWarps][32];
     __shared__ int n_sh;
     __shared__ float z_sh;
+    __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float balance = 0.f, z = 0.f;   // thread 0's
-    for (int s = 0; s < S; s++) {
-        if (warp == 0) {
-            int n = 0;
-            float zs = 0.f;
-            for (int b = lane; b < B; b += 32) {
-                n += ws.valid[(int64_t)s * B + b];
-                zs += ws.z[(int64_t)s * B + b];
-            }
-            n = __reduce_add_sync(kFull, n);
-            zs = warp_sum(zs);
-            if (lane == 0) {
-                n_sh = n;
-                z_sh = zs;
-            }
+    const int block = blockIdx.x, blocks = gridDim.x, s = blockIdx.y;
+    const int e = block * 32 + lane;
+    float p = 0.f;
+    int c = 0;
+    if (e < E) {
+#pragma unroll 4
+        for (int b = warp; b < B; b += kRlWarps) {
+            p += ws.prob[((int64_t)s * B + b) * E + e];
+            c += ws.picks[((int64_t)s * B + b) * E + e];
         }
-        __syncthreads();
-        const int n = n_sh;
-        const float inv = n > 0 ? 1.f / (float)n : 0.f;
-        float dot = 0.f;
-        for (int e = threadIdx.x; e < E; e += 1024) {
-            float p = 0.f;
-            int c = 0;
-            for (int b = 0; b < B; b++) {
-                p += ws.prob[((int64_t)s * B + b) * E + e];
-                c += ws.picks[((int64_t)s * B + b) * E + e];
-            }
-            p *= inv;
-            counts[(int64_t)s * E + e] = c;
-            prob_mean[(int64_t)s * E + e] = p;
-            dot = fmaf((float)c, p, dot);
-        }
-        dot = warp_sum(dot);
-        if (lane == 0) part[warp] = dot;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            float d = 0.f;
-            for (int w = 0; w < 32; w++) d += part[w];
-            balance += d * inv * ((float)E / (float)k);
-            z += z_sh * inv;
-            n_valid[s] = n;
-        }
-        __syncthreads();
     }
-    if (threadIdx.x == 0) {
+    prob[warp][lane] = p;
+    picks[warp][lane] = c;
+    if (warp == 1) {
+        int n = 0;
+        for (int b = lane; b < B; b += 32) n += ws.valid[(int64_t)s * B + b];
+        n = __reduce_add_sync(kFull, n);
+        if (lane == 0) n_sh = n;
+    } else if (warp == 2) {
+        float z = 0.f;
+        for (int b = lane; b < B; b += 32) z += ws.z[(int64_t)s * B + b];
+        z = warp_sum(z);
+        if (lane == 0) z_sh = z;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    const int n = n_sh;
+    const float inv = n > 0 ? 1.f / (float)n : 0.f;
+    p = 0.f;
+    c = 0;
+#pragma unroll
+    for (int w = 0; w < kRlWarps; w++) {
+        p += prob[w][lane];
+        c += picks[w][lane];
+    }
+    p *= inv;
+    if (e < E) {
+        counts[(int64_t)s * E + e] = c;
+        prob_mean[(int64_t)s * E + e] = p;
+    }
+    const float dot = warp_sum((float)c * p);
+    if (lane == 0) {
+        ws.balance[(int64_t)s * blocks + block] = dot * inv * ((float)E / (float)k);
+        if (block == 0) {
+            n_valid[s] = n;
+            ws.z_mean[s] = z_sh * inv;
+        }
+        __threadfence();
+        last = atomicAdd(ws.arrived, 1) == blocks * S - 1;
+    }
+    __syncwarp();
+    if (!last) return;
+    __threadfence();
+    float balance = 0.f, z = 0.f;
+    for (int i = lane; i < S * blocks; i += 32) balance += __ldcg(ws.balance + i);
+    for (int i = lane; i < S; i += 32) z += __ldcg(ws.z_mean + i);
+    balance = warp_sum(balance);
+    z = warp_sum(z);
+    if (lane == 0) {
         losses[0] = balance / (float)S;
         losses[1] = z / (float)S;
     }
@@ -304,7 +360,7 @@ __global__ void __launch_bounds__(kRlThreads) k_route_backward(
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < VPL; i++) {
-                p[i] = expf(p[i] - base);
+                p[i] = exp_below(p[i] - base);
                 sum += p[i];
             }
             sum = warp_sum(sum);
@@ -318,7 +374,7 @@ __global__ void __launch_bounds__(kRlThreads) k_route_backward(
             const float back = zc - warp_sum(dot);
             float chosen = 0.f;
             if (id >= 0) {
-                const float q = expf(to_float(src[id]) - base) * inv;
+                const float q = exp_below(to_float(src[id]) - base) * inv;
                 chosen = q * (lead * (float)__ldg(c + id) + back);
             }
 #pragma unroll
@@ -416,7 +472,8 @@ cudaError_t route_backward(const L *logits, const int32_t *ids, const float *w, 
 size_t balance_loss_ws_bytes(int S, int T, int E)
 {
     const int B = loss_ctas(S, T);
-    return 2 * align256((size_t)S * B * E * 4) + 2 * align256((size_t)S * B * 4);
+    return 2 * align256((size_t)S * B * E * 4) + 2 * align256((size_t)S * B * 4) +
+           align256((size_t)S * loss_blocks(E) * 4) + align256((size_t)S * 4) + 256;
 }
 
 cudaError_t launch_balance_loss(const void *logits, int type, const int32_t *ids,
@@ -433,8 +490,8 @@ cudaError_t launch_balance_loss(const void *logits, int type, const int32_t *ids
                                          dev_status, st);
     if (err != cudaSuccess) return err;
     MOE_TRACED_LAUNCH("k_balance_finish", st,
-        err = launch_pdl(k_balance_finish, dim3(1), dim3(1024), 0, st, w, S, B, E, k, counts,
-                         prob_mean, n_valid, losses));
+        err = launch_pdl(k_balance_finish, dim3(loss_blocks(E), S), dim3(kRlThreads), 0, st, w, S, B,
+                         E, k, counts, prob_mean, n_valid, losses));
     return err;
 }
 
