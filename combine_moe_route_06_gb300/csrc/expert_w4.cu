@@ -205,7 +205,15 @@ constexpr int kXStagesMax = 12;
 constexpr int kAColumns = kW4Chunk / 2;             // 64 columns a block
 constexpr int kAFirst = 2 * kMaxRowsTile;           // after two tiles of sums
 constexpr int kTmemColumns = kAFirst + kAStages * kAColumns;   // 512: all of it
+constexpr int64_t kPart = kMaxRowsTile * kW4Tile;   // partial sums of one part of a tile
+constexpr int kPartsAtOnce = 4;
+constexpr int kMinPart = 12;                        // chunks worth a part of their own
 constexpr int kGroupBytes = kW4Chunk / 64 * 1024;   // an 8-row group's chunk: 2 KiB
+
+// A barrier wait tells a phase from the one two before it only by the order of
+// events.  A team at chunk j has seen the MMAs of chunk j - 2 kAStages end, so a
+// weight stage must come round no sooner than that.
+static_assert(kWStages >= 2 * kAStages, "weight stages come round too soon for the teams' waits");
 
 struct MmShared {
     uint64_t w_full[kWStages], w_empty[kWStages];
@@ -276,6 +284,14 @@ __device__ __forceinline__ int owner(int total, int B, int g)
     return b;
 }
 
+// Parts of a tile that are in memory, and with them their sums.
+__device__ __forceinline__ int arrived(const int32_t *p)
+{
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
 // After a wait that gave up: waits (with a limit) for the copies in flight, whose
 // barriers are `full`; `next` is the stage to be filled next, in phase `phase`.
 __device__ __forceinline__ void drain(uint64_t *full, int stages, int next, uint32_t phase,
@@ -303,62 +319,55 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
     // The row counts are older than k_w4_rows, which has passed its own wait when
     // this kernel starts: they and the weights may be read before pdl_wait.
     pdl_trigger();
-    if (tid == 0) {
-        sh.most = 0;
-        sh.dead = 0;
-        for (int i = 0; i < kWStages; i++) {
-            mbar_init(&sh.w_full[i], 1);
-            mbar_init(&sh.w_empty[i], 4);
-        }
-        for (int i = 0; i < kXStagesMax; i++) {
-            mbar_init(&sh.x_full[i], 1);
-            mbar_init(&sh.x_empty[i], 1);
-        }
-        for (int i = 0; i < kAStages; i++) {
-            mbar_init(&sh.a_full[i], 4);
-            mbar_init(&sh.a_empty[i], 1);
-        }
-        for (int i = 0; i < 2; i++) {
-            mbar_init(&sh.sums_full[i], 1);
-            mbar_init(&sh.sums_empty[i], kEpilogueWarps);
-        }
-        mbar_init(&sh.done, 1);
-        mbar_init_fence();
-    }
-    if (warp == kWarpMma) tmem_alloc(&sh.tmem, kTmemColumns);
     bool bad = false;
     for (int e = tid; e < E; e += kMmThreads) {
         int start, count;
         expert_rows(offsets, counts, block_rows, a_rows, e, start, count, bad);
         sh.start[e] = start;
-        sh.count[e] = count;
+        sh.count[e] = offsets && offsets[e + 1] < offsets[e] ? -1 : count;
+    }
+    if (warp == kWarpMma) tmem_alloc(&sh.tmem, kTmemColumns);
+    if (warp == kWarpW) {
+        if (lane == 0) sh.dead = 0;
+        if (lane < kWStages) {
+            mbar_init(&sh.w_full[lane], 1);
+            mbar_init(&sh.w_empty[lane], 4);
+        }
+        if (lane < kXStagesMax) {
+            mbar_init(&sh.x_full[lane], 1);
+            mbar_init(&sh.x_empty[lane], 1);
+        }
+        if (lane < kAStages) {
+            mbar_init(&sh.a_full[lane], 4);
+            mbar_init(&sh.a_empty[lane], 1);
+        }
+        if (lane < 2) {
+            mbar_init(&sh.sums_full[lane], 1);
+            mbar_init(&sh.sums_empty[lane], kEpilogueWarps);
+        }
+        if (lane == 2) mbar_init(&sh.done, 1);
+        mbar_init_fence();
     }
     __syncthreads();
     if (warp == 0) {
-        // prefix sums of the experts' row tiles.  Ranges that overlap (offsets that
-        // fall) could hold more rows than there are: those past a_rows are dropped.
+        // prefix sums of the experts' row tiles.  Runs could only overlap where the
+        // offsets fall: from there on no expert has rows.
         int tiles_before = 0, most = 0;
-        int64_t rows_before = 0;
+        bool fell = false;
         for (int e0 = 0; e0 < E; e0 += 32) {
             const int e = e0 + lane;
-            int64_t rows = e < E ? sh.count[e] : 0;
-            const int count = (int)rows;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int64_t o = __shfl_up_sync(kFull, rows, off);
-                if (lane >= off) rows += o;
+            int count = e < E ? sh.count[e] : 0;
+            const unsigned falls = __ballot_sync(kFull, count < 0);
+            if (fell || (falls & (lanemask_lt() | 1u << lane))) {
+                count = 0;
+                if (e < E) sh.count[e] = 0;
             }
-            const bool drop = count > 0 && rows_before + rows > a_rows;
-            if (drop) {
-                sh.count[e] = 0;
-                bad = true;
-            }
-            const int n = drop ? 0 : tiles_of(count);
+            fell = fell || falls;
+            const int n = tiles_of(count);
             if (n > 0) most = max(most, rows_per_tile(count, n) / 8);
             const int inc = warp_inclusive_scan(n);
             if (e < E) sh.before[e] = tiles_before + inc - n;
             tiles_before += __shfl_sync(kFull, inc, 31);
-            rows_before += __shfl_sync(kFull, rows, 31);
         }
         most = __reduce_max_sync(kFull, most);
         if (lane == 0) {
@@ -372,14 +381,19 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
     tmem_fence_after();
 
     const uint32_t tmem = sh.tmem;
-    const int total = sh.before[E] * tiles * chunks;
-    // at least a chunk for every CTA that takes part, so each part of a cut tile arrives
-    const int B = min(total, (int)gridDim.x);
+    const int tasks = sh.before[E] * tiles, total = tasks * chunks;
+    // Every CTA takes part where that leaves it kMinPart chunks; else the tiles are
+    // cut into parts of at least that (short tiles not at all).
+    const int most_parts = max(1, chunks / kMinPart);
+    const int B = tasks <= (int)gridDim.x / most_parts ? tasks * most_parts : min(total, (int)gridDim.x);
     const bool idle = (int)blockIdx.x >= B;
     Walk walk{sh, idle ? 0 : cut(total, blockIdx.x, B), idle ? 0 : cut(total, blockIdx.x + 1, B), E,
               tiles, chunks};
-    const int x_stage_bytes = sh.most * kGroupBytes;
-    const int x_stages = min(kXStagesMax, kXBytes / max(1, x_stage_bytes));
+    // a stage of row operands holds up to four chunks, as many as leave three stages or more
+    const int tile_bytes = max(1, sh.most) * kGroupBytes;
+    const int x_chunks = kXBytes / tile_bytes >= 12 ? 4 : kXBytes / tile_bytes >= 6 ? 2 : 1;
+    const int x_stage_bytes = x_chunks * tile_bytes;
+    const int x_stages = min(kXStagesMax, kXBytes / x_stage_bytes);
     const bool runs = offsets != nullptr;
     volatile int *dead = &sh.dead;
     Segment g;
@@ -408,7 +422,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
         }
         if (!ok) drain(sh.w_full, kWStages, s, phase, issued);
     } else if (warp == kWarpX) {
-        // ---- row operands: one bulk copy per chunk
+        // ---- row operands: one bulk copy per chunk, one barrier per stage
         pdl_wait();
         const int64_t groups = row_groups(a_rows, E);
         int s = 0;
@@ -416,12 +430,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
         while (ok && walk.next(g)) {
             const int64_t group0 = row_group(runs, sh.start[g.e], block_rows, g.e) + g.row0 / 8;
             const uint32_t bytes = (g.rows + 7) / 8 * kGroupBytes;
-            for (int c = g.c0; c < g.c1; c++) {
+            for (int c = g.c0; c < g.c1; c += x_chunks) {
+                const int n = min(x_chunks, g.c1 - c);
                 if (!(ok = mbar_wait_warp(&sh.x_empty[s], phase ^ 1, dead))) break;
                 if (elect_lane()) {
-                    mbar_expect(&sh.x_full[s], bytes);
-                    bulk_load(xring + s * x_stage_bytes, x16 + (c * groups + group0) * kGroupBytes,
-                              bytes, &sh.x_full[s]);
+                    mbar_expect(&sh.x_full[s], n * bytes);
+                    for (int i = 0; i < n; i++)
+                        bulk_load(xring + s * x_stage_bytes + i * tile_bytes,
+                                  x16 + ((c + i) * groups + group0) * kGroupBytes, bytes,
+                                  &sh.x_full[s]);
                 }
                 __syncwarp();
                 issued |= 1u << s;
@@ -439,30 +456,33 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
         while (ok && walk.next(g)) {
             const uint32_t word = mma_f16_word((g.rows + 15) / 16 * 16);
             if (!(ok = mbar_wait_warp(&sh.sums_empty[d], pd ^ 1, dead))) break;
-            for (int c = g.c0; c < g.c1; c++) {
-                if (!(ok = mbar_wait_warp(&sh.x_full[sx], px, dead) &&
-                           mbar_wait_warp(&sh.a_full[sa], pa, dead)))
-                    break;
-                tmem_fence_after();
-                const uint32_t a = tmem + kAFirst + sa * kAColumns;
-                const uint64_t b = mma_smem_word(smem_addr(xring) + sx * x_stage_bytes, kGroupBytes);
-                if (elect_lane()) {
+            for (int cx = g.c0; ok && cx < g.c1; cx += x_chunks) {
+                if (!(ok = mbar_wait_warp(&sh.x_full[sx], px, dead))) break;
+                uint64_t b = mma_smem_word(smem_addr(xring) + sx * x_stage_bytes, kGroupBytes);
+                const int end = min(cx + x_chunks, g.c1);
+                for (int c = cx; c < end; c++, b += tile_bytes >> 4) {
+                    if (!(ok = mbar_wait_warp(&sh.a_full[sa], pa, dead))) break;
+                    tmem_fence_after();
+                    const uint32_t a = tmem + kAFirst + sa * kAColumns;
+                    if (elect_lane()) {
 #pragma unroll
-                    for (int i = 0; i < kW4Chunk / 16; i++)     // 32 bytes a step, 1 KiB an atom
-                        mma_f16(tmem + d * kMaxRowsTile, a + i * 8,
-                                b + (uint64_t)((i & 3) * 2 + (i >> 2) * 64), word, c > g.c0 || i > 0);
-                    mma_commit(&sh.a_empty[sa]);
-                    mma_commit(&sh.x_empty[sx]);
-                    if (c == g.c1 - 1) mma_commit(&sh.sums_full[d]);
+                        for (int i = 0; i < kW4Chunk / 16; i++)     // 32 bytes a step, 1 KiB an atom
+                            mma_f16(tmem + d * kMaxRowsTile, a + i * 8,
+                                    b + (uint64_t)((i & 3) * 2 + (i >> 2) * 64), word,
+                                    c > g.c0 || i > 0);
+                        mma_commit(&sh.a_empty[sa]);
+                        if (c == end - 1) mma_commit(&sh.x_empty[sx]);
+                        if (c == g.c1 - 1) mma_commit(&sh.sums_full[d]);
+                    }
+                    __syncwarp();
+                    if (++sa == kAStages) {
+                        sa = 0;
+                        pa ^= 1;
+                    }
                 }
-                __syncwarp();
                 if (++sx == x_stages) {
                     sx = 0;
                     px ^= 1;
-                }
-                if (++sa == kAStages) {
-                    sa = 0;
-                    pa ^= 1;
                 }
             }
             d ^= 1;
@@ -552,10 +572,13 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
             // one answer for the four warps, which meet at barriers below
             if (!named_all(1, kEpilogueWarps * 32, mbar_wait(&sh.sums_full[d], pd, dead))) break;
             tmem_fence_after();
-            bool finish = true;
-            if (parts > 1) {
-                float *slot =
-                    partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * (kMaxRowsTile * kW4Tile);
+            // a cut tile: its last part to be done is summed here with the others' from
+            // memory, any other part goes there
+            bool finish = true, held = true;       // held: this part's sums are in tensor memory only
+            if (parts > 1 &&
+                !(finish = named_all(1, kEpilogueWarps * 32, arrived(arrivals + first) == parts - 1))) {
+                held = false;
+                float *slot = partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * kPart;
                 for (int cb = 0; cb < blocks; cb++) {
                     float v[8];
                     tmem_load8(sums + cb * 8, v);
@@ -570,19 +593,32 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
                 __threadfence();
             }
             for (int cb = 0; finish && cb < blocks; cb++) {
-                float v[8];
+                float v[8], own[8];
+                if (held) tmem_load8(sums + cb * 8, own);
                 if (parts > 1) {
 #pragma unroll
                     for (int j = 0; j < 8; j++) v[j] = 0.f;
-                    for (int p = first; p < first + parts; p++) {
-                        // a part that starts the tile is its CTA's last, any other its first
-                        const float *slot = partial + (int64_t)(2 * p + (p == first)) *
-                                                          (kMaxRowsTile * kW4Tile);
+                    // a part that starts the tile is its CTA's last, any other its first
+                    const float *at = partial + (int64_t)2 * first * kPart + cb * 8 * kW4Tile + row;
+                    const int here = held ? (int)blockIdx.x - first : -1;
+                    for (int p = 0; p < parts; p += kPartsAtOnce) {
+                        float more[kPartsAtOnce][8];
 #pragma unroll
-                        for (int j = 0; j < 8; j++) v[j] += __ldcg(slot + (cb * 8 + j) * kW4Tile + row);
+                        for (int i = 0; i < kPartsAtOnce; i++)
+#pragma unroll
+                            for (int j = 0; j < 8; j++)
+                                more[i][j] = p + i < parts && p + i != here
+                                                 ? __ldcg(at + (2 * (p + i) + (p + i == 0)) * kPart +
+                                                          j * kW4Tile)
+                                                 : 0.f;
+#pragma unroll
+                        for (int i = 0; i < kPartsAtOnce; i++)
+#pragma unroll
+                            for (int j = 0; j < 8; j++) v[j] += p + i == here ? own[j] : more[i][j];
                     }
                 } else {
-                    tmem_load8(sums + cb * 8, v);
+#pragma unroll
+                    for (int j = 0; j < 8; j++) v[j] = own[j];
                 }
                 const float mine = cb < 4 ? scale[0] : cb < 8 ? scale[1] : cb < 12 ? scale[2] : scale[3];
 #pragma unroll
@@ -678,7 +714,8 @@ cudaError_t launch_expert_w4(const uint16_t *a, int a_rows, const int32_t *offse
     int32_t *arrivals = (int32_t *)((uint8_t *)partial + kPartialBytes);
     const int ctas = di.sm_count < kMaxCtas ? di.sm_count : kMaxCtas;
     const int fit = resident_grid((const void *)k_w4_rows, kRowsThreads, 0);
-    const int grid = fit > 0 && a_rows > fit ? fit : a_rows;
+    const int most = fit > 0 && fit < 6 * di.sm_count ? fit : 6 * di.sm_count;
+    const int grid = a_rows > most ? most : a_rows;
     MOE_TRACED_LAUNCH("k_w4_rows", st,
         err = launch_pdl(k_w4_rows, dim3(grid), dim3(kRowsThreads), 0, st, (const int4 *)a, a_rows,
                          offsets, counts, block_rows, E, K, x16, row_scale, arrivals, kMaxCtas));
