@@ -133,6 +133,14 @@ __global__ void __launch_bounds__(kRowsThreads) k_w4_rows(
     const int V = K / 8, padded = 16 * w4_chunks(K);
     const int64_t groups = row_groups(a_rows, E);
     for (int r = blockIdx.x; r < a_rows; r += gridDim.x) {
+        // the row's loads go out before its expert is looked up
+        const int4 *src = a + (int64_t)r * V;
+        int4 held[kRowsHeld];
+#pragma unroll
+        for (int h = 0; h < kRowsHeld; h++) {
+            const int v = tid + h * kRowsThreads;
+            held[h] = v < V ? src[v] : make_int4(0, 0, 0, 0);
+        }
         // the expert whose run or block holds row r
         int e;
         if (offsets) {
@@ -155,15 +163,9 @@ __global__ void __launch_bounds__(kRowsThreads) k_w4_rows(
         if (i < 0 || i >= count) continue;      // uniform per CTA
         const int64_t group = row_group(offsets != nullptr, start, block_rows, e) + (i >> 3);
         const int r8 = i & 7;
-        const int4 *src = a + (int64_t)r * V;
-        int4 held[kRowsHeld];
         uint32_t top = 0;
 #pragma unroll
-        for (int h = 0; h < kRowsHeld; h++) {
-            const int v = tid + h * kRowsThreads;
-            held[h] = v < V ? src[v] : make_int4(0, 0, 0, 0);
-            top = max(top, abs_max_bits(held[h]));
-        }
+        for (int h = 0; h < kRowsHeld; h++) top = max(top, abs_max_bits(held[h]));
         for (int v = tid + kRowsHeld * kRowsThreads; v < V; v += kRowsThreads)
             top = max(top, abs_max_bits(src[v]));
         top = __reduce_max_sync(kFull, top);
@@ -222,7 +224,7 @@ struct MmShared {
     uint64_t sums_full[2], sums_empty[2];
     int before[kMaxE + 1];           // row tiles of the experts before e
     int start[kMaxE], count[kMaxE];
-    float up[8][kW4Tile / 2];        // gated epilogue: up factors on their way to the gate's warps
+    float swap[2][16][kW4Tile / 2];  // gated epilogue: sums on their way to the other factor's warp
     uint64_t done;
     uint32_t tmem;
     int most;                        // largest row tile, in 8-row groups
@@ -235,7 +237,7 @@ constexpr size_t kMmSmem = 1024 + kXBytes + (size_t)kWStages * kW4BlockBytes + s
 __device__ __forceinline__ int tiles_of(int count) { return (count + kMaxRowsTile - 1) / kMaxRowsTile; }
 __device__ __forceinline__ int rows_per_tile(int count, int tiles)
 {
-    return ((count + tiles - 1) / tiles + 15) / 16 * 16;
+    return ((tiles == 1 ? count : (count + tiles - 1) / tiles) + 15) / 16 * 16;
 }
 
 struct Segment {
@@ -244,31 +246,56 @@ struct Segment {
     int task;
 };
 
-// The chunks [at, to) of this CTA, one tile after the other.
+// The last e < E with before[e] * tiles <= task, by a whole warp: two ballots over
+// at most 32 values each (E <= 1024).
+__device__ __forceinline__ int expert_of(const MmShared &sh, int E, int tiles, int task)
+{
+    const int lane = threadIdx.x & 31;
+    const int step = (E + 31) / 32;
+    const int at = lane * step;
+    const unsigned below = __ballot_sync(kFull, at < E && sh.before[at] * tiles <= task);
+    const int base = (31 - __clz((int)below)) * step;      // before[0] = 0: some bit is set
+    if (step == 1) return base;
+    const unsigned below2 =
+        __ballot_sync(kFull, lane < step && base + lane < E && sh.before[base + lane] * tiles <= task);
+    return base + 31 - __clz((int)below2);
+}
+
+// The chunks [at, to) of this CTA, one tile after the other; for whole warps.
 struct Walk {
     const MmShared &sh;
     int at, to;
     int E, tiles, chunks;
+    int task, c0;
+    __device__ Walk(const MmShared &s, int from, int end, int E_, int tiles_, int chunks_)
+        : sh(s), at(from), to(end), E(E_), tiles(tiles_), chunks(chunks_)
+    {
+        task = at / chunks;
+        c0 = at - task * chunks;
+    }
     __device__ bool next(Segment &g)
     {
         if (at >= to) return false;
-        g.task = at / chunks;
-        g.c0 = at - g.task * chunks;
-        g.c1 = min(chunks, g.c0 + to - at);
+        g.task = task;
+        g.c0 = c0;
+        g.c1 = min(chunks, c0 + to - at);
         at += g.c1 - g.c0;
-        int lo = 0, hi = E - 1;      // the last expert with before[e] * tiles <= task
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (sh.before[mid] * tiles <= g.task) lo = mid;
-            else hi = mid - 1;
+        task++;
+        c0 = 0;
+        g.e = expert_of(sh, E, tiles, g.task);
+        const int local = g.task - sh.before[g.e] * tiles;
+        const int nt = sh.before[g.e + 1] - sh.before[g.e];
+        const int count = sh.count[g.e];
+        if (nt == 1) {
+            g.tile = local;
+            g.row0 = 0;
+            g.rows = count;
+        } else {
+            const int per = rows_per_tile(count, nt);
+            g.tile = local / nt;
+            g.row0 = (local - g.tile * nt) * per;
+            g.rows = min(per, count - g.row0);
         }
-        g.e = lo;
-        const int local = g.task - sh.before[lo] * tiles;
-        const int nt = sh.before[lo + 1] - sh.before[lo];
-        g.tile = local / nt;
-        const int count = sh.count[lo], per = rows_per_tile(count, nt);
-        g.row0 = (local - g.tile * nt) * per;
-        g.rows = min(per, count - g.row0);
         return true;
     }
 };
@@ -300,6 +327,88 @@ __device__ __forceinline__ void drain(uint64_t *full, int stages, int next, uint
     for (int i = 0; i < stages; i++)
         for (int n = 0; (issued >> i & 1) && n < 100000; n++)
             if (mbar_try(&full[i], i < next ? phase : phase ^ 1)) break;
+}
+
+struct Finish {
+    uint32_t sums;             // the tile's sums in tensor memory, at this warp's lanes
+    const float *from;         // parts of a cut tile: at this thread's row of the first one
+    int parts, here;           // how many, and which of them is in tensor memory only (-1: none)
+    bool have;                 // two parts, eight columns of the other one are loaded already
+    float f;
+    int rows, row;             // rows of `a`; this thread's weight row in the tile
+    bool gated, store;
+    __nv_bfloat16 *dst;        // output of the tile's first row of `a`
+    int N;
+};
+
+// The outputs of a tile, COLS rows of `a` at a time.  The two factors of a gated
+// output are 64 lanes apart: the gate's warps finish the first half of the columns
+// and the up's the second, and each sends the other what it lacks.
+template <int COLS>
+__device__ __forceinline__ void finish_tile(const Finish &p, const float (&scale)[kMaxRowsTile / 32],
+                                            const float (&ahead)[8], MmShared &sh)
+{
+    for (int c0 = 0; c0 < p.rows; c0 += COLS) {
+        float v[COLS];
+        if (p.parts == 1 || p.here >= 0) tmem_load(p.sums + c0, v);
+        if (p.parts > 1) {
+#pragma unroll
+            for (int j0 = 0; j0 < COLS; j0 += 8) {
+                if (c0 + j0 >= p.rows) break;
+                float sum[8] = {};
+                if (p.have && c0 + j0 == 0) {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) sum[j] = 0.f + v[j] + ahead[j];
+                } else {
+                    // a part that starts the tile is its CTA's last, any other its first
+                    const float *at = p.from + (c0 + j0) * kW4Tile;
+                    for (int q = 0; q < p.parts; q += kPartsAtOnce) {
+                        float more[kPartsAtOnce][8];
+#pragma unroll
+                        for (int i = 0; i < kPartsAtOnce; i++)
+#pragma unroll
+                            for (int j = 0; j < 8; j++)
+                                more[i][j] =
+                                    q + i < p.parts && q + i != p.here
+                                        ? __ldcg(at + (2 * (q + i) + (q + i == 0)) * kPart + j * kW4Tile)
+                                        : 0.f;
+#pragma unroll
+                        for (int i = 0; i < kPartsAtOnce; i++)
+#pragma unroll
+                            for (int j = 0; j < 8; j++)
+                                sum[j] += q + i == p.here ? v[j0 + j] : more[i][j];
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; j++) v[j0 + j] = sum[j];
+            }
+        }
+        const float mine = c0 < 32 ? scale[0] : c0 < 64 ? scale[1] : c0 < 96 ? scale[2] : scale[3];
+#pragma unroll
+        for (int j = 0; j < COLS; j++) v[j] = v[j] * __shfl_sync(kFull, mine, (c0 + j) & 31) * p.f;
+        if (p.gated) {
+            const bool up = p.row >= kW4Tile / 2;
+            const int r = p.row % (kW4Tile / 2);
+            named_barrier(1, kEpilogueWarps * 32);          // the last columns' reads are over
+#pragma unroll
+            for (int j = 0; j < COLS / 2; j++) sh.swap[up][j][r] = up ? v[j] : v[COLS / 2 + j];
+            named_barrier(1, kEpilogueWarps * 32);
+#pragma unroll
+            for (int j = 0; j < COLS / 2; j++) {
+                const float other = sh.swap[!up][j][r];
+                const float gate = up ? other : v[j];
+                const float factor = up ? v[COLS / 2 + j] : other;
+                const int at = c0 + j + (up ? COLS / 2 : 0);
+                if (p.store && at < p.rows)
+                    p.dst[(int64_t)at * p.N] =
+                        __float2bfloat16_rn(__fdividef(gate, 1.f + __expf(-gate)) * factor);
+            }
+        } else if (p.store) {
+#pragma unroll
+            for (int j = 0; j < COLS; j++)
+                if (c0 + j < p.rows) p.dst[(int64_t)(c0 + j) * p.N] = __float2bfloat16_rn(v[j]);
+        }
+    }
 }
 
 __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
@@ -387,8 +496,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
     const int most_parts = max(1, chunks / kMinPart);
     const int B = tasks <= (int)gridDim.x / most_parts ? tasks * most_parts : min(total, (int)gridDim.x);
     const bool idle = (int)blockIdx.x >= B;
-    Walk walk{sh, idle ? 0 : cut(total, blockIdx.x, B), idle ? 0 : cut(total, blockIdx.x + 1, B), E,
-              tiles, chunks};
+    Walk walk(sh, idle ? 0 : cut(total, blockIdx.x, B), idle ? 0 : cut(total, blockIdx.x + 1, B), E,
+              tiles, chunks);
     // a stage of row operands holds up to four chunks, as many as leave three stages or more
     const int tile_bytes = max(1, sh.most) * kGroupBytes;
     const int x_chunks = kXBytes / tile_bytes >= 12 ? 4 : kXBytes / tile_bytes >= 6 ? 2 : 1;
@@ -568,6 +677,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
 #pragma unroll
             for (int i = 0; i < kMaxRowsTile / 32; i++)
                 scale[i] = lane + 32 * i < g.rows ? __ldcg(row_scale + scale0 + lane + 32 * i) : 0.f;
+            // where the other part of a tile cut in two is in memory already, its first block
+            const bool early = parts > 1 && arrived(arrivals + first) == parts - 1;
+            const int other = blockIdx.x == first ? first + 1 : first;
+            float ahead[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                ahead[j] = early && parts == 2
+                               ? __ldcg(partial + (2 * other + (other == first)) * kPart + j * kW4Tile + row)
+                               : 0.f;
             const uint32_t sums = tmem + ((uint32_t)(quarter * 32) << 16) + d * kMaxRowsTile;
             // one answer for the four warps, which meet at barriers below
             if (!named_all(1, kEpilogueWarps * 32, mbar_wait(&sh.sums_full[d], pd, dead))) break;
@@ -576,12 +694,13 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
             // memory, any other part goes there
             bool finish = true, held = true;       // held: this part's sums are in tensor memory only
             if (parts > 1 &&
-                !(finish = named_all(1, kEpilogueWarps * 32, arrived(arrivals + first) == parts - 1))) {
+                !(finish = named_all(1, kEpilogueWarps * 32,
+                                     early || arrived(arrivals + first) == parts - 1))) {
                 held = false;
                 float *slot = partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * kPart;
                 for (int cb = 0; cb < blocks; cb++) {
                     float v[8];
-                    tmem_load8(sums + cb * 8, v);
+                    tmem_load(sums + cb * 8, v);
 #pragma unroll
                     for (int j = 0; j < 8; j++) __stcg(slot + (cb * 8 + j) * kW4Tile + row, v[j]);
                 }
@@ -592,55 +711,11 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
                 finish = sh.last;
                 __threadfence();
             }
-            for (int cb = 0; finish && cb < blocks; cb++) {
-                float v[8], own[8];
-                if (held) tmem_load8(sums + cb * 8, own);
-                if (parts > 1) {
-#pragma unroll
-                    for (int j = 0; j < 8; j++) v[j] = 0.f;
-                    // a part that starts the tile is its CTA's last, any other its first
-                    const float *at = partial + (int64_t)2 * first * kPart + cb * 8 * kW4Tile + row;
-                    const int here = held ? (int)blockIdx.x - first : -1;
-                    for (int p = 0; p < parts; p += kPartsAtOnce) {
-                        float more[kPartsAtOnce][8];
-#pragma unroll
-                        for (int i = 0; i < kPartsAtOnce; i++)
-#pragma unroll
-                            for (int j = 0; j < 8; j++)
-                                more[i][j] = p + i < parts && p + i != here
-                                                 ? __ldcg(at + (2 * (p + i) + (p + i == 0)) * kPart +
-                                                          j * kW4Tile)
-                                                 : 0.f;
-#pragma unroll
-                        for (int i = 0; i < kPartsAtOnce; i++)
-#pragma unroll
-                            for (int j = 0; j < 8; j++) v[j] += p + i == here ? own[j] : more[i][j];
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; j++) v[j] = own[j];
-                }
-                const float mine = cb < 4 ? scale[0] : cb < 8 ? scale[1] : cb < 12 ? scale[2] : scale[3];
-#pragma unroll
-                for (int j = 0; j < 8; j++)
-                    v[j] = v[j] * __shfl_sync(kFull, mine, (cb & 3) * 8 + j) * f;
-                if (gated) {
-                    named_barrier(1, kEpilogueWarps * 32);      // the last block's reads are over
-                    if (row >= per)
-#pragma unroll
-                        for (int j = 0; j < 8; j++) sh.up[j][row - per] = v[j];
-                    named_barrier(1, kEpilogueWarps * 32);
-                    if (row < per)
-#pragma unroll
-                        for (int j = 0; j < 8; j++)
-                            v[j] = v[j] / (1.f + __expf(-v[j])) * sh.up[j][row];
-                }
-                if (row < per && n < N)
-#pragma unroll
-                    for (int j = 0; j < 8; j++)
-                        if (cb * 8 + j < g.rows)
-                            dst[(int64_t)(cb * 8 + j) * N] = __float2bfloat16_rn(v[j]);
-            }
+            const Finish fin{sums, partial + (int64_t)2 * first * kPart + row, parts,
+                             held ? (int)blockIdx.x - first : -1, early && parts == 2, f, g.rows,
+                             row, gated, n < N, dst, N};
+            if (finish && g.rows <= 8) finish_tile<8>(fin, scale, ahead, sh);
+            else if (finish) finish_tile<32>(fin, scale, ahead, sh);
             tmem_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.sums_empty[d]);
