@@ -840,9 +840,8 @@ def moe_expert_product_w4(a, w4, w_factor, y, ws, expert_offsets=None, masked_co
     lib = load_library()
     rows, K = a.shape
     N, E = y.shape[-1], w_factor.shape[0]
-    # the size of w4 in the layout: blocks of 9,216 bytes, 128 columns by 128 rows (gated: 64 outputs)
-    outputs = 64 if gated else 128
-    if w4.numel() < E * -(-N // outputs) * -(-K // 128) * 9216:
+    # the size of w4 in the layout: blocks of 9,216 bytes, 128 rows by 128 columns
+    if w4.numel() < E * -(-N // 128) * (2 if gated else 1) * -(-K // 128) * 9216:
         raise ValueError(f"w4: {w4.numel()} bytes are not the packed weights of E={E}, N={N}, K={K}, "
                          f"gated={gated}")
     _check(lib.moe_expert_product_w4(

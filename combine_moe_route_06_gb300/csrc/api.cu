@@ -1019,7 +1019,7 @@ static moe_status_t check_w4(const char *fn, int E, int N, int K, int gated)
     REQUIRE(K >= 16 && K % 16 == 0 && K <= (1 << 20),
             "%s: K=%d must be a multiple of 16 in [16, 2^20]", fn, K);
     REQUIRE(gated == 0 || gated == 1, "%s: gated=%d must be 0 or 1", fn, gated);
-    REQUIRE((int64_t)E * w4_tiles(N, gated) * w4_chunks(K) < ((int64_t)1 << 31),
+    REQUIRE((int64_t)E * w4_tiles(N, gated) * w4_chunks(K) * 2 < ((int64_t)1 << 31),
             "%s: E=%d experts of %d x %d weights are too many", fn, E, N, K);
     return MOE_OK;
 }
@@ -1076,7 +1076,7 @@ moe_status_t moe_expert_product_w4(const uint16_t *a, int a_rows, const int32_t 
         REQUIRE_ARR(expert_offsets, E + 1, 4);
     }
     // the chunks of the call are numbered in 32 bits
-    REQUIRE(((int64_t)a_rows / 128 + 1 + E) * w4_tiles(N, gated) * w4_chunks(K) < ((int64_t)1 << 31),
+    REQUIRE(((int64_t)a_rows / 128 + 1 + E) * w4_tiles(N, gated) * w4_chunks(K) * 2 < ((int64_t)1 << 31),
             "%s: a_rows=%d rows of K=%d by N=%d outputs are too many for one call", __func__, a_rows,
             K, N);
     REQUIRE_ARR(a, (int64_t)a_rows * K, 16);

@@ -40,18 +40,20 @@ __global__ void __launch_bounds__(kPackThreads) k_w4_pack(const uint8_t *__restr
 {
     pdl_wait();
     pdl_trigger();
-    const int tiles = w4_tiles(N, gated), chunks = w4_chunks(K);
-    const int64_t pieces = (int64_t)E * tiles * chunks * (kW4Tile * 4);
+    const int tiles = w4_tiles(N, gated), chunks = w4_chunks(K), blocks = w4_blocks(N, gated);
+    const int64_t pieces = (int64_t)E * tiles * chunks * blocks * (kW4Tile * 4);
     const int rows = gated ? 2 * N : N;
     for (int64_t at = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; at < pieces;
          at += (int64_t)gridDim.x * kPackThreads) {
         // the four pieces of a row are neighbours, so a warp reads whole 64-byte spans
         const int j = (int)(at & 3), i = (int)(at >> 2) & (kW4Tile - 1);
         const int64_t block = at / (kW4Tile * 4);
-        const int c = (int)(block % chunks);
-        const int t = (int)(block / chunks % tiles);
-        const int e = (int)(block / chunks / tiles);
-        const int n = w4_source_row(t, i, N, gated);
+        const int h = (int)(block % blocks);
+        const int c = (int)(block / blocks % chunks);
+        const int t = (int)(block / blocks / chunks % tiles);
+        const int e = (int)(block / blocks / chunks / tiles);
+        const int output = w4_output(t, h, i, N, gated);
+        const int n = output < N ? output + (gated && h ? N : 0) : -1;
         const int k0 = c * kW4Chunk + j * 32;
         uint2 q[2] = {make_uint2(0, 0), make_uint2(0, 0)};
         uint32_t s[2] = {0, 0};
@@ -205,10 +207,10 @@ constexpr int kWStages = 11;                        // 9 KiB weight blocks in fl
 constexpr int kXBytes = 96 * 1024;                  // ring of row operands
 constexpr int kXStagesMax = 12;
 constexpr int kAColumns = kW4Chunk / 2;             // 64 columns a block
-constexpr int kAFirst = 2 * kMaxRowsTile;           // after two tiles of sums
+constexpr int kAFirst = 2 * kMaxRowsTile;           // after the sums
 constexpr int kTmemColumns = kAFirst + kAStages * kAColumns;   // 512: all of it
-constexpr int64_t kPart = kMaxRowsTile * kW4Tile;   // partial sums of one part of a tile
-constexpr int kPartsAtOnce = 4;
+constexpr int64_t kPart = 2 * kMaxRowsTile * kW4Tile;   // partial sums of one part of a tile
+constexpr int kPartsAtOnce = 2;
 constexpr int kMinPart = 12;                        // chunks worth a part of their own
 constexpr int kGroupBytes = kW4Chunk / 64 * 1024;   // an 8-row group's chunk: 2 KiB
 
@@ -224,7 +226,6 @@ struct MmShared {
     uint64_t sums_full[2], sums_empty[2];
     int before[kMaxE + 1];           // row tiles of the experts before e
     int start[kMaxE], count[kMaxE];
-    float swap[2][16][kW4Tile / 2];  // gated epilogue: sums on their way to the other factor's warp
     uint64_t done;
     uint32_t tmem;
     int most;                        // largest row tile, in 8-row groups
@@ -329,85 +330,99 @@ __device__ __forceinline__ void drain(uint64_t *full, int stages, int next, uint
             if (mbar_try(&full[i], i < next ? phase : phase ^ 1)) break;
 }
 
+// One block times one chunk of rows: eight steps of 16 columns, 32 bytes apart in an
+// atom of the row operand, the atoms 1 KiB.
+__device__ __forceinline__ void mma_block(uint32_t sums, uint32_t a, uint64_t b, uint32_t word, bool add)
+{
+#pragma unroll
+    for (int i = 0; i < kW4Chunk / 16; i++)
+        mma_f16(sums, a + i * 8, b + (uint64_t)((i & 3) * 2 + (i >> 2) * 64), word, add || i > 0);
+}
+
 struct Finish {
     uint32_t sums;             // the tile's sums in tensor memory, at this warp's lanes
+    int second;                // columns from the first block's sums to the second's
     const float *from;         // parts of a cut tile: at this thread's row of the first one
     int parts, here;           // how many, and which of them is in tensor memory only (-1: none)
-    bool have;                 // two parts, eight columns of the other one are loaded already
+    bool have;                 // two parts, the first eight columns of the other are loaded already
     float f;
-    int rows, row;             // rows of `a`; this thread's weight row in the tile
-    bool gated, store;
-    __nv_bfloat16 *dst;        // output of the tile's first row of `a`
-    int N;
+    int rows;                  // rows of `a`
+    int team, teams;           // the teams that finish the tile take its rows of `a` in turn
 };
 
-// The outputs of a tile, COLS rows of `a` at a time.  The two factors of a gated
-// output are 64 lanes apart: the gate's warps finish the first half of the columns
-// and the up's the second, and each sends the other what it lacks.
-template <int COLS>
-__device__ __forceinline__ void finish_tile(const Finish &p, const float (&scale)[kMaxRowsTile / 32],
-                                            const float (&ahead)[8], MmShared &sh)
+// Sums of COLS rows of `a` from c0 on, block h, times the rows' scales and the
+// expert's factor; of a cut tile (CUT) over all of its parts in their order.
+template <int COLS, bool CUT>
+__device__ __forceinline__ void tile_sums(const Finish &p, int h, int c0,
+                                          const float (&scale)[kMaxRowsTile / 32],
+                                          const float (&ahead)[8], float (&v)[COLS])
 {
-    for (int c0 = 0; c0 < p.rows; c0 += COLS) {
-        float v[COLS];
-        if (p.parts == 1 || p.here >= 0) tmem_load(p.sums + c0, v);
-        if (p.parts > 1) {
+    if (!CUT || p.here >= 0) tmem_load(p.sums + h * p.second + c0, v);
+    if constexpr (CUT) {
+        if (p.have && c0 == 0) {
 #pragma unroll
-            for (int j0 = 0; j0 < COLS; j0 += 8) {
-                if (c0 + j0 >= p.rows) break;
-                float sum[8] = {};
-                if (p.have && c0 + j0 == 0) {
+            for (int j = 0; j < COLS; j++) v[j] = 0.f + v[j] + ahead[j];
+        } else {
+            float sum[COLS] = {};
+            // a part that starts the tile is its CTA's last, any other its first
+            const float *at = p.from + (h * kMaxRowsTile + c0) * kW4Tile;
+            for (int q = 0; q < p.parts; q += kPartsAtOnce) {
+                float more[kPartsAtOnce][COLS];
 #pragma unroll
-                    for (int j = 0; j < 8; j++) sum[j] = 0.f + v[j] + ahead[j];
-                } else {
-                    // a part that starts the tile is its CTA's last, any other its first
-                    const float *at = p.from + (c0 + j0) * kW4Tile;
-                    for (int q = 0; q < p.parts; q += kPartsAtOnce) {
-                        float more[kPartsAtOnce][8];
+                for (int i = 0; i < kPartsAtOnce; i++)
 #pragma unroll
-                        for (int i = 0; i < kPartsAtOnce; i++)
+                    for (int j = 0; j < COLS; j++)
+                        more[i][j] = q + i < p.parts && q + i != p.here
+                                         ? __ldcg(at + (2 * (q + i) + (q + i == 0)) * kPart + j * kW4Tile)
+                                         : 0.f;
 #pragma unroll
-                            for (int j = 0; j < 8; j++)
-                                more[i][j] =
-                                    q + i < p.parts && q + i != p.here
-                                        ? __ldcg(at + (2 * (q + i) + (q + i == 0)) * kPart + j * kW4Tile)
-                                        : 0.f;
+                for (int i = 0; i < kPartsAtOnce; i++)
 #pragma unroll
-                        for (int i = 0; i < kPartsAtOnce; i++)
-#pragma unroll
-                            for (int j = 0; j < 8; j++)
-                                sum[j] += q + i == p.here ? v[j0 + j] : more[i][j];
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 8; j++) v[j0 + j] = sum[j];
+                    for (int j = 0; j < COLS; j++) sum[j] += q + i == p.here ? v[j] : more[i][j];
             }
+#pragma unroll
+            for (int j = 0; j < COLS; j++) v[j] = sum[j];
         }
-        const float mine = c0 < 32 ? scale[0] : c0 < 64 ? scale[1] : c0 < 96 ? scale[2] : scale[3];
+    }
+    const float mine = c0 < 32 ? scale[0] : c0 < 64 ? scale[1] : c0 < 96 ? scale[2] : scale[3];
 #pragma unroll
-        for (int j = 0; j < COLS; j++) v[j] = v[j] * __shfl_sync(kFull, mine, (c0 + j) & 31) * p.f;
-        if (p.gated) {
-            const bool up = p.row >= kW4Tile / 2;
-            const int r = p.row % (kW4Tile / 2);
-            named_barrier(1, kEpilogueWarps * 32);          // the last columns' reads are over
-#pragma unroll
-            for (int j = 0; j < COLS / 2; j++) sh.swap[up][j][r] = up ? v[j] : v[COLS / 2 + j];
-            named_barrier(1, kEpilogueWarps * 32);
-#pragma unroll
-            for (int j = 0; j < COLS / 2; j++) {
-                const float other = sh.swap[!up][j][r];
-                const float gate = up ? other : v[j];
-                const float factor = up ? v[COLS / 2 + j] : other;
-                const int at = c0 + j + (up ? COLS / 2 : 0);
-                if (p.store && at < p.rows)
-                    p.dst[(int64_t)at * p.N] =
-                        __float2bfloat16_rn(__fdividef(gate, 1.f + __expf(-gate)) * factor);
-            }
-        } else if (p.store) {
+    for (int j = 0; j < COLS; j++) v[j] = v[j] * __shfl_sync(kFull, mine, (c0 + j) & 31) * p.f;
+}
+
+// Outputs of this thread's weight row(s), COLS rows of `a` at a time.  dst: the
+// output of the tile's first row of `a`; `store`: not padding.
+template <int COLS, bool CUT>
+__device__ __forceinline__ void finish_gated(const Finish &p, const float (&scale)[kMaxRowsTile / 32],
+                                             const float (&ahead)[2][8], __nv_bfloat16 *dst, int N,
+                                             bool store)
+{
+#pragma unroll 1
+    for (int c0 = p.team * COLS; c0 < p.rows; c0 += p.teams * COLS) {
+        float gate[COLS], up[COLS];
+        tile_sums<COLS, CUT>(p, 0, c0, scale, ahead[0], gate);
+        tile_sums<COLS, CUT>(p, 1, c0, scale, ahead[1], up);
+        if (store)
 #pragma unroll
             for (int j = 0; j < COLS; j++)
-                if (c0 + j < p.rows) p.dst[(int64_t)(c0 + j) * p.N] = __float2bfloat16_rn(v[j]);
-        }
+                if (c0 + j < p.rows)
+                    dst[(int64_t)(c0 + j) * N] =
+                        __float2bfloat16_rn(__fdividef(gate[j], 1.f + __expf(-gate[j])) * up[j]);
+    }
+}
+template <int COLS, bool CUT>
+__device__ __forceinline__ void finish_plain(const Finish &p, int h,
+                                             const float (&scale)[kMaxRowsTile / 32],
+                                             const float (&ahead)[8], __nv_bfloat16 *dst, int N,
+                                             bool store)
+{
+#pragma unroll 1
+    for (int c0 = p.team * COLS; c0 < p.rows; c0 += p.teams * COLS) {
+        float v[COLS];
+        tile_sums<COLS, CUT>(p, h, c0, scale, ahead, v);
+        if (store)
+#pragma unroll
+            for (int j = 0; j < COLS; j++)
+                if (c0 + j < p.rows) dst[(int64_t)(c0 + j) * N] = __float2bfloat16_rn(v[j]);
     }
 }
 
@@ -423,7 +438,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
     MmShared &sh = *(MmShared *)(wring + kWStages * kW4BlockBytes);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kFull, tid >> 5, 0);
-    const int tiles = w4_tiles(N, gated), chunks = w4_chunks(K);
+    const int tiles = w4_tiles(N, gated), chunks = w4_chunks(K), blocks = w4_blocks(N, gated);
 
     // The row counts are older than k_w4_rows, which has passed its own wait when
     // this kernel starts: they and the weights may be read before pdl_wait.
@@ -450,10 +465,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
             mbar_init(&sh.a_full[lane], 4);
             mbar_init(&sh.a_empty[lane], 1);
         }
-        if (lane < 2) {
-            mbar_init(&sh.sums_full[lane], 1);
-            mbar_init(&sh.sums_empty[lane], kEpilogueWarps);
-        }
+        if (lane < 2) mbar_init(&sh.sums_full[lane], 1);
         if (lane == 2) mbar_init(&sh.done, 1);
         mbar_init_fence();
     }
@@ -482,6 +494,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
         if (lane == 0) {
             sh.before[E] = tiles_before;
             sh.most = most;
+            const int warps = blocks == 2 && most > 8 ? kDecodeWarps : kEpilogueWarps;
+            mbar_init(&sh.sums_empty[0], warps);
+            mbar_init(&sh.sums_empty[1], warps);
+            mbar_init_fence();
         }
     }
     if (bad && blockIdx.x == 0) flag_status(dev_status, MOE_ERR_INVALID_ARG);
@@ -503,6 +519,13 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
     const int x_chunks = kXBytes / tile_bytes >= 12 ? 4 : kXBytes / tile_bytes >= 6 ? 2 : 1;
     const int x_stage_bytes = x_chunks * tile_bytes;
     const int x_stages = min(kXStagesMax, kXBytes / x_stage_bytes);
+    // sums: two tiles of 128 columns in turn, the blocks' 64 columns apart in them, which
+    // the epilogue warps finish while the next tile is summed; two blocks with more than
+    // 64 rows of `a` take all 256 columns, and the decode warps, which then have nothing
+    // to decode into, finish the tile (16 warps take a quarter of the time of four)
+    const bool large = blocks == 2 && sh.most > 8;
+    const int sums_stages = large ? 1 : 2;
+    const int second = large ? kMaxRowsTile : kMaxRowsTile / 2;
     const bool runs = offsets != nullptr;
     volatile int *dead = &sh.dead;
     Segment g;
@@ -514,8 +537,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
         uint32_t phase = 0, issued = 0;
         while (ok && walk.next(g)) {
             const uint8_t *src =
-                w4 + (((int64_t)g.e * tiles + g.tile) * chunks + g.c0) * (int64_t)kW4BlockBytes;
-            for (int c = g.c0; c < g.c1; c++, src += kW4BlockBytes) {
+                w4 + (((int64_t)g.e * tiles + g.tile) * chunks + g.c0) * blocks * (int64_t)kW4BlockBytes;
+            for (int i = 0; i < (g.c1 - g.c0) * blocks; i++, src += kW4BlockBytes) {
                 if (!(ok = mbar_wait_warp(&sh.w_empty[s], phase ^ 1, dead))) break;
                 if (elect_lane()) {
                     mbar_expect(&sh.w_full[s], kW4BlockBytes);
@@ -559,7 +582,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
         }
         if (!ok) drain(sh.x_full, x_stages, s, phase, issued);
     } else if (warp == kWarpMma) {
-        // ---- MMA: eight steps of 16 columns per chunk, into the two tiles of sums in turn
+        // ---- MMA
         int sx = 0, sa = 0, d = 0;
         uint32_t px = 0, pa = 0, pd = 0;
         while (ok && walk.next(g)) {
@@ -570,21 +593,24 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
                 uint64_t b = mma_smem_word(smem_addr(xring) + sx * x_stage_bytes, kGroupBytes);
                 const int end = min(cx + x_chunks, g.c1);
                 for (int c = cx; c < end; c++, b += tile_bytes >> 4) {
-                    if (!(ok = mbar_wait_warp(&sh.a_full[sa], pa, dead))) break;
-                    tmem_fence_after();
+                    const uint32_t sums = tmem + d * kMaxRowsTile;
                     const uint32_t a = tmem + kAFirst + sa * kAColumns;
+                    if (!(ok = mbar_wait_warp(&sh.a_full[sa], pa, dead))) break;
+                    if (blocks == 2 && !(ok = mbar_wait_warp(&sh.a_full[sa + 1], pa, dead))) break;
+                    tmem_fence_after();
                     if (elect_lane()) {
-#pragma unroll
-                        for (int i = 0; i < kW4Chunk / 16; i++)     // 32 bytes a step, 1 KiB an atom
-                            mma_f16(tmem + d * kMaxRowsTile, a + i * 8,
-                                    b + (uint64_t)((i & 3) * 2 + (i >> 2) * 64), word,
-                                    c > g.c0 || i > 0);
+                        mma_block(sums, a, b, word, c > g.c0);
                         mma_commit(&sh.a_empty[sa]);
+                        if (blocks == 2) {
+                            mma_block(sums + second, a + kAColumns, b, word, c > g.c0);
+                            mma_commit(&sh.a_empty[sa + 1]);
+                        }
                         if (c == end - 1) mma_commit(&sh.x_empty[sx]);
                         if (c == g.c1 - 1) mma_commit(&sh.sums_full[d]);
                     }
                     __syncwarp();
-                    if (++sa == kAStages) {
+                    sa += blocks;
+                    if (sa == kAStages) {
                         sa = 0;
                         pa ^= 1;
                     }
@@ -594,80 +620,82 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
                     px ^= 1;
                 }
             }
-            d ^= 1;
-            if (d == 0) pd ^= 1;
+            if (++d == sums_stages) {
+                d = 0;
+                pd ^= 1;
+            }
         }
         // the MMAs in flight end before their memory goes
         if (elect_lane()) mma_commit(&sh.done);
         __syncwarp();
         for (int n = 0; n < 100000 && !mbar_try(&sh.done, 0); n++) {}
-    } else if (warp < kDecodeWarps) {
-        // ---- decode: team t of four warps (one per quarter of the tensor-memory lanes, a row
-        // a lane) has every kAStages-th chunk and A stage t
-        const int quarter = warp & 3, team = warp >> 2;
-        const int row = quarter * 32 + lane;
-        const uint32_t a_at =
-            tmem + ((uint32_t)(quarter * 32) << 16) + kAFirst + team * kAColumns;
-        int sw = team;               // stage of the team's next chunk
-        uint32_t pw = 0, pa = 0;
-        for (int c = walk.at + team; c < walk.to; c += kAStages) {
-            if (!mbar_wait_warp(&sh.w_full[sw], pw, dead)) break;
-            const uint8_t *block = wring + sw * kW4BlockBytes;
-            uint4 q[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) q[j] = *(const uint4 *)(block + (j * kW4Tile + row) * 16);
-            const uint2 sc = *(const uint2 *)(block + kW4CodeBytes + row * 8);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.w_empty[sw]);
-            sw += kAStages;
-            if (sw >= kWStages) {
-                sw -= kWStages;
-                pw ^= 1;
-            }
-            if (!mbar_wait_warp(&sh.a_empty[team], pa ^ 1, dead)) break;
-            pa ^= 1;
-            tmem_fence_after();
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const uint32_t s4 = h ? sc.y : sc.x;
-                const uint32_t s01 = e4m3x2_to_half2(s4), s23 = e4m3x2_to_half2(s4 >> 16);
-                const uint32_t group_scale[4] = {
-                    __byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232),
-                    __byte_perm(s23, 0, 0x1010), __byte_perm(s23, 0, 0x3232)};
-                const uint32_t word[8] = {q[2 * h].x,     q[2 * h].y,     q[2 * h].z,
-                                          q[2 * h].w,     q[2 * h + 1].x, q[2 * h + 1].y,
-                                          q[2 * h + 1].z, q[2 * h + 1].w};
-                uint32_t out[32];
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    uint32_t half2s[4];
-                    e2m1x8_to_half2(word[i], half2s);
-#pragma unroll
-                    for (int p = 0; p < 4; p++)
-                        out[4 * i + p] = mul_half2(half2s[p], group_scale[i >> 1]);
-                }
-                tmem_store32(a_at + h * 32, out);
-            }
-            tmem_wait_st();
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.a_full[team]);
-        }
     } else {
-        // ---- epilogue: a thread has one weight row, eight rows of `a` at a time
-        const int quarter = warp & 3;
+        // ---- decode: team t of four warps (one per quarter of the tensor-memory lanes, a row
+        // a lane) has every kAStages-th block and A stage t.  Epilogue: a thread has one row
+        // of each of the tile's blocks.
+        const bool decodes = warp < kDecodeWarps, finishes = large ? decodes : !decodes;
+        const int quarter = warp & 3, team = decodes ? warp >> 2 : 0;
+        const int finishers = large ? kDecodeWarps * 32 : kEpilogueWarps * 32;
         const int row = quarter * 32 + lane;
-        const int per = w4_outputs_per_tile(gated);
+        const uint32_t at_lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t a_at = at_lanes + kAFirst + team * kAColumns;
+        int sw = team;               // stage of the team's next block
+        uint32_t pw = 0, pa = 0;
+        int mine = team, seen = 0;   // that block's number; blocks of the segments so far
         int d = 0;
         uint32_t pd = 0;
-        pdl_wait();
-        while (walk.next(g)) {
+        if (!decodes) pdl_wait();
+        while (ok && walk.next(g)) {
+            seen += (g.c1 - g.c0) * blocks;
+            for (; decodes && mine < seen; mine += kAStages) {
+                if (!(ok = mbar_wait_warp(&sh.w_full[sw], pw, dead))) break;
+                const uint8_t *block = wring + sw * kW4BlockBytes;
+                uint4 q[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++) q[j] = *(const uint4 *)(block + (j * kW4Tile + row) * 16);
+                const uint2 sc = *(const uint2 *)(block + kW4CodeBytes + row * 8);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.w_empty[sw]);
+                sw += kAStages;
+                if (sw >= kWStages) {
+                    sw -= kWStages;
+                    pw ^= 1;
+                }
+                if (!(ok = mbar_wait_warp(&sh.a_empty[team], pa ^ 1, dead))) break;
+                pa ^= 1;
+                tmem_fence_after();
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const uint32_t s4 = h ? sc.y : sc.x;
+                    const uint32_t s01 = e4m3x2_to_half2(s4), s23 = e4m3x2_to_half2(s4 >> 16);
+                    const uint32_t group_scale[4] = {
+                        __byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232),
+                        __byte_perm(s23, 0, 0x1010), __byte_perm(s23, 0, 0x3232)};
+                    const uint32_t word[8] = {q[2 * h].x,     q[2 * h].y,     q[2 * h].z,
+                                              q[2 * h].w,     q[2 * h + 1].x, q[2 * h + 1].y,
+                                              q[2 * h + 1].z, q[2 * h + 1].w};
+                    uint32_t out[32];
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        uint32_t half2s[4];
+                        e2m1x8_to_half2(word[i], half2s);
+#pragma unroll
+                        for (int p = 0; p < 4; p++)
+                            out[4 * i + p] = mul_half2(half2s[p], group_scale[i >> 1]);
+                    }
+                    tmem_store32(a_at + h * 32, out);
+                }
+                tmem_wait_st();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.a_full[team]);
+            }
+            if (!finishes) continue;
+            if (decodes) pdl_wait();
             const float f = __ldg(factor + g.e);
             const int64_t scale0 =
                 (int64_t)row_group(runs, sh.start[g.e], block_rows, g.e) * 8 + g.row0;
-            const int n = g.tile * per + row % per;
-            __nv_bfloat16 *dst = y + (int64_t)(sh.start[g.e] + g.row0) * N + n;
-            const int blocks = (g.rows + 7) / 8;
+            __nv_bfloat16 *out = y + (int64_t)(sh.start[g.e] + g.row0) * N;
             int first = 0, parts = 1;
             if (g.c1 - g.c0 < chunks) {
                 first = owner(total, B, g.task * chunks);
@@ -680,47 +708,71 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
             // where the other part of a tile cut in two is in memory already, its first block
             const bool early = parts > 1 && arrived(arrivals + first) == parts - 1;
             const int other = blockIdx.x == first ? first + 1 : first;
-            float ahead[8];
+            float ahead[2][8];
 #pragma unroll
-            for (int j = 0; j < 8; j++)
-                ahead[j] = early && parts == 2
-                               ? __ldcg(partial + (2 * other + (other == first)) * kPart + j * kW4Tile + row)
-                               : 0.f;
-            const uint32_t sums = tmem + ((uint32_t)(quarter * 32) << 16) + d * kMaxRowsTile;
-            // one answer for the four warps, which meet at barriers below
-            if (!named_all(1, kEpilogueWarps * 32, mbar_wait(&sh.sums_full[d], pd, dead))) break;
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    ahead[h][j] = early && parts == 2 && h < blocks
+                                      ? __ldcg(partial + (2 * other + (other == first)) * kPart +
+                                               (h * kMaxRowsTile + j) * kW4Tile + row)
+                                      : 0.f;
+            const uint32_t sums = at_lanes + d * kMaxRowsTile;
+            // one answer for all the warps, which meet at barriers below
+            if (!(ok = named_all(1, finishers, ok && mbar_wait(&sh.sums_full[d], pd, dead)))) break;
             tmem_fence_after();
             // a cut tile: its last part to be done is summed here with the others' from
             // memory, any other part goes there
             bool finish = true, held = true;       // held: this part's sums are in tensor memory only
             if (parts > 1 &&
-                !(finish = named_all(1, kEpilogueWarps * 32,
+                !(finish = named_all(1, finishers,
                                      early || arrived(arrivals + first) == parts - 1))) {
                 held = false;
                 float *slot = partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * kPart;
-                for (int cb = 0; cb < blocks; cb++) {
-                    float v[8];
-                    tmem_load(sums + cb * 8, v);
+                for (int h = 0; h < blocks; h++)
+                    for (int c0 = team * 8; c0 < g.rows; c0 += finishers / 128 * 8) {
+                        float v[8];
+                        tmem_load(sums + h * second + c0, v);
 #pragma unroll
-                    for (int j = 0; j < 8; j++) __stcg(slot + (cb * 8 + j) * kW4Tile + row, v[j]);
-                }
+                        for (int j = 0; j < 8; j++)
+                            __stcg(slot + (h * kMaxRowsTile + c0 + j) * kW4Tile + row, v[j]);
+                    }
                 __threadfence();
-                named_barrier(1, kEpilogueWarps * 32);
-                if (quarter == 0 && lane == 0) sh.last = atomicAdd(arrivals + first, 1) == parts - 1;
-                named_barrier(1, kEpilogueWarps * 32);
+                named_barrier(1, finishers);
+                if (team == 0 && quarter == 0 && lane == 0)
+                    sh.last = atomicAdd(arrivals + first, 1) == parts - 1;
+                named_barrier(1, finishers);
                 finish = sh.last;
                 __threadfence();
             }
-            const Finish fin{sums, partial + (int64_t)2 * first * kPart + row, parts,
-                             held ? (int)blockIdx.x - first : -1, early && parts == 2, f, g.rows,
-                             row, gated, n < N, dst, N};
-            if (finish && g.rows <= 8) finish_tile<8>(fin, scale, ahead, sh);
-            else if (finish) finish_tile<32>(fin, scale, ahead, sh);
+            if (finish) {
+                const Finish fin{sums, second, partial + (int64_t)2 * first * kPart + row, parts,
+                                 held ? (int)blockIdx.x - first : -1, early && parts == 2, f, g.rows,
+                                 team, finishers / 128};
+                if (gated) {
+                    const int n = w4_output(g.tile, 0, row, N, true);
+                    if (parts > 1) finish_gated<8, true>(fin, scale, ahead, out + n, N, n < N);
+                    else if (g.rows <= 8) finish_gated<8, false>(fin, scale, ahead, out + n, N, n < N);
+                    else finish_gated<16, false>(fin, scale, ahead, out + n, N, n < N);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        if (h == blocks) break;
+                        const int n = w4_output(g.tile, h, row, N, false);
+                        if (parts > 1) finish_plain<8, true>(fin, h, scale, ahead[h], out + n, N, n < N);
+                        else if (g.rows <= 8)
+                            finish_plain<8, false>(fin, h, scale, ahead[h], out + n, N, n < N);
+                        else finish_plain<16, false>(fin, h, scale, ahead[h], out + n, N, n < N);
+                    }
+                }
+            }
             tmem_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.sums_empty[d]);
-            d ^= 1;
-            if (d == 0) pd ^= 1;
+            if (++d == sums_stages) {
+                d = 0;
+                pd ^= 1;
+            }
         }
     }
     __syncthreads();
@@ -735,13 +787,13 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
 
 size_t w4_bytes(int E, int N, int K, bool gated)
 {
-    return (size_t)E * w4_tiles(N, gated) * w4_chunks(K) * kW4BlockBytes;
+    return (size_t)E * w4_tiles(N, gated) * w4_chunks(K) * w4_blocks(N, gated) * kW4BlockBytes;
 }
 
 cudaError_t launch_w4_pack(const uint8_t *codes, const uint8_t *scales, int E, int N, int K,
                            bool gated, uint8_t *w4, cudaStream_t st)
 {
-    const int64_t pieces = (int64_t)E * w4_tiles(N, gated) * w4_chunks(K) * (kW4Tile * 4);
+    const int64_t pieces = (int64_t)(w4_bytes(E, N, K, gated) / kW4BlockBytes) * (kW4Tile * 4);
     const int64_t want = (pieces + kPackThreads - 1) / kPackThreads;
     const int64_t fit = resident_grid((const void *)k_w4_pack, kPackThreads, 0);
     const int64_t grid = fit > 0 && want > fit ? fit : want;
@@ -756,14 +808,14 @@ namespace {
 
 // Workspace of one call: the rows in operand form, their scales, the partial
 // sums of cut tiles (two a CTA) and the arrival counters (one a CTA).
-constexpr int kMaxCtas = 256;
+constexpr int kMaxCtas = 160;
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 size_t x16_bytes(int a_rows, int E, int K)
 {
     return align256((size_t)row_groups(a_rows, E) * w4_chunks(K) * kGroupBytes);
 }
 size_t scale_bytes(int a_rows, int E) { return align256((size_t)row_groups(a_rows, E) * 8 * 4); }
-constexpr size_t kPartialBytes = (size_t)2 * kMaxCtas * kMaxRowsTile * kW4Tile * 4;
+constexpr size_t kPartialBytes = (size_t)2 * kMaxCtas * kPart * 4;
 
 }  // namespace
 

@@ -117,28 +117,25 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&v)[
         "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
 }
-// 8 or 32 columns of the warp's 32 lanes, ready for use.
+// 8 or 16 columns of the warp's 32 lanes, ready for use.
 template <int COLS>
 __device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[COLS])
 {
-    if constexpr (COLS == 32) {
-        uint32_t r[32];
+    if constexpr (COLS == 16) {
+        uint32_t r[16];
         asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-            "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
             "tcgen05.wait::ld.sync.aligned;"
             : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
               "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-              "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-              "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-              "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+              "=r"(r[14]), "=r"(r[15])
             : "r"(addr)
             : "memory");
 #pragma unroll
-        for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
+        for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
     } else {
-        static_assert(COLS == 8, "8 or 32 columns");
+        static_assert(COLS == 8, "8 or 16 columns");
         uint32_t r[8];
         asm volatile(
             "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"

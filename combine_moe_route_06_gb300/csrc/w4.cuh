@@ -5,15 +5,17 @@
 // [2^-10, 2688] or is 0, so it is exact in fp16 (and normal there).
 //
 // Packed form: blocks of 128 rows x 128 columns, 9,216 bytes each, so a block
-// is one bulk copy and any row count or K is padded with zero codes:
-//   block (expert e, row tile t, column chunk c) at ((e*tiles + t)*chunks + c) * 9216
+// is one bulk copy and any row count or K is padded with zero codes.  A tile is
+// one or two blocks of rows that share their columns of the other operand:
+//   gated weights [gate; up]: 128 gate rows and the same 128 up rows, so that the
+//     two factors of an output meet in one lane;
+//   else two row blocks where their number is even, one where it is odd.
+//   block h (expert e, tile t, column chunk c) at
+//     (((e*tiles + t)*chunks + c)*blocks + h) * 9216
 //   codes : [4][128 rows][16 bytes], piece j of a row = its columns 128c+32j .. +31,
 //           first value of a byte in the low nibble
 //   scales: [128 rows][8 bytes] from byte 8192 on
-// Lanes that own consecutive rows read consecutive 16-byte pieces of shared
-// memory.  A tile holds rows 128t .. 128t+127 of the weight, or of a gated
-// weight [gate; up] the 64 gate rows 64t .. 64t+63 and then the same 64 up rows,
-// so one tile has both factors of 64 outputs.
+// Lanes that own consecutive rows read consecutive 16-byte pieces of shared memory.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -27,23 +29,25 @@ constexpr int kW4Chunk = 128;                                  // columns of a b
 constexpr int kW4CodeBytes = kW4Tile * kW4Chunk / 2;           // 8192
 constexpr int kW4BlockBytes = kW4CodeBytes + kW4Tile * kW4Chunk / 16;   // 9216
 
-__host__ __device__ __forceinline__ int w4_outputs_per_tile(bool gated)
+// Row blocks per tile, outputs per tile, tiles and column chunks of a weight.
+__host__ __device__ __forceinline__ int w4_blocks(int N, bool gated)
 {
-    return gated ? kW4Tile / 2 : kW4Tile;
+    return gated || (N + kW4Tile - 1) / kW4Tile % 2 == 0 ? 2 : 1;
+}
+__host__ __device__ __forceinline__ int w4_outputs(int N, bool gated)
+{
+    return gated ? kW4Tile : kW4Tile * w4_blocks(N, gated);
 }
 __host__ __device__ __forceinline__ int w4_tiles(int N, bool gated)
 {
-    const int per = w4_outputs_per_tile(gated);
-    return (N + per - 1) / per;
+    return (N + w4_outputs(N, gated) - 1) / w4_outputs(N, gated);
 }
 __host__ __device__ __forceinline__ int w4_chunks(int K) { return (K + kW4Chunk - 1) / kW4Chunk; }
 
-// Row of the weight [N or 2N] that row i of tile t holds, or -1 for padding.
-__host__ __device__ __forceinline__ int w4_source_row(int t, int i, int N, bool gated)
+// Output that row i of block h of tile t belongs to (N or more: padding).
+__host__ __device__ __forceinline__ int w4_output(int t, int h, int i, int N, bool gated)
 {
-    const int per = w4_outputs_per_tile(gated);
-    const int n = t * per + i % per;
-    return n < N ? (i < per ? n : N + n) : -1;
+    return gated ? t * kW4Tile + i : (t * w4_blocks(N, gated) + h) * kW4Tile + i;
 }
 
 // Eight codes (one 32-bit word, first value in the low nibble) to fp16 pairs.

@@ -724,8 +724,7 @@ moe_status_t moe_expert_scale_nvfp4(const uint8_t *recv_q, const int32_t *expert
  *   scales  [E][rows][K/16] uint8 (E4M3) in.
  *           rows = N, or 2N for gated weights: the N gate rows, then the N up rows.
  *   w4      moe_w4_bytes(E, N, K, gated) bytes out, 16-byte aligned: 9/16 byte a
- *           weight, N and K rounded up to the 128 x 128 blocks of the layout
- *           (64 outputs by 128 columns for gated weights).
+ *           weight, N and K rounded up to multiples of 128.
  * N a multiple of 8, K a multiple of 16, 1 <= E <= 1024.
  */
 size_t moe_w4_bytes(int E, int N, int K, int gated);
