@@ -210,7 +210,6 @@ constexpr int kAColumns = kW4Chunk / 2;             // 64 columns a block
 constexpr int kAFirst = 2 * kMaxRowsTile;           // after the sums
 constexpr int kTmemColumns = kAFirst + kAStages * kAColumns;   // 512: all of it
 constexpr int64_t kPart = 2 * kMaxRowsTile * kW4Tile;   // partial sums of one part of a tile
-constexpr int kPartsAtOnce = 2;
 constexpr int kMinPart = 12;                        // chunks worth a part of their own
 constexpr int kGroupBytes = kW4Chunk / 64 * 1024;   // an 8-row group's chunk: 2 KiB
 
@@ -301,16 +300,17 @@ struct Walk {
     }
 };
 
-// First chunk of CTA b of B when `total` chunks are cut evenly.
-__device__ __forceinline__ int cut(int total, int b, int B) { return (int)((int64_t)total * b / B); }
-// The CTA whose part holds chunk g.
-__device__ __forceinline__ int owner(int total, int B, int g)
-{
-    int b = (int)((int64_t)g * B / total);
-    while (cut(total, b + 1, B) <= g) b++;
-    while (cut(total, b, B) > g) b--;
-    return b;
-}
+// `total` chunks cut into B parts: the first `more` have base + 1 of them, the rest base.
+struct Cut {
+    int base, more;
+    __device__ Cut(int total, int B) : base(B ? total / B : 0), more(B ? total - base * B : 0) {}
+    __device__ int start(int b) const { return b * base + min(b, more); }
+    __device__ int owner(int g) const       // the part that holds chunk g
+    {
+        const int longer = more * (base + 1);
+        return g < longer ? g / (base + 1) : more + (g - longer) / base;
+    }
+};
 
 // Parts of a tile that are in memory, and with them their sums.
 __device__ __forceinline__ int arrived(const int32_t *p)
@@ -350,43 +350,51 @@ struct Finish {
     int team, teams;           // the teams that finish the tile take its rows of `a` in turn
 };
 
-// Sums of COLS rows of `a` from c0 on, block h, times the rows' scales and the
-// expert's factor; of a cut tile (CUT) over all of its parts in their order.
-template <int COLS, bool CUT>
+// Sums of COLS rows of `a` from c0 on, for BLOCKS blocks from h on, times the rows'
+// scales and the expert's factor; of a cut tile (CUT) over all of its parts in
+// their order.
+template <int COLS, int BLOCKS, bool CUT>
 __device__ __forceinline__ void tile_sums(const Finish &p, int h, int c0,
                                           const float (&scale)[kMaxRowsTile / 32],
-                                          const float (&ahead)[8], float (&v)[COLS])
+                                          const float (&ahead)[2][8], float (&v)[BLOCKS][COLS])
 {
-    if (!CUT || p.here >= 0) tmem_load(p.sums + h * p.second + c0, v);
+    if (!CUT || p.here >= 0)
+#pragma unroll
+        for (int b = 0; b < BLOCKS; b++) tmem_load(p.sums + (h + b) * p.second + c0, v[b]);
     if constexpr (CUT) {
         if (p.have && c0 == 0) {
 #pragma unroll
-            for (int j = 0; j < COLS; j++) v[j] = 0.f + v[j] + ahead[j];
+            for (int b = 0; b < BLOCKS; b++)
+#pragma unroll
+                for (int j = 0; j < COLS; j++)
+                    v[b][j] = 0.f + v[b][j] + (h + b ? ahead[1][j] : ahead[0][j]);
         } else {
-            float sum[COLS] = {};
+            float sum[BLOCKS][COLS] = {};
             // a part that starts the tile is its CTA's last, any other its first
             const float *at = p.from + (h * kMaxRowsTile + c0) * kW4Tile;
-            for (int q = 0; q < p.parts; q += kPartsAtOnce) {
-                float more[kPartsAtOnce][COLS];
+            for (int q = 0; q < p.parts; q++) {
+                const float *part = at + (2 * q + (q == 0)) * kPart;
 #pragma unroll
-                for (int i = 0; i < kPartsAtOnce; i++)
+                for (int b = 0; b < BLOCKS; b++)
 #pragma unroll
                     for (int j = 0; j < COLS; j++)
-                        more[i][j] = q + i < p.parts && q + i != p.here
-                                         ? __ldcg(at + (2 * (q + i) + (q + i == 0)) * kPart + j * kW4Tile)
-                                         : 0.f;
-#pragma unroll
-                for (int i = 0; i < kPartsAtOnce; i++)
-#pragma unroll
-                    for (int j = 0; j < COLS; j++) sum[j] += q + i == p.here ? v[j] : more[i][j];
+                        sum[b][j] += q == p.here
+                                         ? v[b][j]
+                                         : __ldcg(part + (b * kMaxRowsTile + j) * kW4Tile);
             }
 #pragma unroll
-            for (int j = 0; j < COLS; j++) v[j] = sum[j];
+            for (int b = 0; b < BLOCKS; b++)
+#pragma unroll
+                for (int j = 0; j < COLS; j++) v[b][j] = sum[b][j];
         }
     }
     const float mine = c0 < 32 ? scale[0] : c0 < 64 ? scale[1] : c0 < 96 ? scale[2] : scale[3];
 #pragma unroll
-    for (int j = 0; j < COLS; j++) v[j] = v[j] * __shfl_sync(kFull, mine, (c0 + j) & 31) * p.f;
+    for (int j = 0; j < COLS; j++) {
+        const float by = __shfl_sync(kFull, mine, (c0 + j) & 31);
+#pragma unroll
+        for (int b = 0; b < BLOCKS; b++) v[b][j] = v[b][j] * by * p.f;
+    }
 }
 
 // Outputs of this thread's weight row(s), COLS rows of `a` at a time.  dst: the
@@ -398,31 +406,30 @@ __device__ __forceinline__ void finish_gated(const Finish &p, const float (&scal
 {
 #pragma unroll 1
     for (int c0 = p.team * COLS; c0 < p.rows; c0 += p.teams * COLS) {
-        float gate[COLS], up[COLS];
-        tile_sums<COLS, CUT>(p, 0, c0, scale, ahead[0], gate);
-        tile_sums<COLS, CUT>(p, 1, c0, scale, ahead[1], up);
+        float v[2][COLS];
+        tile_sums<COLS, 2, CUT>(p, 0, c0, scale, ahead, v);
         if (store)
 #pragma unroll
             for (int j = 0; j < COLS; j++)
                 if (c0 + j < p.rows)
                     dst[(int64_t)(c0 + j) * N] =
-                        __float2bfloat16_rn(__fdividef(gate[j], 1.f + __expf(-gate[j])) * up[j]);
+                        __float2bfloat16_rn(__fdividef(v[0][j], 1.f + __expf(-v[0][j])) * v[1][j]);
     }
 }
 template <int COLS, bool CUT>
 __device__ __forceinline__ void finish_plain(const Finish &p, int h,
                                              const float (&scale)[kMaxRowsTile / 32],
-                                             const float (&ahead)[8], __nv_bfloat16 *dst, int N,
+                                             const float (&ahead)[2][8], __nv_bfloat16 *dst, int N,
                                              bool store)
 {
 #pragma unroll 1
     for (int c0 = p.team * COLS; c0 < p.rows; c0 += p.teams * COLS) {
-        float v[COLS];
-        tile_sums<COLS, CUT>(p, h, c0, scale, ahead, v);
+        float v[1][COLS];
+        tile_sums<COLS, 1, CUT>(p, h, c0, scale, ahead, v);
         if (store)
 #pragma unroll
             for (int j = 0; j < COLS; j++)
-                if (c0 + j < p.rows) dst[(int64_t)(c0 + j) * N] = __float2bfloat16_rn(v[j]);
+                if (c0 + j < p.rows) dst[(int64_t)(c0 + j) * N] = __float2bfloat16_rn(v[0][j]);
     }
 }
 
@@ -510,13 +517,14 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
     // Every CTA takes part where that leaves it kMinPart chunks; else the tiles are
     // cut into parts of at least that (short tiles not at all).
     const int most_parts = max(1, chunks / kMinPart);
-    const int B = tasks <= (int)gridDim.x / most_parts ? tasks * most_parts : min(total, (int)gridDim.x);
+    const int B = tasks * most_parts <= (int)gridDim.x ? tasks * most_parts : min(total, (int)gridDim.x);
     const bool idle = (int)blockIdx.x >= B;
-    Walk walk(sh, idle ? 0 : cut(total, blockIdx.x, B), idle ? 0 : cut(total, blockIdx.x + 1, B), E,
-              tiles, chunks);
+    const Cut cut(total, B);
+    Walk walk(sh, idle ? 0 : cut.start(blockIdx.x), idle ? 0 : cut.start(blockIdx.x + 1), E, tiles,
+              chunks);
     // a stage of row operands holds up to four chunks, as many as leave three stages or more
     const int tile_bytes = max(1, sh.most) * kGroupBytes;
-    const int x_chunks = kXBytes / tile_bytes >= 12 ? 4 : kXBytes / tile_bytes >= 6 ? 2 : 1;
+    const int x_chunks = 12 * tile_bytes <= kXBytes ? 4 : 6 * tile_bytes <= kXBytes ? 2 : 1;
     const int x_stage_bytes = x_chunks * tile_bytes;
     const int x_stages = min(kXStagesMax, kXBytes / x_stage_bytes);
     // sums: two tiles of 128 columns in turn, the blocks' 64 columns apart in them, which
@@ -698,8 +706,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
             __nv_bfloat16 *out = y + (int64_t)(sh.start[g.e] + g.row0) * N;
             int first = 0, parts = 1;
             if (g.c1 - g.c0 < chunks) {
-                first = owner(total, B, g.task * chunks);
-                parts = owner(total, B, g.task * chunks + chunks - 1) - first + 1;
+                first = cut.owner(g.task * chunks);
+                parts = cut.owner(g.task * chunks + chunks - 1) - first + 1;
             }
             float scale[kMaxRowsTile / 32];      // of rows lane, lane + 32, ... of the tile
 #pragma unroll
@@ -759,10 +767,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
                     for (int h = 0; h < 2; h++) {
                         if (h == blocks) break;
                         const int n = w4_output(g.tile, h, row, N, false);
-                        if (parts > 1) finish_plain<8, true>(fin, h, scale, ahead[h], out + n, N, n < N);
+                        if (parts > 1) finish_plain<8, true>(fin, h, scale, ahead, out + n, N, n < N);
                         else if (g.rows <= 8)
-                            finish_plain<8, false>(fin, h, scale, ahead[h], out + n, N, n < N);
-                        else finish_plain<16, false>(fin, h, scale, ahead[h], out + n, N, n < N);
+                            finish_plain<8, false>(fin, h, scale, ahead, out + n, N, n < N);
+                        else finish_plain<16, false>(fin, h, scale, ahead, out + n, N, n < N);
                     }
                 }
             }
