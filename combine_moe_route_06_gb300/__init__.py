@@ -14,6 +14,7 @@ torch.uint16 tensors (the bits are what matters).
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -160,11 +161,11 @@ def load_library() -> ctypes.CDLL:
                                    ctypes.c_int),
             "moe_combine_backward": ([P, P, i32, P, P, P, i32, i32, i32, i32, P, P, P, P],
                                      ctypes.c_int),
-            "moe_w4_bytes": ([i32, i32, i32, i32], sz),
             "moe_w4_pack": ([P, P, i32, i32, i32, i32, P, sz, P], ctypes.c_int),
-            "moe_expert_product_w4_workspace_bytes": ([i32, i32, i32, i32], sz),
             "moe_expert_product_w4": ([P, i32, P, P, i32, P, P, i32, i32, i32, i32, P, P, sz, P, P],
                                       ctypes.c_int),
+            "moe_w4_bytes": ([i32, i32, i32, i32], sz),
+            "moe_expert_product_w4_workspace_bytes": ([i32, i32, i32, i32], sz),
             "moe_trace_enable": ([ctypes.c_char_p, i32], ctypes.c_int),
             "moe_trace_disable": ([], None),
             "moe_trace_reset": ([], None),
@@ -216,28 +217,22 @@ def _status_ptr(dev_status):
     return _dev(dev_status, "dev_status", (torch.int32,))
 
 
-def _arr(t, name: str, dtypes, shape):
-    """Address of a contiguous CUDA tensor of one of `dtypes` and of `shape` (None: any size)."""
-    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.is_contiguous()
-            and (shape is None or t.shape == shape)):
-        return t.data_ptr()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor (got {t.device})")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+_ops_module = None
 
 
-def _opt(t, name: str, dtypes, shape):
-    return None if t is None else _arr(t, name, dtypes, shape)
-
-
-_I32, _F32, _U8 = (torch.int32,), (torch.float32,), (torch.uint8,)
-_LOGIT_TYPES = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16}
+def _ops():
+    """The compiled entry points (csrc/binding.cpp) of the training and 4-bit expert calls."""
+    global _ops_module
+    if _ops_module is None:
+        load_library()
+        if not os.path.exists(_build.OPS_PATH):
+            raise MoeLibraryMissing(
+                f"{_build.OPS_PATH} is not built; run `python -c 'import __graft_entry__ as g; g.build()'`")
+        spec = importlib.util.spec_from_file_location("_moe_ops", _build.OPS_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _ops_module = module
+    return _ops_module
 
 
 def moe_version() -> int:
@@ -756,16 +751,10 @@ def moe_balance_loss(logits, topk_ids, counts, prob_mean, lse, n_valid, losses, 
     """Router losses: logits f32 or bf16 [S,T,E], topk_ids i32 [S,T,k], token_mask uint8 [S,T]
     (None: all valid) -> counts i32 [S,E], prob_mean f32 [S,E], lse f32 [S,T], n_valid i32 [S],
     losses f32 [2] (balance, z); ws is a uint8 device tensor."""
-    lib = load_library()
-    S, T, E = logits.shape
-    k = topk_ids.shape[-1]
-    _check(lib.moe_balance_loss(
-        _arr(logits, "logits", _LOGIT_TYPES, None), _LOGIT_TYPES[logits.dtype], S, T, E, k,
-        _arr(topk_ids, "topk_ids", _I32, (S, T, k)), _opt(token_mask, "token_mask", _U8, (S, T)),
-        _arr(counts, "counts", _I32, (S, E)), _arr(prob_mean, "prob_mean", _F32, (S, E)),
-        _arr(lse, "lse", _F32, (S, T)), _arr(n_valid, "n_valid", _I32, (S,)),
-        _arr(losses, "losses", _F32, (2,)), _arr(ws, "ws", _U8, None), ws.numel(),
-        _opt(dev_status, "dev_status", _I32, None), _stream(stream)))
+    rc = _ops().balance_loss(logits, topk_ids, counts, prob_mean, lse, n_valid, losses, ws,
+                             token_mask, dev_status, stream)
+    if rc:
+        _check(rc)
 
 
 def moe_route_backward(logits, topk_ids, topk_w, d_topk_w, lse, counts, n_valid, d_losses,
@@ -773,39 +762,20 @@ def moe_route_backward(logits, topk_ids, topk_w, d_topk_w, lse, counts, n_valid,
     """Gradient in the logits [S,T,E] (f32 or bf16) of the routing weights (topk_w, d_topk_w f32
     [S,T,k], both or neither None) and of the two losses (d_losses f32 [2] with what
     moe_balance_loss wrote, or None) -> d_logits of the logits' type."""
-    lib = load_library()
-    S, T, E = d_logits.shape
-    if topk_ids is None and topk_w is not None:
-        raise ValueError("topk_ids: needed with topk_w")
-    k = topk_ids.shape[-1] if topk_ids is not None else 1
-    if d_losses is not None and topk_ids is None:
-        raise ValueError("topk_ids: needed with d_losses (k enters the balance loss)")
-    if d_losses is None:
-        logits = lse = counts = n_valid = None
-    _check(lib.moe_route_backward(
-        _opt(logits, "logits", (d_logits.dtype,), (S, T, E)), _LOGIT_TYPES.get(d_logits.dtype, -1),
-        S, T, E, k, _opt(topk_ids, "topk_ids", _I32, (S, T, k)),
-        _opt(topk_w, "topk_w", _F32, (S, T, k)), _opt(d_topk_w, "d_topk_w", _F32, (S, T, k)),
-        _opt(lse, "lse", _F32, (S, T)), _opt(counts, "counts", _I32, (S, E)),
-        _opt(n_valid, "n_valid", _I32, (S,)), _opt(d_losses, "d_losses", _F32, (2,)),
-        _opt(token_mask, "token_mask", _U8, (S, T)),
-        _arr(d_logits, "d_logits", _LOGIT_TYPES, None), _opt(dev_status, "dev_status", _I32, None),
-        _stream(stream)))
+    rc = _ops().route_backward(logits, topk_ids, topk_w, d_topk_w, lse, counts, n_valid, d_losses,
+                               d_logits, token_mask, dev_status, stream)
+    if rc:
+        _check(rc)
 
 
 def moe_combine_backward(d_out, y, pair_row, topk_w, d_y, d_topk_w, recv_pair=None,
                          dev_status=None, stream=None):
     """Gradient of moe_combine: d_out bf16 [S,T,H], y bf16 [y_rows,H] -> d_y bf16 [y_rows,H],
     d_topk_w f32 [S,T,k]; rows with recv_pair i32 [y_rows] < 0 are set to zero."""
-    lib = load_library()
-    S, T, H = d_out.shape
-    rows, k = y.shape[0], pair_row.shape[-1]
-    _check(lib.moe_combine_backward(
-        _arr(d_out, "d_out", _BF16_TYPES, None), _arr(y, "y", _BF16_TYPES, (rows, H)), rows,
-        _arr(pair_row, "pair_row", _I32, (S, T, k)), _arr(topk_w, "topk_w", _F32, (S, T, k)),
-        _opt(recv_pair, "recv_pair", _I32, (rows,)), S, T, k, H,
-        _arr(d_y, "d_y", _BF16_TYPES, (rows, H)), _arr(d_topk_w, "d_topk_w", _F32, (S, T, k)),
-        _opt(dev_status, "dev_status", _I32, None), _stream(stream)))
+    rc = _ops().combine_backward(d_out, y, pair_row, topk_w, d_y, d_topk_w, recv_pair, dev_status,
+                                 stream)
+    if rc:
+        _check(rc)
 
 
 def moe_w4_bytes(E: int, N: int, K: int, gated: bool = False) -> int:
@@ -819,14 +789,9 @@ def moe_w4_bytes(E: int, N: int, K: int, gated: bool = False) -> int:
 def moe_w4_pack(codes, scales, w4, gated=False, stream=None):
     """codes uint8 [E,rows,K/2] (E2M1, first value in the low nibble), scales uint8 [E,rows,K/16]
     (E4M3), rows = N or for gated weights 2N (gate, then up) -> w4 uint8 [moe_w4_bytes]."""
-    lib = load_library()
-    E, rows, half = codes.shape
-    if gated and rows % 2:
-        raise ValueError(f"codes: gated weights have an even number of rows, got {rows}")
-    N, K = rows // 2 if gated else rows, 2 * half
-    _check(lib.moe_w4_pack(_arr(codes, "codes", _U8, None),
-                           _arr(scales, "scales", _U8, (E, rows, K // 16)), E, N, K, int(gated),
-                           _arr(w4, "w4", _U8, None), w4.numel(), _stream(stream)))
+    rc = _ops().w4_pack(codes, scales, w4, gated, stream)
+    if rc:
+        _check(rc)
 
 
 def moe_expert_product_w4_workspace_bytes(a_rows: int, E: int, N: int, K: int) -> int:
@@ -837,19 +802,10 @@ def moe_expert_product_w4(a, w4, w_factor, y, ws, expert_offsets=None, masked_co
                           block_rows=0, gated=False, dev_status=None, stream=None):
     """a bf16 [rows,K] times every expert's packed 4-bit weights -> y bf16 [rows,N]; the experts'
     rows by expert_offsets i32 [E+1] or by masked_counts i32 [E] with block_rows; w_factor f32 [E]."""
-    lib = load_library()
-    rows, K = a.shape
-    N, E = y.shape[-1], w_factor.shape[0]
-    # the size of w4 in the layout: blocks of 9,216 bytes, 128 rows by 128 columns
-    if w4.numel() < E * -(-N // 128) * (2 if gated else 1) * -(-K // 128) * 9216:
-        raise ValueError(f"w4: {w4.numel()} bytes are not the packed weights of E={E}, N={N}, K={K}, "
-                         f"gated={gated}")
-    _check(lib.moe_expert_product_w4(
-        _arr(a, "a", _BF16_TYPES, None), rows, _opt(expert_offsets, "expert_offsets", _I32, (E + 1,)),
-        _opt(masked_counts, "masked_counts", _I32, (E,)), block_rows, _arr(w4, "w4", _U8, None),
-        _arr(w_factor, "w_factor", _F32, (E,)), E, N, K, int(gated),
-        _arr(y, "y", _BF16_TYPES, (rows, N)), _arr(ws, "ws", _U8, None), ws.numel(),
-        _opt(dev_status, "dev_status", _I32, None), _stream(stream)))
+    rc = _ops().expert_product_w4(a, w4, w_factor, y, ws, expert_offsets, masked_counts, block_rows,
+                                  gated, dev_status, stream)
+    if rc:
+        _check(rc)
 
 
 class MoePath:

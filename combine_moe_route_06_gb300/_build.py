@@ -3,6 +3,8 @@
 Each .cu translation unit compiles in its own nvcc process (in parallel),
 then one nvcc link produces the shared library.  The CUDA runtime is linked
 statically, so loading the library needs no GPU driver (only calls do).
+The Python entry points of csrc/binding.cpp become _moe_ops.so beside it (g++,
+torch's headers and libraries of the installation that runs the build).
 """
 from __future__ import annotations
 
@@ -11,12 +13,17 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libmoeroute.so")
+OPS_PATH = os.path.join(OUT_DIR, "_moe_ops.so")
+BINDING = os.path.join(CSRC, "binding.cpp")
 HEADER = os.path.join(ROOT, "include", "moe_route.h")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -41,13 +48,13 @@ def _sources():
 
 def _deps():
     return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
-        sorted(glob.glob(os.path.join(CSRC, "*.h"))) + [HEADER]
+        sorted(glob.glob(os.path.join(CSRC, "*.h"))) + [BINDING, HEADER]
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(OPS_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(OPS_PATH))
     return any(os.path.getmtime(d) > t for d in _deps())
 
 
@@ -70,15 +77,41 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             print(r.stdout + r.stderr)
         return obj
 
+    def compile_binding():
+        base = os.path.dirname(torch.__file__)
+        obj = os.path.join(OUT_DIR, "binding.o")
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-c", BINDING, "-o", obj,
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+               "-I", os.path.join(base, "include"),
+               "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include"),
+               "-I", sysconfig.get_paths()["include"]]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for {BINDING}:\n{r.stdout}\n{r.stderr}")
+        return obj
+
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding_obj = binding.result()
     tmp = LIB_PATH + f".{os.getpid()}.tmp"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    # torch's libraries are in the process when the module is imported; libmoeroute.so is
+    # found beside it and is the copy that ctypes loads from the same path
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = OPS_PATH + f".{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, binding_obj, "-L", torch_lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", OUT_DIR, "-l:libmoeroute.so",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, OPS_PATH)
     return LIB_PATH
 
 
