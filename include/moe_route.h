@@ -776,7 +776,7 @@ moe_status_t moe_expert_product_w4(const uint16_t *a, int a_rows, const int32_t 
  *   topk_ids   [S][T][k] int32; ids < 0 are not counted, ids >= E are skipped
  *              and flag MOE_ERR_BAD_EXPERT_ID.
  *   token_mask [S][T] uint8 or NULL: tokens with 0 are not valid.  Nothing of
- *              theirs is read (their logits may hold anything), lse is 0.
+ *              theirs counts (their logits may hold anything), lse is 0.
  *   counts, prob_mean [S][E]; lse [S][T] float32; n_valid [S] int32;
  *   losses [2] float32, all out, kept for moe_route_backward.
  *   ws         moe_balance_loss_workspace_bytes(S, T, E) bytes, 256-byte aligned.
@@ -801,7 +801,7 @@ moe_status_t moe_balance_loss(const void *logits, int logits_type, int S, int T,
  *   d_losses   [2] float32 or NULL (no gradient comes through the losses; logits,
  *              lse, counts and n_valid may then be NULL).
  *   lse, counts, n_valid  as moe_balance_loss wrote them, for the same token_mask.
- *   token_mask as there; tokens with 0 get a zero row, nothing of theirs is read.
+ *   token_mask as there; tokens with 0 get a zero row, whatever theirs holds.
  *   d_logits   [S][T][E] of logits_type out, apart from the inputs.
  *   ids < 0 carry no gradient; ids >= E neither, and flag MOE_ERR_BAD_EXPERT_ID.
  */
