@@ -596,36 +596,40 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
         while (ok && walk.next(g)) {
             const uint32_t word = mma_f16_word((g.rows + 15) / 16 * 16);
             if (!(ok = mbar_wait_warp(&sh.sums_empty[d], pd ^ 1, dead))) break;
-            for (int cx = g.c0; ok && cx < g.c1; cx += x_chunks) {
-                if (!(ok = mbar_wait_warp(&sh.x_full[sx], px, dead))) break;
-                uint64_t b = mma_smem_word(smem_addr(xring) + sx * x_stage_bytes, kGroupBytes);
-                const int end = min(cx + x_chunks, g.c1);
-                for (int c = cx; c < end; c++, b += tile_bytes >> 4) {
-                    const uint32_t sums = tmem + d * kMaxRowsTile;
-                    const uint32_t a = tmem + kAFirst + sa * kAColumns;
-                    if (!(ok = mbar_wait_warp(&sh.a_full[sa], pa, dead))) break;
-                    if (blocks == 2 && !(ok = mbar_wait_warp(&sh.a_full[sa + 1], pa, dead))) break;
-                    tmem_fence_after();
-                    if (elect_lane()) {
-                        mma_block(sums, a, b, word, c > g.c0);
-                        mma_commit(&sh.a_empty[sa]);
-                        if (blocks == 2) {
-                            mma_block(sums + second, a + kAColumns, b, word, c > g.c0);
-                            mma_commit(&sh.a_empty[sa + 1]);
-                        }
-                        if (c == end - 1) mma_commit(&sh.x_empty[sx]);
-                        if (c == g.c1 - 1) mma_commit(&sh.sums_full[d]);
-                    }
-                    __syncwarp();
-                    sa += blocks;
-                    if (sa == kAStages) {
-                        sa = 0;
-                        pa ^= 1;
-                    }
+            const uint32_t sums = tmem + d * kMaxRowsTile;
+            int left = 0;                // chunks left in the stage of row operands
+            uint64_t b = 0;
+            for (int c = g.c0; c < g.c1; c++) {
+                // (a stage of row operands that has been waited for passes again)
+                if (!(ok = mbar_wait3_warp(&sh.a_full[sa], pa, &sh.a_full[sa + blocks - 1], pa,
+                                           &sh.x_full[sx], px, dead)))
+                    break;
+                tmem_fence_after();
+                if (left == 0) {
+                    left = min(x_chunks, g.c1 - c);
+                    b = mma_smem_word(smem_addr(xring) + sx * x_stage_bytes, kGroupBytes);
                 }
-                if (++sx == x_stages) {
+                const uint32_t a = tmem + kAFirst + sa * kAColumns;
+                if (elect_lane()) {
+                    mma_block(sums, a, b, word, c > g.c0);
+                    mma_commit(&sh.a_empty[sa]);
+                    if (blocks == 2) {
+                        mma_block(sums + second, a + kAColumns, b, word, c > g.c0);
+                        mma_commit(&sh.a_empty[sa + 1]);
+                    }
+                    if (left == 1) mma_commit(&sh.x_empty[sx]);
+                    if (c == g.c1 - 1) mma_commit(&sh.sums_full[d]);
+                }
+                __syncwarp();
+                b += tile_bytes >> 4;
+                if (--left == 0 && ++sx == x_stages) {
                     sx = 0;
                     px ^= 1;
+                }
+                sa += blocks;
+                if (sa == kAStages) {
+                    sa = 0;
+                    pa ^= 1;
                 }
             }
             if (++d == sums_stages) {

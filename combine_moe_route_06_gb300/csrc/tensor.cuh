@@ -75,6 +75,35 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, v
     return __all_sync(kFull, mbar_wait(bar, parity, dead));
 }
 
+// Three barriers at once, by a whole warp that polls (a wait on each in turn would
+// cost their latencies one after the other, about 100 clocks each).
+__device__ __forceinline__ bool mbar_wait3_warp(uint64_t *bar0, uint32_t parity0, uint64_t *bar1,
+                                                uint32_t parity1, uint64_t *bar2, uint32_t parity2,
+                                                volatile int *dead)
+{
+    uint64_t start = 0;
+    for (int i = 1;; i++) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p, q, r;\n\t"
+                     "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+                     "mbarrier.test_wait.parity.shared::cta.b64 r, [%5], %6;\n\t"
+                     "and.pred p, p, q;\n\tand.pred p, p, r;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(smem_addr(bar0)), "r"(parity0), "r"(smem_addr(bar1)), "r"(parity1),
+                       "r"(smem_addr(bar2)), "r"(parity2)
+                     : "memory");
+        if (__all_sync(kFull, ok)) return true;
+        if ((i & 63) == 0) {
+            const uint64_t now = global_ns();
+            if (start == 0) start = now;
+            const bool late = now - start > kWaitLimitNs;
+            if (late) *dead = 1;
+            if (__any_sync(kFull, late || *dead)) return false;
+        }
+    }
+}
+
 // Bytes (a multiple of 16, both ends 16-byte aligned) from global to shared
 // memory; the barrier counts them.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
