@@ -261,29 +261,59 @@ __device__ __forceinline__ int expert_of(const MmShared &sh, int E, int tiles, i
     return base + 31 - __clz((int)below2);
 }
 
-// The chunks [at, to) of this CTA, one tile after the other; for whole warps.
+// `total` chunks cut into B parts: the first `more` have base + 1 of them, the rest base.
+struct Cut {
+    int base, more;
+    __device__ Cut(int total, int B) : base(B ? total / B : 0), more(B ? total - base * B : 0) {}
+    __device__ int start(int b) const { return b * base + min(b, more); }
+    __device__ int owner(int g) const       // the part that holds chunk g
+    {
+        const int longer = more * (base + 1);
+        return g < longer ? g / (base + 1) : more + (g - longer) / base;
+    }
+};
+
+struct WorkShape {
+    int E, tiles, chunks, blocks;
+};
+
+__device__ __forceinline__ int total_chunks(const MmShared &sh, const WorkShape &w)
+{
+    return sh.before[w.E] * w.tiles * w.chunks;
+}
+// CTAs that take part: all where that leaves each kMinPart chunks; else the tiles are
+// cut into parts of at least that (short tiles not at all).
+__device__ __forceinline__ int parts_of(int total, const WorkShape &w)
+{
+    const int most = max(1, w.chunks / kMinPart), tasks = total / w.chunks;
+    return tasks * most <= (int)gridDim.x ? tasks * most : min(total, (int)gridDim.x);
+}
+
+// The chunks of this CTA, one tile after the other; for whole warps.
 struct Walk {
     const MmShared &sh;
+    const WorkShape &w;
     int at, to;
-    int E, tiles, chunks;
     int task, c0;
-    __device__ Walk(const MmShared &s, int from, int end, int E_, int tiles_, int chunks_)
-        : sh(s), at(from), to(end), E(E_), tiles(tiles_), chunks(chunks_)
+    __device__ Walk(const MmShared &s, const WorkShape &shape, const Cut &cut, int B) : sh(s), w(shape)
     {
-        task = at / chunks;
-        c0 = at - task * chunks;
+        const int b = blockIdx.x;
+        at = b < B ? cut.start(b) : 0;
+        to = b < B ? cut.start(b + 1) : 0;
+        task = at / w.chunks;
+        c0 = at - task * w.chunks;
     }
     __device__ bool next(Segment &g)
     {
         if (at >= to) return false;
         g.task = task;
         g.c0 = c0;
-        g.c1 = min(chunks, c0 + to - at);
+        g.c1 = min(w.chunks, c0 + to - at);
         at += g.c1 - g.c0;
         task++;
         c0 = 0;
-        g.e = expert_of(sh, E, tiles, g.task);
-        const int local = g.task - sh.before[g.e] * tiles;
+        g.e = expert_of(sh, w.E, w.tiles, g.task);
+        const int local = g.task - sh.before[g.e] * w.tiles;
         const int nt = sh.before[g.e + 1] - sh.before[g.e];
         const int count = sh.count[g.e];
         if (nt == 1) {
@@ -297,18 +327,6 @@ struct Walk {
             g.rows = min(per, count - g.row0);
         }
         return true;
-    }
-};
-
-// `total` chunks cut into B parts: the first `more` have base + 1 of them, the rest base.
-struct Cut {
-    int base, more;
-    __device__ Cut(int total, int B) : base(B ? total / B : 0), more(B ? total - base * B : 0) {}
-    __device__ int start(int b) const { return b * base + min(b, more); }
-    __device__ int owner(int g) const       // the part that holds chunk g
-    {
-        const int longer = more * (base + 1);
-        return g < longer ? g / (base + 1) : more + (g - longer) / base;
     }
 };
 
@@ -433,6 +451,91 @@ __device__ __forceinline__ void finish_plain(const Finish &p, int h,
     }
 }
 
+// By one warp: the experts' rows, and before[e], the row tiles of those before e.
+// Runs could only overlap where the offsets fall: from there on no expert has rows.
+__device__ __forceinline__ void scan_experts(MmShared &sh, const int32_t *offsets,
+                                             const int32_t *counts, int block_rows, int a_rows, int E,
+                                             int blocks, uint32_t *dev_status)
+{
+    constexpr int kAhead = 4;            // loads in flight
+    const int lane = threadIdx.x & 31;
+    int tiles_before = 0, most = 0;
+    bool fell = false, bad = false;
+    for (int e0 = 0; e0 < E; e0 += 32 * kAhead) {
+        int start[kAhead], count[kAhead];
+        bool falls[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; i++) {
+            const int e = e0 + 32 * i + lane;
+            start[i] = count[i] = 0;
+            falls[i] = false;
+            if (e < E) {
+                expert_rows(offsets, counts, block_rows, a_rows, e, start[i], count[i], bad);
+                falls[i] = offsets && __ldg(offsets + e + 1) < __ldg(offsets + e);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; i++) {
+            const int e = e0 + 32 * i + lane;
+            if (e0 + 32 * i >= E) break;
+            const unsigned fall = __ballot_sync(kFull, falls[i]);
+            if (fell || (fall & (lanemask_lt() | 1u << lane))) count[i] = 0;
+            fell = fell || fall;
+            const int n = tiles_of(count[i]);
+            if (n > 0) most = max(most, rows_per_tile(count[i], n) / 8);
+            const int inc = warp_inclusive_scan(n);
+            if (e < E) {
+                sh.start[e] = start[i];
+                sh.count[e] = count[i];
+                sh.before[e] = tiles_before + inc - n;
+            }
+            tiles_before += __shfl_sync(kFull, inc, 31);
+        }
+    }
+    most = __reduce_max_sync(kFull, most);
+    if (lane == 0) {
+        sh.before[E] = tiles_before;
+        sh.most = most;
+        const int warps = blocks == 2 && most > 8 ? kDecodeWarps : kEpilogueWarps;
+        mbar_init(&sh.sums_empty[0], warps);
+        mbar_init(&sh.sums_empty[1], warps);
+        mbar_init_fence();
+    }
+    if (bad && blockIdx.x == 0) flag_status(dev_status, MOE_ERR_INVALID_ARG);
+    __syncwarp();
+}
+
+// The weight warp's work: the CTA's blocks into the ring.
+__device__ __forceinline__ void load_weights(MmShared &sh, uint8_t *wring, const uint8_t *w4,
+                                             const WorkShape &w)
+{
+    const int total = total_chunks(sh, w), B = parts_of(total, w);
+    Walk walk(sh, w, Cut(total, B), B);
+    Segment g;
+    int s = 0;
+    uint32_t phase = 0, issued = 0;
+    bool ok = true;
+    while (ok && walk.next(g)) {
+        // (the blocks of a segment are one after the other in memory)
+        const uint8_t *src = w4 + (((int64_t)g.e * w.tiles + g.tile) * w.chunks + g.c0) * w.blocks *
+                                      (int64_t)kW4BlockBytes;
+        for (int i = 0; i < (g.c1 - g.c0) * w.blocks; i++, src += kW4BlockBytes) {
+            if (!(ok = mbar_wait_warp(&sh.w_empty[s], phase ^ 1, &sh.dead))) break;
+            if (elect_lane()) {
+                mbar_expect(&sh.w_full[s], kW4BlockBytes);
+                bulk_load(wring + s * kW4BlockBytes, src, kW4BlockBytes, &sh.w_full[s]);
+            }
+            __syncwarp();
+            issued |= 1u << s;
+            if (++s == kWStages) {
+                s = 0;
+                phase ^= 1;
+            }
+        }
+    }
+    if (!ok) drain(sh.w_full, kWStages, s, phase, issued);
+}
+
 __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
     const uint8_t *__restrict__ w4, const float *__restrict__ factor, const uint8_t *x16,
     const float *row_scale, float *partial, int32_t *arrivals, const int32_t *__restrict__ offsets,
@@ -450,20 +553,24 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
     // The row counts are older than k_w4_rows, which has passed its own wait when
     // this kernel starts: they and the weights may be read before pdl_wait.
     pdl_trigger();
-    bool bad = false;
-    for (int e = tid; e < E; e += kMmThreads) {
-        int start, count;
-        expert_rows(offsets, counts, block_rows, a_rows, e, start, count, bad);
-        sh.start[e] = start;
-        sh.count[e] = offsets && offsets[e + 1] < offsets[e] ? -1 : count;
-    }
-    if (warp == kWarpMma) tmem_alloc(&sh.tmem, kTmemColumns);
+    volatile int *dead = &sh.dead;
+    const WorkShape shape{E, tiles, chunks, blocks};
     if (warp == kWarpW) {
-        if (lane == 0) sh.dead = 0;
+        // ---- weight blocks, one bulk copy each.  This warp first finds out what there is to do,
+        // in shared memory for all.
         if (lane < kWStages) {
             mbar_init(&sh.w_full[lane], 1);
             mbar_init(&sh.w_empty[lane], 4);
         }
+        if (lane == 0) sh.dead = 0;
+        mbar_init_fence();
+        scan_experts(sh, offsets, counts, block_rows, a_rows, E, blocks, dev_status);
+        named_barrier(2, kMmThreads);
+        load_weights(sh, wring, w4, shape);
+        __syncthreads();
+        return;
+    }
+    if (warp == kWarpX) {
         if (lane < kXStagesMax) {
             mbar_init(&sh.x_full[lane], 1);
             mbar_init(&sh.x_empty[lane], 1);
@@ -475,53 +582,19 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
         if (lane < 2) mbar_init(&sh.sums_full[lane], 1);
         if (lane == 2) mbar_init(&sh.done, 1);
         mbar_init_fence();
+    } else if (warp == kWarpMma) {
+        tmem_alloc(&sh.tmem, kTmemColumns);
+        tmem_fence_before();
     }
-    __syncthreads();
-    if (warp == 0) {
-        // prefix sums of the experts' row tiles.  Runs could only overlap where the
-        // offsets fall: from there on no expert has rows.
-        int tiles_before = 0, most = 0;
-        bool fell = false;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int e = e0 + lane;
-            int count = e < E ? sh.count[e] : 0;
-            const unsigned falls = __ballot_sync(kFull, count < 0);
-            if (fell || (falls & (lanemask_lt() | 1u << lane))) {
-                count = 0;
-                if (e < E) sh.count[e] = 0;
-            }
-            fell = fell || falls;
-            const int n = tiles_of(count);
-            if (n > 0) most = max(most, rows_per_tile(count, n) / 8);
-            const int inc = warp_inclusive_scan(n);
-            if (e < E) sh.before[e] = tiles_before + inc - n;
-            tiles_before += __shfl_sync(kFull, inc, 31);
-        }
-        most = __reduce_max_sync(kFull, most);
-        if (lane == 0) {
-            sh.before[E] = tiles_before;
-            sh.most = most;
-            const int warps = blocks == 2 && most > 8 ? kDecodeWarps : kEpilogueWarps;
-            mbar_init(&sh.sums_empty[0], warps);
-            mbar_init(&sh.sums_empty[1], warps);
-            mbar_init_fence();
-        }
-    }
-    if (bad && blockIdx.x == 0) flag_status(dev_status, MOE_ERR_INVALID_ARG);
-    tmem_fence_before();
-    __syncthreads();
+    named_barrier(2, kMmThreads);
     tmem_fence_after();
 
     const uint32_t tmem = sh.tmem;
-    const int tasks = sh.before[E] * tiles, total = tasks * chunks;
-    // Every CTA takes part where that leaves it kMinPart chunks; else the tiles are
-    // cut into parts of at least that (short tiles not at all).
-    const int most_parts = max(1, chunks / kMinPart);
-    const int B = tasks * most_parts <= (int)gridDim.x ? tasks * most_parts : min(total, (int)gridDim.x);
-    const bool idle = (int)blockIdx.x >= B;
+    const int total = total_chunks(sh, shape), B = parts_of(total, shape);
     const Cut cut(total, B);
-    Walk walk(sh, idle ? 0 : cut.start(blockIdx.x), idle ? 0 : cut.start(blockIdx.x + 1), E, tiles,
-              chunks);
+    Walk walk(sh, shape, cut, B);
+    Segment g;
+    bool ok = true;
     // a stage of row operands holds up to four chunks, as many as leave three stages or more
     const int tile_bytes = max(1, sh.most) * kGroupBytes;
     const int x_chunks = 12 * tile_bytes <= kXBytes ? 4 : 6 * tile_bytes <= kXBytes ? 2 : 1;
@@ -535,33 +608,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
     const int sums_stages = large ? 1 : 2;
     const int second = large ? kMaxRowsTile : kMaxRowsTile / 2;
     const bool runs = offsets != nullptr;
-    volatile int *dead = &sh.dead;
-    Segment g;
-    bool ok = true;
 
-    if (warp == kWarpW) {
-        // ---- weight blocks: one bulk copy each
-        int s = 0;
-        uint32_t phase = 0, issued = 0;
-        while (ok && walk.next(g)) {
-            const uint8_t *src =
-                w4 + (((int64_t)g.e * tiles + g.tile) * chunks + g.c0) * blocks * (int64_t)kW4BlockBytes;
-            for (int i = 0; i < (g.c1 - g.c0) * blocks; i++, src += kW4BlockBytes) {
-                if (!(ok = mbar_wait_warp(&sh.w_empty[s], phase ^ 1, dead))) break;
-                if (elect_lane()) {
-                    mbar_expect(&sh.w_full[s], kW4BlockBytes);
-                    bulk_load(wring + s * kW4BlockBytes, src, kW4BlockBytes, &sh.w_full[s]);
-                }
-                __syncwarp();
-                issued |= 1u << s;
-                if (++s == kWStages) {
-                    s = 0;
-                    phase ^= 1;
-                }
-            }
-        }
-        if (!ok) drain(sh.w_full, kWStages, s, phase, issued);
-    } else if (warp == kWarpX) {
+    if (warp == kWarpX) {
         // ---- row operands: one bulk copy per chunk, one barrier per stage
         pdl_wait();
         const int64_t groups = row_groups(a_rows, E);
