@@ -145,14 +145,16 @@ __global__ void __launch_bounds__(kRlThreads) k_balance_part(
     float z = 0.f;
     int n = 0;
     bool bad_id = false;
-    // the next row's loads are in flight while this one is summed, and the mark of
-    // the row after it, so that rows that are not valid are never loaded
+    // R rows at a time, whose reductions overlap; the next ones' loads are in flight
+    // meanwhile, and the marks of those after them, so that rows that are not valid are
+    // never loaded
+    constexpr int R = VPL <= 12 ? 2 : 1;
     struct Row {
         L v[VPL];
         int id;
         bool valid;
-    } next;
-    const int step = B * kRlWarps;
+    } next[R];
+    const int64_t step = B * kRlWarps;
     auto valid = [&](int64_t t) { return t < T && (mask == nullptr || mask[(int64_t)s * T + t] != 0); };
     auto load = [&](int64_t t, bool marked, Row &r) {
         r.valid = marked;
@@ -165,43 +167,63 @@ __global__ void __launch_bounds__(kRlThreads) k_balance_part(
         for (int i = 0; i < VPL; i++)
             if (lane + 32 * i < E) r.v[i] = src[lane + 32 * i];
     };
-    const int t0 = b * kRlWarps + warp;
-    load(t0, valid(t0), next);
-    bool marked = valid(t0 + step);
-    for (int64_t t = t0; t < T; t += step) {
-        const Row now = next;
-        load(t + step, marked, next);
-        marked = valid(t + 2 * step);
-        const int64_t row = (int64_t)s * T + t;
-        if (!now.valid) {
-            if (lane == 0) lse[row] = 0.f;
-            continue;
-        }
-        n++;
-        if (now.id >= E) bad_id = true;
-        else if (now.id >= 0) atomicAdd(&picks[now.id], 1);
-        float v[VPL];
-        float top = -INFINITY;
+    const int64_t t0 = b * kRlWarps + warp;
+    bool marked[R];
 #pragma unroll
-        for (int i = 0; i < VPL; i++) {
-            v[i] = lane + 32 * i < E ? to_float(now.v[i]) : -INFINITY;
-            top = fmaxf(top, v[i]);
-        }
-        top = warp_max(top);
-        const float base = top == -INFINITY ? 0.f : top;   // a row of -inf: all terms 0
-        float sum = 0.f;
+    for (int r = 0; r < R; r++) {
+        load(t0 + r * step, valid(t0 + r * step), next[r]);
+        marked[r] = valid(t0 + (R + r) * step);
+    }
+    for (int64_t t = t0; t < T; t += R * step) {
+        Row now[R];
+        float top[R], sum[R], v[R][VPL];
 #pragma unroll
-        for (int i = 0; i < VPL; i++) {
-            v[i] = exp_below(v[i] - base);
-            sum += v[i];
-        }
-        sum = warp_sum(sum);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        for (int r = 0; r < R; r++) {
+            now[r] = next[r];
+            load(t + (R + r) * step, marked[r], next[r]);
+            marked[r] = valid(t + (2 * R + r) * step);
+            top[r] = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < VPL; i++) acc[i] = fmaf(v[i], inv, acc[i]);
-        const float l = base + logf(sum);
-        if (sum != 0.f) z = fmaf(l, l, z);
-        if (lane == 0) lse[row] = l;
+            for (int i = 0; i < VPL; i++) {
+                v[r][i] = now[r].valid && lane + 32 * i < E ? to_float(now[r].v[i]) : -INFINITY;
+                top[r] = fmaxf(top[r], v[r][i]);
+            }
+        }
+#pragma unroll
+        for (int off = 16; off; off >>= 1)
+#pragma unroll
+            for (int r = 0; r < R; r++) top[r] = fmaxf(top[r], __shfl_xor_sync(kFull, top[r], off));
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            top[r] = top[r] == -INFINITY ? 0.f : top[r];     // a row of -inf: all terms 0
+            sum[r] = 0.f;
+#pragma unroll
+            for (int i = 0; i < VPL; i++) {
+                v[r][i] = exp_below(v[r][i] - top[r]);
+                sum[r] += v[r][i];
+            }
+        }
+#pragma unroll
+        for (int off = 16; off; off >>= 1)
+#pragma unroll
+            for (int r = 0; r < R; r++) sum[r] += __shfl_xor_sync(kFull, sum[r], off);
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            if (t + r * step >= T) break;
+            const int64_t row = (int64_t)s * T + t + r * step;
+            float l = 0.f;                                   // what a token that is not valid gets
+            if (now[r].valid) {
+                n++;
+                if (now[r].id >= E) bad_id = true;
+                else if (now[r].id >= 0) atomicAdd(&picks[now[r].id], 1);
+                const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r];
+#pragma unroll
+                for (int i = 0; i < VPL; i++) acc[i] = fmaf(v[r][i], inv, acc[i]);
+                l = top[r] + logf(sum[r]);
+                if (sum[r] != 0.f) z = fmaf(l, l, z);
+            }
+            if (lane == 0) lse[row] = l;
+        }
     }
     if (bad_id) flag_status(dev_status, MOE_ERR_BAD_EXPERT_ID);
 #pragma unroll
