@@ -87,7 +87,12 @@ __host__ __device__ __forceinline__ int64_t row_groups(int a_rows, int E)
 }
 
 constexpr int kRowsThreads = 128;
-constexpr int kRowsHeld = 4;        // 16-byte vectors of a row that a thread keeps
+// Two forms.  FEW: at 32 registers one CTA per SM fits beside one of k_expert_w4,
+// which then starts on all SMs at once (else the SMs that hold a row start 3 us after
+// the others).  Not FEW: a thread keeps its part of the row between the two passes,
+// six CTAs per SM, for rows whose bytes are the bound.
+constexpr int kRowsAheadFew = 5, kRowsAheadMany = 4;   // 16-byte loads in flight per thread
+constexpr int kRowsCtasFew = 16, kRowsCtasMany = 6;
 
 // Operand layout of the rows: chunk c of group g at (c * groups + g) * 2048 bytes,
 // so a tile's rows are one bulk copy per chunk; in each of its two 64-column
@@ -120,8 +125,25 @@ __device__ __forceinline__ int4 scale_to_half8(int4 v, float by)
     return make_int4((int)h[0], (int)h[1], (int)h[2], (int)h[3]);
 }
 
-// One CTA per row.  Also zeroes the arrival counters of k_expert_w4.
-__global__ void __launch_bounds__(kRowsThreads) k_w4_rows(
+// The expert whose run holds row r: the last e < E with offsets[e] <= r, by a warp in
+// two ballots over at most 32 values each (E <= 1024).
+__device__ __forceinline__ int run_of(const int32_t *offsets, int E, int r)
+{
+    const int lane = threadIdx.x & 31;
+    const int step = (E + 31) / 32;
+    const int s = lane * step < E ? __ldg(offsets + lane * step) : 0x7fffffff;
+    const unsigned below = __ballot_sync(kFull, s <= r);
+    const int base = below ? (31 - __clz((int)below)) * step : 0;
+    const int s2 = lane < step && base + lane < E ? __ldg(offsets + base + lane) : 0x7fffffff;
+    const unsigned below2 = __ballot_sync(kFull, s2 <= r);
+    return base + (below2 ? 31 - __clz((int)below2) : 0);
+}
+
+// One CTA per row, `grid` rows apart.  With blocks, candidate q is row q / E of block
+// q % E, so that the rows in use come first; every warp looks 32 candidates over at
+// once.  Also zeroes the arrival counters of k_expert_w4.
+template <bool FEW>
+__global__ void __launch_bounds__(kRowsThreads, FEW ? kRowsCtasFew : kRowsCtasMany) k_w4_rows(
     const int4 *__restrict__ a, int a_rows, const int32_t *__restrict__ offsets,
     const int32_t *__restrict__ counts, int block_rows, int E, int K, uint8_t *__restrict__ x16,
     float *__restrict__ row_scale, int32_t *__restrict__ arrivals, int n_arrivals)
@@ -134,64 +156,61 @@ __global__ void __launch_bounds__(kRowsThreads) k_w4_rows(
         for (int i = tid; i < n_arrivals; i += kRowsThreads) arrivals[i] = 0;
     const int V = K / 8, padded = 16 * w4_chunks(K);
     const int64_t groups = row_groups(a_rows, E);
-    for (int r = blockIdx.x; r < a_rows; r += gridDim.x) {
-        // the row's loads go out before its expert is looked up
-        const int4 *src = a + (int64_t)r * V;
-        int4 held[kRowsHeld];
+    const int candidates = offsets ? a_rows : E * block_rows;
+    for (int64_t q0 = blockIdx.x; q0 < candidates; q0 += 32 * (int64_t)gridDim.x) {
+        const int64_t mine = q0 + lane * (int64_t)gridDim.x;
+        unsigned used = __ballot_sync(kFull, mine < candidates &&
+                                                 (offsets || (int)mine / E < __ldg(counts + (int)mine % E)));
+        for (; used; used &= used - 1) {
+            const int q = (int)(q0 + (__ffs(used) - 1) * (int64_t)gridDim.x);
+            const int e = offsets ? run_of(offsets, E, q) : q % E;
+            int start, count;
+            bool bad = false;
+            expert_rows(offsets, counts, block_rows, a_rows, e, start, count, bad);
+            const int i = offsets ? q - start : q / E;
+            if (i < 0 || i >= count) continue;      // uniform per CTA
+            const int64_t group = row_group(offsets != nullptr, start, block_rows, e) + (i >> 3);
+            const int r8 = i & 7;
+            const int4 *src = a + (int64_t)(start + i) * V;
+            constexpr int kAhead = FEW ? kRowsAheadFew : kRowsAheadMany;
+            uint32_t top = 0;
+            int4 x[FEW ? 1 : kAhead];               // the row's first vectors, kept if not FEW
+            for (int v0 = tid; v0 < V; v0 += kAhead * kRowsThreads) {
+                int4 y[kAhead];
 #pragma unroll
-        for (int h = 0; h < kRowsHeld; h++) {
-            const int v = tid + h * kRowsThreads;
-            held[h] = v < V ? src[v] : make_int4(0, 0, 0, 0);
+                for (int h = 0; h < kAhead; h++)
+                    y[h] = v0 + h * kRowsThreads < V ? src[v0 + h * kRowsThreads] : make_int4(0, 0, 0, 0);
+#pragma unroll
+                for (int h = 0; h < kAhead; h++) {
+                    top = max(top, abs_max_bits(y[h]));
+                    if (!FEW && v0 == tid) x[h] = y[h];
+                }
+            }
+            top = __reduce_max_sync(kFull, top);
+            __syncthreads();                        // the last row's reads of part[] are over
+            if (lane == 0) part[tid >> 5] = top;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kRowsThreads / 32; w++) top = max(top, part[w]);
+            // 2^shift takes the largest value to [2^14, 2^15); at most 2^127 (rows of
+            // bf16's smallest values stay below, where fp16 still holds all their bits)
+            const int field = (int)(top >> 7);
+            const int shift = min(14 - ((field > 0 ? field : 1) - 127), 127);
+            const float by = __uint_as_float((uint32_t)(shift + 127) << 23);
+            if (tid == 0)
+                row_scale[group * 8 + r8] =
+                    __uint_as_float(shift == 127 ? 0x00400000u : (uint32_t)(127 - shift) << 23);
+            int v = tid;
+            if constexpr (!FEW)
+#pragma unroll
+                for (int h = 0; h < kAhead; h++, v += kRowsThreads)
+                    if (v < padded)
+                        st_cg(row_piece(x16, groups, group, r8, v),
+                              v < V ? scale_to_half8(x[h], by) : make_int4(0, 0, 0, 0));
+            for (; v < padded; v += kRowsThreads)               // (from L1 this time)
+                st_cg(row_piece(x16, groups, group, r8, v),
+                      v < V ? scale_to_half8(src[v], by) : make_int4(0, 0, 0, 0));
         }
-        // the expert whose run or block holds row r
-        int e;
-        if (offsets) {
-            const int step = (E + 31) / 32;
-            const int at = lane * step;
-            const int s = at < E ? __ldg(offsets + at) : 0x7fffffff;
-            const unsigned below = __ballot_sync(kFull, s <= r);
-            const int base = below ? (31 - __clz((int)below)) * step : 0;
-            const int s2 = lane < step && base + lane < E ? __ldg(offsets + base + lane) : 0x7fffffff;
-            const unsigned below2 = __ballot_sync(kFull, s2 <= r);
-            e = base + (below2 ? 31 - __clz((int)below2) : 0);
-        } else {
-            e = r / block_rows;
-            if (e >= E) break;          // rows past the last block
-        }
-        int start, count;
-        bool bad = false;
-        expert_rows(offsets, counts, block_rows, a_rows, e, start, count, bad);
-        const int i = r - start;
-        if (i < 0 || i >= count) continue;      // uniform per CTA
-        const int64_t group = row_group(offsets != nullptr, start, block_rows, e) + (i >> 3);
-        const int r8 = i & 7;
-        uint32_t top = 0;
-#pragma unroll
-        for (int h = 0; h < kRowsHeld; h++) top = max(top, abs_max_bits(held[h]));
-        for (int v = tid + kRowsHeld * kRowsThreads; v < V; v += kRowsThreads)
-            top = max(top, abs_max_bits(src[v]));
-        top = __reduce_max_sync(kFull, top);
-        __syncthreads();                        // the last row's reads of part[] are over
-        if (lane == 0) part[tid >> 5] = top;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kRowsThreads / 32; w++) top = max(top, part[w]);
-        // 2^shift takes the largest value to [2^14, 2^15); at most 2^127 (rows of
-        // bf16's smallest values stay below, where fp16 still holds all their bits)
-        const int field = (int)(top >> 7);
-        const int shift = min(14 - ((field > 0 ? field : 1) - 127), 127);
-        const float by = __uint_as_float((uint32_t)(shift + 127) << 23);
-        if (tid == 0)
-            row_scale[group * 8 + r8] =
-                __uint_as_float(shift == 127 ? 0x00400000u : (uint32_t)(127 - shift) << 23);
-#pragma unroll
-        for (int h = 0; h < kRowsHeld; h++) {
-            const int v = tid + h * kRowsThreads;
-            if (v < padded) st_cg(row_piece(x16, groups, group, r8, v), scale_to_half8(held[h], by));
-        }
-        for (int v = tid + kRowsHeld * kRowsThreads; v < padded; v += kRowsThreads)
-            st_cg(row_piece(x16, groups, group, r8, v),
-                  v < V ? scale_to_half8(src[v], by) : make_int4(0, 0, 0, 0));
     }
 }
 
@@ -900,12 +919,21 @@ cudaError_t launch_expert_w4(const uint16_t *a, int a_rows, const int32_t *offse
     float *partial = (float *)((uint8_t *)row_scale + scale_bytes(a_rows, E));
     int32_t *arrivals = (int32_t *)((uint8_t *)partial + kPartialBytes);
     const int ctas = di.sm_count < kMaxCtas ? di.sm_count : kMaxCtas;
-    const int fit = resident_grid((const void *)k_w4_rows, kRowsThreads, 0);
-    const int most = fit > 0 && fit < 6 * di.sm_count ? fit : 6 * di.sm_count;
+    // Few rows: at most one run row per SM, or blocks, of which a serving step uses a
+    // few rows each (48 x 64 rows with 48 in use: xx us in this form, xx in the other).
+    const bool few = counts ? (int64_t)E * block_rows <= 32 * (int64_t)di.sm_count : a_rows <= di.sm_count;
+    const int most = few ? di.sm_count : kRowsCtasMany * di.sm_count;
     const int grid = a_rows > most ? most : a_rows;
+    if (few) {
+        // (an SM does not change its division of shared memory while a CTA is on it)
+        err = cudaFuncSetAttribute(k_w4_rows<true>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                   cudaSharedmemCarveoutMaxShared);
+        if (err != cudaSuccess) return err;
+    }
     MOE_TRACED_LAUNCH("k_w4_rows", st,
-        err = launch_pdl(k_w4_rows, dim3(grid), dim3(kRowsThreads), 0, st, (const int4 *)a, a_rows,
-                         offsets, counts, block_rows, E, K, x16, row_scale, arrivals, kMaxCtas));
+        err = launch_pdl(few ? k_w4_rows<true> : k_w4_rows<false>, dim3(grid), dim3(kRowsThreads), 0,
+                         st, (const int4 *)a, a_rows, offsets, counts, block_rows, E, K, x16,
+                         row_scale, arrivals, kMaxCtas));
     if (err != cudaSuccess) return err;
     err = cudaFuncSetAttribute(k_expert_w4, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMmSmem);
     if (err != cudaSuccess) return err;
