@@ -87,12 +87,8 @@ __host__ __device__ __forceinline__ int64_t row_groups(int a_rows, int E)
 }
 
 constexpr int kRowsThreads = 128;
-// Two forms.  FEW: at 32 registers one CTA per SM fits beside one of k_expert_w4,
-// which then starts on all SMs at once (else the SMs that hold a row start 3 us after
-// the others).  Not FEW: a thread keeps its part of the row between the two passes,
-// six CTAs per SM, for rows whose bytes are the bound.
-constexpr int kRowsAheadFew = 5, kRowsAheadMany = 4;   // 16-byte loads in flight per thread
-constexpr int kRowsCtasFew = 16, kRowsCtasMany = 6;
+constexpr int kRowsHeld = 4;        // 16-byte vectors of a row that a thread keeps
+constexpr int kRowsCtas = 8;        // CTAs per SM (16,384 rows of 2,048: 189 us for the call; six 191, four 202)
 
 // Operand layout of the rows: chunk c of group g at (c * groups + g) * 2048 bytes,
 // so a tile's rows are one bulk copy per chunk; in each of its two 64-column
@@ -142,8 +138,7 @@ __device__ __forceinline__ int run_of(const int32_t *offsets, int E, int r)
 // One CTA per row, `grid` rows apart.  With blocks, candidate q is row q / E of block
 // q % E, so that the rows in use come first; every warp looks 32 candidates over at
 // once.  Also zeroes the arrival counters of k_expert_w4.
-template <bool FEW>
-__global__ void __launch_bounds__(kRowsThreads, FEW ? kRowsCtasFew : kRowsCtasMany) k_w4_rows(
+__global__ void __launch_bounds__(kRowsThreads, kRowsCtas) k_w4_rows(
     const int4 *__restrict__ a, int a_rows, const int32_t *__restrict__ offsets,
     const int32_t *__restrict__ counts, int block_rows, int E, int K, uint8_t *__restrict__ x16,
     float *__restrict__ row_scale, int32_t *__restrict__ arrivals, int n_arrivals)
@@ -172,20 +167,15 @@ __global__ void __launch_bounds__(kRowsThreads, FEW ? kRowsCtasFew : kRowsCtasMa
             const int64_t group = row_group(offsets != nullptr, start, block_rows, e) + (i >> 3);
             const int r8 = i & 7;
             const int4 *src = a + (int64_t)(start + i) * V;
-            constexpr int kAhead = FEW ? kRowsAheadFew : kRowsAheadMany;
             uint32_t top = 0;
-            int4 x[FEW ? 1 : kAhead];               // the row's first vectors, kept if not FEW
-            for (int v0 = tid; v0 < V; v0 += kAhead * kRowsThreads) {
-                int4 y[kAhead];
+            int4 x[kRowsHeld];                      // the row's first vectors
 #pragma unroll
-                for (int h = 0; h < kAhead; h++)
-                    y[h] = v0 + h * kRowsThreads < V ? src[v0 + h * kRowsThreads] : make_int4(0, 0, 0, 0);
+            for (int h = 0; h < kRowsHeld; h++)
+                x[h] = tid + h * kRowsThreads < V ? src[tid + h * kRowsThreads] : make_int4(0, 0, 0, 0);
 #pragma unroll
-                for (int h = 0; h < kAhead; h++) {
-                    top = max(top, abs_max_bits(y[h]));
-                    if (!FEW && v0 == tid) x[h] = y[h];
-                }
-            }
+            for (int h = 0; h < kRowsHeld; h++) top = max(top, abs_max_bits(x[h]));
+            for (int v = tid + kRowsHeld * kRowsThreads; v < V; v += kRowsThreads)
+                top = max(top, abs_max_bits(src[v]));
             top = __reduce_max_sync(kFull, top);
             __syncthreads();                        // the last row's reads of part[] are over
             if (lane == 0) part[tid >> 5] = top;
@@ -201,12 +191,11 @@ __global__ void __launch_bounds__(kRowsThreads, FEW ? kRowsCtasFew : kRowsCtasMa
                 row_scale[group * 8 + r8] =
                     __uint_as_float(shift == 127 ? 0x00400000u : (uint32_t)(127 - shift) << 23);
             int v = tid;
-            if constexpr (!FEW)
 #pragma unroll
-                for (int h = 0; h < kAhead; h++, v += kRowsThreads)
-                    if (v < padded)
-                        st_cg(row_piece(x16, groups, group, r8, v),
-                              v < V ? scale_to_half8(x[h], by) : make_int4(0, 0, 0, 0));
+            for (int h = 0; h < kRowsHeld; h++, v += kRowsThreads)
+                if (v < padded)
+                    st_cg(row_piece(x16, groups, group, r8, v),
+                          v < V ? scale_to_half8(x[h], by) : make_int4(0, 0, 0, 0));
             for (; v < padded; v += kRowsThreads)               // (from L1 this time)
                 st_cg(row_piece(x16, groups, group, r8, v),
                       v < V ? scale_to_half8(src[v], by) : make_int4(0, 0, 0, 0));
@@ -919,21 +908,11 @@ cudaError_t launch_expert_w4(const uint16_t *a, int a_rows, const int32_t *offse
     float *partial = (float *)((uint8_t *)row_scale + scale_bytes(a_rows, E));
     int32_t *arrivals = (int32_t *)((uint8_t *)partial + kPartialBytes);
     const int ctas = di.sm_count < kMaxCtas ? di.sm_count : kMaxCtas;
-    // Few rows: at most one run row per SM, or blocks, of which a serving step uses a
-    // few rows each (48 x 64 rows with 48 in use: xx us in this form, xx in the other).
-    const bool few = counts ? (int64_t)E * block_rows <= 32 * (int64_t)di.sm_count : a_rows <= di.sm_count;
-    const int most = few ? di.sm_count : kRowsCtasMany * di.sm_count;
+    const int most = kRowsCtas * di.sm_count;
     const int grid = a_rows > most ? most : a_rows;
-    if (few) {
-        // (an SM does not change its division of shared memory while a CTA is on it)
-        err = cudaFuncSetAttribute(k_w4_rows<true>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                   cudaSharedmemCarveoutMaxShared);
-        if (err != cudaSuccess) return err;
-    }
     MOE_TRACED_LAUNCH("k_w4_rows", st,
-        err = launch_pdl(few ? k_w4_rows<true> : k_w4_rows<false>, dim3(grid), dim3(kRowsThreads), 0,
-                         st, (const int4 *)a, a_rows, offsets, counts, block_rows, E, K, x16,
-                         row_scale, arrivals, kMaxCtas));
+        err = launch_pdl(k_w4_rows, dim3(grid), dim3(kRowsThreads), 0, st, (const int4 *)a, a_rows,
+                         offsets, counts, block_rows, E, K, x16, row_scale, arrivals, kMaxCtas));
     if (err != cudaSuccess) return err;
     err = cudaFuncSetAttribute(k_expert_w4, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMmSmem);
     if (err != cudaSuccess) return err;
