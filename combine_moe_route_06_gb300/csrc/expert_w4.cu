@@ -236,6 +236,8 @@ struct MmShared {
     uint64_t done;
     uint32_t tmem;
     int most;                        // largest row tile, in 8-row groups
+    int total, parts;                // chunks of the call, CTAs that share them
+    int base, more;                  // the first `more` CTAs have base + 1 chunks, the rest base
     int last;                        // this CTA arrived last at a cut tile
     volatile int dead;               // a wait gave up
 };
@@ -269,32 +271,16 @@ __device__ __forceinline__ int expert_of(const MmShared &sh, int E, int tiles, i
     return base + 31 - __clz((int)below2);
 }
 
-// `total` chunks cut into B parts: the first `more` have base + 1 of them, the rest base.
-struct Cut {
-    int base, more;
-    __device__ Cut(int total, int B) : base(B ? total / B : 0), more(B ? total - base * B : 0) {}
-    __device__ int start(int b) const { return b * base + min(b, more); }
-    __device__ int owner(int g) const       // the part that holds chunk g
-    {
-        const int longer = more * (base + 1);
-        return g < longer ? g / (base + 1) : more + (g - longer) / base;
-    }
-};
-
 struct WorkShape {
     int E, tiles, chunks, blocks;
 };
 
-__device__ __forceinline__ int total_chunks(const MmShared &sh, const WorkShape &w)
+// The chunk that CTA b starts with, and the CTA that has chunk g.
+__device__ __forceinline__ int first_chunk(const MmShared &sh, int b) { return b * sh.base + min(b, sh.more); }
+__device__ __forceinline__ int owner_of(const MmShared &sh, int g)
 {
-    return sh.before[w.E] * w.tiles * w.chunks;
-}
-// CTAs that take part: all where that leaves each kMinPart chunks; else the tiles are
-// cut into parts of at least that (short tiles not at all).
-__device__ __forceinline__ int parts_of(int total, const WorkShape &w)
-{
-    const int most = max(1, w.chunks / kMinPart), tasks = total / w.chunks;
-    return tasks * most <= (int)gridDim.x ? tasks * most : min(total, (int)gridDim.x);
+    const int longer = sh.more * (sh.base + 1);
+    return g < longer ? g / (sh.base + 1) : sh.more + (g - longer) / sh.base;
 }
 
 // The chunks of this CTA, one tile after the other; for whole warps.
@@ -303,11 +289,11 @@ struct Walk {
     const WorkShape &w;
     int at, to;
     int task, c0;
-    __device__ Walk(const MmShared &s, const WorkShape &shape, const Cut &cut, int B) : sh(s), w(shape)
+    __device__ Walk(const MmShared &s, const WorkShape &shape) : sh(s), w(shape)
     {
         const int b = blockIdx.x;
-        at = b < B ? cut.start(b) : 0;
-        to = b < B ? cut.start(b + 1) : 0;
+        at = b < sh.parts ? first_chunk(sh, b) : 0;
+        to = b < sh.parts ? first_chunk(sh, b + 1) : 0;
         task = at / w.chunks;
         c0 = at - task * w.chunks;
     }
@@ -462,9 +448,10 @@ __device__ __forceinline__ void finish_plain(const Finish &p, int h,
 // By one warp: the experts' rows, and before[e], the row tiles of those before e.
 // Runs could only overlap where the offsets fall: from there on no expert has rows.
 __device__ __forceinline__ void scan_experts(MmShared &sh, const int32_t *offsets,
-                                             const int32_t *counts, int block_rows, int a_rows, int E,
-                                             int blocks, uint32_t *dev_status)
+                                             const int32_t *counts, int block_rows, int a_rows,
+                                             const WorkShape &w, uint32_t *dev_status)
 {
+    const int E = w.E;
     constexpr int kAhead = 4;            // loads in flight
     const int lane = threadIdx.x & 31;
     int tiles_before = 0, most = 0;
@@ -504,7 +491,17 @@ __device__ __forceinline__ void scan_experts(MmShared &sh, const int32_t *offset
     if (lane == 0) {
         sh.before[E] = tiles_before;
         sh.most = most;
-        const int warps = blocks == 2 && most > 8 ? kDecodeWarps : kEpilogueWarps;
+        // Every CTA takes part where that leaves it kMinPart chunks; else the tiles are cut
+        // into parts of at least that (short tiles not at all).
+        const int tasks = tiles_before * w.tiles, total = tasks * w.chunks;
+        const int most_parts = max(1, w.chunks / kMinPart);
+        const int parts = tasks * most_parts <= (int)gridDim.x ? tasks * most_parts
+                                                               : min(total, (int)gridDim.x);
+        sh.total = total;
+        sh.parts = parts;
+        sh.base = parts ? total / parts : 0;
+        sh.more = parts ? total - sh.base * parts : 0;
+        const int warps = w.blocks == 2 && most > 8 ? kDecodeWarps : kEpilogueWarps;
         mbar_init(&sh.sums_empty[0], warps);
         mbar_init(&sh.sums_empty[1], warps);
         mbar_init_fence();
@@ -517,8 +514,7 @@ __device__ __forceinline__ void scan_experts(MmShared &sh, const int32_t *offset
 __device__ __forceinline__ void load_weights(MmShared &sh, uint8_t *wring, const uint8_t *w4,
                                              const WorkShape &w)
 {
-    const int total = total_chunks(sh, w), B = parts_of(total, w);
-    Walk walk(sh, w, Cut(total, B), B);
+    Walk walk(sh, w);
     Segment g;
     int s = 0;
     uint32_t phase = 0, issued = 0;
@@ -544,11 +540,131 @@ __device__ __forceinline__ void load_weights(MmShared &sh, uint8_t *wring, const
     if (!ok) drain(sh.w_full, kWStages, s, phase, issued);
 }
 
-__global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
-    const uint8_t *__restrict__ w4, const float *__restrict__ factor, const uint8_t *x16,
-    const float *row_scale, float *partial, int32_t *arrivals, const int32_t *__restrict__ offsets,
-    const int32_t *__restrict__ counts, int block_rows, int a_rows, int E, int N, int K, bool gated,
-    __nv_bfloat16 *y, uint32_t *dev_status)
+struct MmArgs {
+    const uint8_t *w4;
+    const float *factor;
+    const uint8_t *x16;
+    const float *row_scale;
+    float *partial;
+    int32_t *arrivals;
+    const int32_t *offsets, *counts;
+    int block_rows, a_rows, E, N, K;
+    bool gated;
+    __nv_bfloat16 *y;
+    uint32_t *dev_status;
+};
+
+// One block of a thread's weight row out of shared memory (q, sc) into 64 columns of
+// its tensor-memory lane: code times scale, exact in fp16.
+__device__ __forceinline__ void decode_block(const uint4 (&q)[4], uint2 sc, uint32_t a_at)
+{
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const uint32_t s4 = h ? sc.y : sc.x;
+        const uint32_t s01 = e4m3x2_to_half2(s4), s23 = e4m3x2_to_half2(s4 >> 16);
+        const uint32_t group_scale[4] = {__byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232),
+                                         __byte_perm(s23, 0, 0x1010), __byte_perm(s23, 0, 0x3232)};
+        const uint32_t word[8] = {q[2 * h].x,     q[2 * h].y,     q[2 * h].z,     q[2 * h].w,
+                                  q[2 * h + 1].x, q[2 * h + 1].y, q[2 * h + 1].z, q[2 * h + 1].w};
+        uint32_t out[32];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            uint32_t half2s[4];
+            e2m1x8_to_half2(word[i], half2s);
+#pragma unroll
+            for (int j = 0; j < 4; j++) out[4 * i + j] = mul_half2(half2s[j], group_scale[i >> 1]);
+        }
+        tmem_store32(a_at + h * 32, out);
+    }
+    tmem_wait_st();
+}
+
+// The end of a segment, by `teams` teams of four warps: waits for its sums (stage d of
+// them, at `sums` in this warp's lanes, the second block's `second` columns on) and
+// writes the tile's outputs, or this part of a cut tile's sums to memory.  A thread has
+// one row of each of the tile's blocks.  (Inlined: as a function of its own it made the
+// whole kernel a quarter slower, as does any variant that takes local memory.)
+__device__ __forceinline__ bool finish_segment(const MmArgs &p, MmShared &sh, const WorkShape &w, Segment g,
+                                            uint32_t sums, int second, int d, uint32_t parity, int team,
+                                            int teams, bool ok)
+{
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
+    const int row = quarter * 32 + lane;
+    const float f = __ldg(p.factor + g.e);
+    const int64_t scale0 =
+        (int64_t)row_group(p.offsets != nullptr, sh.start[g.e], p.block_rows, g.e) * 8 + g.row0;
+    __nv_bfloat16 *out = p.y + (int64_t)(sh.start[g.e] + g.row0) * p.N;
+    int first = 0, parts = 1;
+    if (g.c1 - g.c0 < w.chunks) {
+        first = owner_of(sh, g.task * w.chunks);
+        parts = owner_of(sh, g.task * w.chunks + w.chunks - 1) - first + 1;
+    }
+    float scale[kMaxRowsTile / 32];      // of rows lane, lane + 32, ... of the tile
+#pragma unroll
+    for (int i = 0; i < kMaxRowsTile / 32; i++)
+        scale[i] = lane + 32 * i < g.rows ? __ldcg(p.row_scale + scale0 + lane + 32 * i) : 0.f;
+    // where the other part of a tile cut in two is in memory already, its first columns
+    const bool early = parts > 1 && arrived(p.arrivals + first) == parts - 1;
+    const int other = blockIdx.x == first ? first + 1 : first;
+    float ahead[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            ahead[h][j] = early && parts == 2 && h < w.blocks
+                              ? __ldcg(p.partial + (2 * other + (other == first)) * kPart +
+                                       (h * kMaxRowsTile + j) * kW4Tile + row)
+                              : 0.f;
+    // one answer for all the warps, which meet at barriers below
+    if (!named_all(1, teams * 128, ok && mbar_wait(&sh.sums_full[d], parity, &sh.dead))) return false;
+    tmem_fence_after();
+    // a cut tile: its last part to be done is summed here with the others' from memory, any
+    // other part goes there
+    bool finish = true, held = true;       // held: this part's sums are in tensor memory only
+    if (parts > 1 &&
+        !(finish = named_all(1, teams * 128, early || arrived(p.arrivals + first) == parts - 1))) {
+        held = false;
+        float *slot = p.partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * kPart;
+        for (int h = 0; h < w.blocks; h++)
+            for (int c0 = team * 8; c0 < g.rows; c0 += teams * 8) {
+                float v[8];
+                tmem_load(sums + h * second + c0, v);
+#pragma unroll
+                for (int j = 0; j < 8; j++) __stcg(slot + (h * kMaxRowsTile + c0 + j) * kW4Tile + row, v[j]);
+            }
+        __threadfence();
+        named_barrier(1, teams * 128);
+        if (team == 0 && row == 0) sh.last = atomicAdd(p.arrivals + first, 1) == parts - 1;
+        named_barrier(1, teams * 128);
+        finish = sh.last;
+        __threadfence();
+    }
+    if (finish) {
+        const Finish fin{sums, second, p.partial + (int64_t)2 * first * kPart + row, parts,
+                         held ? (int)blockIdx.x - first : -1, early && parts == 2, f, g.rows, team, teams};
+        if (p.gated) {
+            const int n = w4_output(g.tile, 0, row, p.N, true);
+            if (parts > 1) finish_gated<8, true>(fin, scale, ahead, out + n, p.N, n < p.N);
+            else if (g.rows <= 8) finish_gated<8, false>(fin, scale, ahead, out + n, p.N, n < p.N);
+            else finish_gated<16, false>(fin, scale, ahead, out + n, p.N, n < p.N);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                if (h == w.blocks) break;
+                const int n = w4_output(g.tile, h, row, p.N, false);
+                if (parts > 1) finish_plain<8, true>(fin, h, scale, ahead, out + n, p.N, n < p.N);
+                else if (g.rows <= 8) finish_plain<8, false>(fin, h, scale, ahead, out + n, p.N, n < p.N);
+                else finish_plain<16, false>(fin, h, scale, ahead, out + n, p.N, n < p.N);
+            }
+        }
+    }
+    tmem_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.sums_empty[d]);
+    return true;
+}
+
+__global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(const __grid_constant__ MmArgs p)
 {
     extern __shared__ uint8_t raw[];
     uint8_t *xring = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
@@ -556,13 +672,13 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
     MmShared &sh = *(MmShared *)(wring + kWStages * kW4BlockBytes);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kFull, tid >> 5, 0);
-    const int tiles = w4_tiles(N, gated), chunks = w4_chunks(K), blocks = w4_blocks(N, gated);
+    const int tiles = w4_tiles(p.N, p.gated), chunks = w4_chunks(p.K), blocks = w4_blocks(p.N, p.gated);
 
     // The row counts are older than k_w4_rows, which has passed its own wait when
     // this kernel starts: they and the weights may be read before pdl_wait.
     pdl_trigger();
     volatile int *dead = &sh.dead;
-    const WorkShape shape{E, tiles, chunks, blocks};
+    const WorkShape shape{p.E, tiles, chunks, blocks};
     if (warp == kWarpW) {
         // ---- weight blocks, one bulk copy each.  This warp first finds out what there is to do,
         // in shared memory for all.
@@ -572,9 +688,9 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
         }
         if (lane == 0) sh.dead = 0;
         mbar_init_fence();
-        scan_experts(sh, offsets, counts, block_rows, a_rows, E, blocks, dev_status);
+        scan_experts(sh, p.offsets, p.counts, p.block_rows, p.a_rows, shape, p.dev_status);
         named_barrier(2, kMmThreads);
-        load_weights(sh, wring, w4, shape);
+        load_weights(sh, wring, p.w4, shape);
         __syncthreads();
         return;
     }
@@ -598,9 +714,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
     tmem_fence_after();
 
     const uint32_t tmem = sh.tmem;
-    const int total = total_chunks(sh, shape), B = parts_of(total, shape);
-    const Cut cut(total, B);
-    Walk walk(sh, shape, cut, B);
+    Walk walk(sh, shape);
     Segment g;
     bool ok = true;
     // a stage of row operands holds up to four chunks, as many as leave three stages or more
@@ -615,16 +729,16 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
     const bool large = blocks == 2 && sh.most > 8;
     const int sums_stages = large ? 1 : 2;
     const int second = large ? kMaxRowsTile : kMaxRowsTile / 2;
-    const bool runs = offsets != nullptr;
+    const bool runs = p.offsets != nullptr;
 
     if (warp == kWarpX) {
         // ---- row operands: one bulk copy per chunk, one barrier per stage
         pdl_wait();
-        const int64_t groups = row_groups(a_rows, E);
+        const int64_t groups = row_groups(p.a_rows, p.E);
         int s = 0;
         uint32_t phase = 0, issued = 0;
         while (ok && walk.next(g)) {
-            const int64_t group0 = row_group(runs, sh.start[g.e], block_rows, g.e) + g.row0 / 8;
+            const int64_t group0 = row_group(runs, sh.start[g.e], p.block_rows, g.e) + g.row0 / 8;
             const uint32_t bytes = (g.rows + 7) / 8 * kGroupBytes;
             for (int c = g.c0; c < g.c1; c += x_chunks) {
                 const int n = min(x_chunks, g.c1 - c);
@@ -633,7 +747,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
                     mbar_expect(&sh.x_full[s], n * bytes);
                     for (int i = 0; i < n; i++)
                         bulk_load(xring + s * x_stage_bytes + i * tile_bytes,
-                                  x16 + ((c + i) * groups + group0) * kGroupBytes, bytes,
+                                  p.x16 + ((c + i) * groups + group0) * kGroupBytes, bytes,
                                   &sh.x_full[s]);
                 }
                 __syncwarp();
@@ -699,11 +813,9 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
         for (int n = 0; n < 100000 && !mbar_try(&sh.done, 0); n++) {}
     } else {
         // ---- decode: team t of four warps (one per quarter of the tensor-memory lanes, a row
-        // a lane) has every kAStages-th block and A stage t.  Epilogue: a thread has one row
-        // of each of the tile's blocks.
+        // a lane) has every kAStages-th block and A stage t.  Then the tile's outputs.
         const bool decodes = warp < kDecodeWarps, finishes = large ? decodes : !decodes;
         const int quarter = warp & 3, team = decodes ? warp >> 2 : 0;
-        const int finishers = large ? kDecodeWarps * 32 : kEpilogueWarps * 32;
         const int row = quarter * 32 + lane;
         const uint32_t at_lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t a_at = at_lanes + kAFirst + team * kAColumns;
@@ -712,7 +824,6 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
         int mine = team, seen = 0;   // that block's number; blocks of the segments so far
         int d = 0;
         uint32_t pd = 0;
-        if (!decodes) pdl_wait();
         while (ok && walk.next(g)) {
             seen += (g.c1 - g.c0) * blocks;
             for (; decodes && mine < seen; mine += kAStages) {
@@ -732,111 +843,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
                 if (!(ok = mbar_wait_warp(&sh.a_empty[team], pa ^ 1, dead))) break;
                 pa ^= 1;
                 tmem_fence_after();
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const uint32_t s4 = h ? sc.y : sc.x;
-                    const uint32_t s01 = e4m3x2_to_half2(s4), s23 = e4m3x2_to_half2(s4 >> 16);
-                    const uint32_t group_scale[4] = {
-                        __byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232),
-                        __byte_perm(s23, 0, 0x1010), __byte_perm(s23, 0, 0x3232)};
-                    const uint32_t word[8] = {q[2 * h].x,     q[2 * h].y,     q[2 * h].z,
-                                              q[2 * h].w,     q[2 * h + 1].x, q[2 * h + 1].y,
-                                              q[2 * h + 1].z, q[2 * h + 1].w};
-                    uint32_t out[32];
-#pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        uint32_t half2s[4];
-                        e2m1x8_to_half2(word[i], half2s);
-#pragma unroll
-                        for (int p = 0; p < 4; p++)
-                            out[4 * i + p] = mul_half2(half2s[p], group_scale[i >> 1]);
-                    }
-                    tmem_store32(a_at + h * 32, out);
-                }
-                tmem_wait_st();
+                decode_block(q, sc, a_at);
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.a_full[team]);
             }
             if (!finishes) continue;
-            if (decodes) pdl_wait();
-            const float f = __ldg(factor + g.e);
-            const int64_t scale0 =
-                (int64_t)row_group(runs, sh.start[g.e], block_rows, g.e) * 8 + g.row0;
-            __nv_bfloat16 *out = y + (int64_t)(sh.start[g.e] + g.row0) * N;
-            int first = 0, parts = 1;
-            if (g.c1 - g.c0 < chunks) {
-                first = cut.owner(g.task * chunks);
-                parts = cut.owner(g.task * chunks + chunks - 1) - first + 1;
-            }
-            float scale[kMaxRowsTile / 32];      // of rows lane, lane + 32, ... of the tile
-#pragma unroll
-            for (int i = 0; i < kMaxRowsTile / 32; i++)
-                scale[i] = lane + 32 * i < g.rows ? __ldcg(row_scale + scale0 + lane + 32 * i) : 0.f;
-            // where the other part of a tile cut in two is in memory already, its first block
-            const bool early = parts > 1 && arrived(arrivals + first) == parts - 1;
-            const int other = blockIdx.x == first ? first + 1 : first;
-            float ahead[2][8];
-#pragma unroll
-            for (int h = 0; h < 2; h++)
-#pragma unroll
-                for (int j = 0; j < 8; j++)
-                    ahead[h][j] = early && parts == 2 && h < blocks
-                                      ? __ldcg(partial + (2 * other + (other == first)) * kPart +
-                                               (h * kMaxRowsTile + j) * kW4Tile + row)
-                                      : 0.f;
-            const uint32_t sums = at_lanes + d * kMaxRowsTile;
-            // one answer for all the warps, which meet at barriers below
-            if (!(ok = named_all(1, finishers, ok && mbar_wait(&sh.sums_full[d], pd, dead)))) break;
-            tmem_fence_after();
-            // a cut tile: its last part to be done is summed here with the others' from
-            // memory, any other part goes there
-            bool finish = true, held = true;       // held: this part's sums are in tensor memory only
-            if (parts > 1 &&
-                !(finish = named_all(1, finishers,
-                                     early || arrived(arrivals + first) == parts - 1))) {
-                held = false;
-                float *slot = partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * kPart;
-                for (int h = 0; h < blocks; h++)
-                    for (int c0 = team * 8; c0 < g.rows; c0 += finishers / 128 * 8) {
-                        float v[8];
-                        tmem_load(sums + h * second + c0, v);
-#pragma unroll
-                        for (int j = 0; j < 8; j++)
-                            __stcg(slot + (h * kMaxRowsTile + c0 + j) * kW4Tile + row, v[j]);
-                    }
-                __threadfence();
-                named_barrier(1, finishers);
-                if (team == 0 && quarter == 0 && lane == 0)
-                    sh.last = atomicAdd(arrivals + first, 1) == parts - 1;
-                named_barrier(1, finishers);
-                finish = sh.last;
-                __threadfence();
-            }
-            if (finish) {
-                const Finish fin{sums, second, partial + (int64_t)2 * first * kPart + row, parts,
-                                 held ? (int)blockIdx.x - first : -1, early && parts == 2, f, g.rows,
-                                 team, finishers / 128};
-                if (gated) {
-                    const int n = w4_output(g.tile, 0, row, N, true);
-                    if (parts > 1) finish_gated<8, true>(fin, scale, ahead, out + n, N, n < N);
-                    else if (g.rows <= 8) finish_gated<8, false>(fin, scale, ahead, out + n, N, n < N);
-                    else finish_gated<16, false>(fin, scale, ahead, out + n, N, n < N);
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        if (h == blocks) break;
-                        const int n = w4_output(g.tile, h, row, N, false);
-                        if (parts > 1) finish_plain<8, true>(fin, h, scale, ahead, out + n, N, n < N);
-                        else if (g.rows <= 8)
-                            finish_plain<8, false>(fin, h, scale, ahead, out + n, N, n < N);
-                        else finish_plain<16, false>(fin, h, scale, ahead, out + n, N, n < N);
-                    }
-                }
-            }
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.sums_empty[d]);
+            pdl_wait();          // what k_w4_rows wrote, the cut tiles' parts, and y
+            ok = finish_segment(p, sh, shape, g, at_lanes + d * kMaxRowsTile, second, d, pd, team,
+                                large ? kAStages : 1, ok);
             if (++d == sums_stages) {
                 d = 0;
                 pd ^= 1;
@@ -845,7 +860,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(
     }
     __syncthreads();
     if (warp == kWarpMma) {
-        if (sh.dead && lane == 0) flag_status(dev_status, MOE_ERR_TIMEOUT);
+        if (sh.dead && lane == 0) flag_status(p.dev_status, MOE_ERR_TIMEOUT);
         tmem_fence_after();
         tmem_free(tmem, kTmemColumns);
     }
@@ -917,9 +932,9 @@ cudaError_t launch_expert_w4(const uint16_t *a, int a_rows, const int32_t *offse
     err = cudaFuncSetAttribute(k_expert_w4, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMmSmem);
     if (err != cudaSuccess) return err;
     MOE_TRACED_LAUNCH("k_expert_w4", st,
-        err = launch_pdl(k_expert_w4, dim3(ctas), dim3(kMmThreads), kMmSmem, st, w4, factor,
-                         (const uint8_t *)x16, (const float *)row_scale, partial, arrivals, offsets,
-                         counts, block_rows, a_rows, E, N, K, gated, (__nv_bfloat16 *)y, dev_status));
+        err = launch_pdl(k_expert_w4, dim3(ctas), dim3(kMmThreads), kMmSmem, st,
+                         MmArgs{w4, factor, x16, row_scale, partial, arrivals, offsets, counts,
+                                block_rows, a_rows, E, N, K, gated, (__nv_bfloat16 *)y, dev_status}));
     return err;
 }
 
