@@ -206,12 +206,14 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) k_w4_rows(
 // ---------------------------------------------------------------- the product
 
 constexpr int kAStages = 4;                         // decoded blocks in tensor memory
-constexpr int kDecodeWarps = 4 * kAStages;          // a team of four per decoded block
+constexpr int kTeams = 3;                           // teams of four warps that decode
+constexpr int kDecodeWarps = 4 * kTeams;
 constexpr int kEpilogueWarps = 4;
 constexpr int kWarpW = kDecodeWarps + kEpilogueWarps, kWarpX = kWarpW + 1, kWarpMma = kWarpW + 2;
 constexpr int kMmThreads = (kWarpMma + 1) * 32;     // the last three: weight loads, row loads, MMA
 constexpr int kMaxRowsTile = 128;                   // rows of `a` per tile
-constexpr int kWStages = 11;                        // 9 KiB weight blocks in flight
+constexpr int kWStages = 11;                        // 9 KiB weight blocks in flight (18: slower, the
+                                                    // first rows come later through the weights)
 constexpr int kXBytes = 96 * 1024;                  // ring of row operands
 constexpr int kXStagesMax = 12;
 constexpr int kAColumns = kW4Chunk / 2;             // 64 columns a block
@@ -222,9 +224,9 @@ constexpr int kMinPart = 12;                        // chunks worth a part of th
 constexpr int kGroupBytes = kW4Chunk / 64 * 1024;   // an 8-row group's chunk: 2 KiB
 
 // A barrier wait tells a phase from the one two before it only by the order of
-// events.  A team at chunk j has seen the MMAs of chunk j - 2 kAStages end, so a
-// weight stage must come round no sooner than that.
-static_assert(kWStages >= 2 * kAStages, "weight stages come round too soon for the teams' waits");
+// events.  A team that waits for weight block j has seen the MMAs of block
+// j - kTeams - kAStages end, so a weight stage must come round no sooner than that.
+static_assert(kWStages >= kTeams + kAStages, "weight stages come round too soon for the teams' waits");
 
 struct MmShared {
     uint64_t w_full[kWStages], w_empty[kWStages];
@@ -501,7 +503,7 @@ __device__ __forceinline__ void scan_experts(MmShared &sh, const int32_t *offset
         sh.parts = parts;
         sh.base = parts ? total / parts : 0;
         sh.more = parts ? total - sh.base * parts : 0;
-        const int warps = w.blocks == 2 && most > 8 ? kDecodeWarps : kEpilogueWarps;
+        const int warps = (w.blocks == 2 && most > 8 ? kDecodeWarps : 0) + kEpilogueWarps;
         mbar_init(&sh.sums_empty[0], warps);
         mbar_init(&sh.sums_empty[1], warps);
         mbar_init_fence();
@@ -717,15 +719,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(const __grid_consta
     Walk walk(sh, shape);
     Segment g;
     bool ok = true;
-    // a stage of row operands holds up to four chunks, as many as leave three stages or more
+    // a stage of row operands holds two chunks where that leaves three stages or more
     const int tile_bytes = max(1, sh.most) * kGroupBytes;
-    const int x_chunks = 12 * tile_bytes <= kXBytes ? 4 : 6 * tile_bytes <= kXBytes ? 2 : 1;
+    const int x_chunks = 6 * tile_bytes <= kXBytes ? 2 : 1;
     const int x_stage_bytes = x_chunks * tile_bytes;
     const int x_stages = min(kXStagesMax, kXBytes / x_stage_bytes);
     // sums: two tiles of 128 columns in turn, the blocks' 64 columns apart in them, which
     // the epilogue warps finish while the next tile is summed; two blocks with more than
     // 64 rows of `a` take all 256 columns, and the decode warps, which then have nothing
-    // to decode into, finish the tile (16 warps take a quarter of the time of four)
+    // to decode into, help to finish the tile (16 warps take a quarter of the time of four)
     const bool large = blocks == 2 && sh.most > 8;
     const int sums_stages = large ? 1 : 2;
     const int second = large ? kMaxRowsTile : kMaxRowsTile / 2;
@@ -813,20 +815,19 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(const __grid_consta
         for (int n = 0; n < 100000 && !mbar_try(&sh.done, 0); n++) {}
     } else {
         // ---- decode: team t of four warps (one per quarter of the tensor-memory lanes, a row
-        // a lane) has every kAStages-th block and A stage t.  Then the tile's outputs.
-        const bool decodes = warp < kDecodeWarps, finishes = large ? decodes : !decodes;
-        const int quarter = warp & 3, team = decodes ? warp >> 2 : 0;
+        // a lane) has every kTeams-th block.  Then the tile's outputs.
+        const bool decodes = warp < kDecodeWarps, finishes = large || !decodes;
+        const int quarter = warp & 3, team = decodes || large ? warp >> 2 : 0;
         const int row = quarter * 32 + lane;
         const uint32_t at_lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-        const uint32_t a_at = at_lanes + kAFirst + team * kAColumns;
         int sw = team;               // stage of the team's next block
-        uint32_t pw = 0, pa = 0;
+        uint32_t pw = 0;
         int mine = team, seen = 0;   // that block's number; blocks of the segments so far
         int d = 0;
         uint32_t pd = 0;
         while (ok && walk.next(g)) {
             seen += (g.c1 - g.c0) * blocks;
-            for (; decodes && mine < seen; mine += kAStages) {
+            for (; decodes && mine < seen; mine += kTeams) {
                 if (!(ok = mbar_wait_warp(&sh.w_full[sw], pw, dead))) break;
                 const uint8_t *block = wring + sw * kW4BlockBytes;
                 uint4 q[4];
@@ -835,23 +836,23 @@ __global__ void __launch_bounds__(kMmThreads, 1) k_expert_w4(const __grid_consta
                 const uint2 sc = *(const uint2 *)(block + kW4CodeBytes + row * 8);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.w_empty[sw]);
-                sw += kAStages;
+                sw += kTeams;
                 if (sw >= kWStages) {
                     sw -= kWStages;
                     pw ^= 1;
                 }
-                if (!(ok = mbar_wait_warp(&sh.a_empty[team], pa ^ 1, dead))) break;
-                pa ^= 1;
+                const int sa = mine % kAStages;
+                if (!(ok = mbar_wait_warp(&sh.a_empty[sa], (mine / kAStages & 1) ^ 1, dead))) break;
                 tmem_fence_after();
-                decode_block(q, sc, a_at);
+                decode_block(q, sc, at_lanes + kAFirst + sa * kAColumns);
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.a_full[team]);
+                if (lane == 0) mbar_arrive(&sh.a_full[sa]);
             }
             if (!finishes) continue;
             pdl_wait();          // what k_w4_rows wrote, the cut tiles' parts, and y
             ok = finish_segment(p, sh, shape, g, at_lanes + d * kMaxRowsTile, second, d, pd, team,
-                                large ? kAStages : 1, ok);
+                                large ? kTeams + 1 : 1, ok);
             if (++d == sums_stages) {
                 d = 0;
                 pd ^= 1;

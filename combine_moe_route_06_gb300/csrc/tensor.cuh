@@ -47,7 +47,7 @@ __device__ __forceinline__ bool mbar_try(uint64_t *bar, uint32_t parity)
 // Waits until the barrier's phase `parity` is over.  Every wait ends: after
 // kWaitLimitNs, or when another thread of the CTA has given up (*dead), the wait
 // returns false and *dead is set.
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kWaitLimitNs = 5000000000ull;
 __device__ __forceinline__ uint64_t global_ns()
 {
     uint64_t t;

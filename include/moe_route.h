@@ -82,6 +82,9 @@
  *                                           written out of bounds (section 4.3,
  *                                           9.2: the cap)
  *     MOE_STATUS_BIT(MOE_ERR_BAD_EXPERT_ID) an id >= E was skipped
+ *     MOE_STATUS_BIT(MOE_ERR_TIMEOUT)       moe_expert_product_w4 only: a wait inside
+ *                                           the kernel gave up after 5 s and its
+ *                                           outputs are not to be used
  *   The library only sets bits; the caller clears the word when it wants.
  *   `dev_status` may be NULL, in which case data errors are not reported.
  * - Results are deterministic: the same inputs give the same bytes.
