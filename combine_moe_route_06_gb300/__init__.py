@@ -3,7 +3,8 @@
 The five calls of the MoE token path (route, dispatch layout, pack, receiver
 permute, combine) run in hand-written sm_103a kernels behind a C ABI
 (``include/moe_route.h``).  This module only marshals torch tensors (device
-pointers, sizes, the current CUDA stream) through ctypes; PyTorch supplies
+pointers, sizes, the current CUDA stream) through ctypes, or for the training
+and 4-bit expert calls through compiled entry points; PyTorch supplies
 device memory and streams.  There is no fallback: if the library is not
 built, importing works but every call raises ``MoeLibraryMissing``.
 
