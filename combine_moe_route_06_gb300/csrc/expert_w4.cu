@@ -93,6 +93,7 @@ __host__ __device__ __forceinline__ int64_t row_groups(int a_rows, int E)
 }
 
 constexpr int kRowsThreads = 128;
+constexpr int kRowsUnseen = 512;    // rows that are read before it is known whether they are used
 constexpr int kRowsHeld = 4;        // 16-byte vectors of a row that a thread keeps
 constexpr int kRowsCtas = 8;        // CTAs per SM (16,384 rows of 2,048: 189 us for the call; six 191, four 202)
 
@@ -158,28 +159,37 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) k_w4_rows(
     const int V = K / 8, padded = 16 * w4_chunks(K);
     const int64_t groups = row_groups(a_rows, E);
     const int candidates = offsets ? a_rows : E * block_rows;
+    // rows past every run are not read, unless they are few: a load less to wait for
+    int end = candidates;
+    if (offsets && a_rows > kRowsUnseen) {
+        int most = 0;
+        for (int i = lane; i <= E; i += 32) most = max(most, __ldg(offsets + i));
+        end = min(a_rows, __reduce_max_sync(kFull, most));
+    }
     for (int64_t q0 = blockIdx.x; q0 < candidates; q0 += 32 * (int64_t)gridDim.x) {
         const int64_t mine = q0 + lane * (int64_t)gridDim.x;
-        unsigned used = __ballot_sync(kFull, mine < candidates &&
-                                                 (offsets || (int)mine / E < __ldg(counts + (int)mine % E)));
+        unsigned used = __ballot_sync(kFull, mine < end && (offsets || (int)mine / E <
+                                                                           __ldg(counts + (int)mine % E)));
         for (; used; used &= used - 1) {
             const int q = (int)(q0 + (__ffs(used) - 1) * (int64_t)gridDim.x);
-            const int e = offsets ? run_of(offsets, E, q) : q % E;
-            int start, count;
-            bool bad = false;
-            expert_rows(offsets, counts, block_rows, a_rows, e, start, count, bad);
-            const int i = offsets ? q - start : q / E;
-            if (i < 0 || i >= count) continue;      // uniform per CTA
-            const int64_t group = row_group(offsets != nullptr, start, block_rows, e) + (i >> 3);
-            const int r8 = i & 7;
-            const int4 *src = a + (int64_t)(start + i) * V;
-            uint32_t top = 0;
+            const int at = offsets ? q : q % E * block_rows + q / E;
+            const int4 *src = a + (int64_t)at * V;
             int4 x[kRowsHeld];                      // the row's first vectors
 #pragma unroll
             for (int h = 0; h < kRowsHeld; h++)
                 x[h] = tid + h * kRowsThreads < V ? src[tid + h * kRowsThreads] : make_int4(0, 0, 0, 0);
+            const int e = offsets ? run_of(offsets, E, q) : q % E;
+            int start, count;
+            bool bad = false;
+            expert_rows(offsets, counts, block_rows, a_rows, e, start, count, bad);
+            const int i = at - start;
+            if (i < 0 || i >= count) continue;      // uniform per CTA
+            const int64_t group = row_group(offsets != nullptr, start, block_rows, e) + (i >> 3);
+            const int r8 = i & 7;
+            uint32_t top = 0;
 #pragma unroll
             for (int h = 0; h < kRowsHeld; h++) top = max(top, abs_max_bits(x[h]));
+#pragma unroll 4
             for (int v = tid + kRowsHeld * kRowsThreads; v < V; v += kRowsThreads)
                 top = max(top, abs_max_bits(src[v]));
             top = __reduce_max_sync(kFull, top);

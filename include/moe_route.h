@@ -751,7 +751,8 @@ moe_status_t moe_w4_pack(const uint8_t *codes, const uint8_t *scales, int E, int
  *   ws       moe_expert_product_w4_workspace_bytes(a_rows, E, N, K) bytes,
  *            256-byte aligned.
  * Rows of y outside the experts' rows are not written.  Row ranges that leave
- * [0, a_rows) are cut to it and flag MOE_ERR_INVALID_ARG.  A NaN or infinity in
+ * [0, a_rows) are cut to it and flag MOE_ERR_INVALID_ARG; offsets that fall flag
+ * it too, and then what y holds in the runs is not to be used.  A NaN or infinity in
  * a row of `a` reaches only that row of y.
  */
 size_t moe_expert_product_w4_workspace_bytes(int a_rows, int E, int N, int K);

@@ -219,6 +219,19 @@ def test_bad_row_ranges_are_cut_and_flagged():
 
 
 @gpu
+@pytest.mark.parametrize("spare", [0, 700])
+def test_falling_offsets(spare):
+    """Offsets that fall are flagged; what is in no run of theirs is not written."""
+    E, N, K = 4, 40, 96
+    codes, scales, factor = make_weights(E, N, K, seed=12)
+    a = rows_of(13, 60 + spare, K)
+    y, status = product(a, pack(codes, scales, False), factor, N, False, offsets=[2, 20, 50, 4, 30])
+    assert status == m.status_bit(m.MOE_ERR_INVALID_ARG)
+    y = ms.f32_from_bf16_bits(y)
+    assert np.all(y[:2] == -7) and np.all(y[50:] == -7)
+
+
+@gpu
 def test_empty_calls():
     codes, scales, factor = make_weights(2, 32, 64, seed=8)
     w4 = pack(codes, scales, False)
