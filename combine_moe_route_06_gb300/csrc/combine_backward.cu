@@ -25,7 +25,8 @@ constexpr int kCbWarps = kCbThreads / 32;
 constexpr int kCbCtas = 2;    // CTAs per SM: 128 registers a thread
 // Rows of a token taken at once, where a token has more than two rows on average
 // or not.  4,096 tokens x 6 rows of 5,120: 92.9 us at eight, 102.7 at two; 16,384
-// tokens x one row of 2,048 (of 8 picks): 37.4 us at two, 59.7 at eight.
+// tokens x one row of 2,048 (of 8 picks): 37.4 us at two, 59.7 at eight (34.0 at two
+// since warps take tokens as they come free).
 constexpr int kManyRows = 8, kFewRows = 2;
 
 __device__ __forceinline__ float dot_bf16x8(int4 a, int4 b, float acc)
@@ -133,23 +134,41 @@ __global__ void __launch_bounds__(kCbThreads, kCbCtas) k_combine_backward(
     const int lane = threadIdx.x & 31, member = TEAM > 1 ? threadIdx.x >> 5 : 0;
     const int64_t gwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
     const int64_t gw = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    const int64_t stride = gwarps / TEAM;
-    // the next token's rows and weights are loaded while this one's are worked on
+    // The CTA's tokens are n0 .. n1 - 1, one warp each (TEAM 1: the warp that is free next,
+    // since tokens have different numbers of rows; a fixed share of them left the last
+    // warps with twice the mean).  The next token's rows and weights are loaded while this
+    // one's are worked on.
+    __shared__ int taken;
+    if (TEAM == 1 && threadIdx.x == 0) taken = kCbWarps;
+    const unsigned base = (unsigned)N / gridDim.x, more = (unsigned)N - base * gridDim.x;   // N < 2^31
+    const int64_t n0 = (int64_t)blockIdx.x * base + min(blockIdx.x, more);
+    const int64_t n1 = n0 + base + (blockIdx.x < more);
+    int64_t next = n0 + (TEAM == 1 ? threadIdx.x >> 5 : 0);
+    auto take = [&]() {
+        if (TEAM > 1) return next + 1;
+        if (n1 - n0 <= kCbWarps) return n1;      // one each
+        int t = 0;
+        if (lane == 0) t = atomicAdd(&taken, 1);
+        return n0 + __shfl_sync(kFull, t, 0);
+    };
     int next_row = -1;
     float next_w = 0.f;
     auto load = [&](int64_t n) {
         next_row = -1;
         next_w = 0.f;
-        if (n < N && lane < k) {
+        if (n < n1 && lane < k) {
             next_row = __ldg(pair_row + n * k + lane);
             next_w = __ldg(w + n * k + lane);
         }
     };
-    load(gw / TEAM);
-    for (int64_t n = gw / TEAM; n < N; n += stride) {
+    load(next);
+    __syncthreads();
+    while (next < n1) {
+        const int64_t n = next;
         int pr = next_row;
         const float wj = next_w;
-        load(n + stride);
+        next = take();
+        load(next);
         if (pr >= y_rows) {
             bad_row = true;
             pr = -1;
