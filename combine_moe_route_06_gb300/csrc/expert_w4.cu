@@ -22,7 +22,7 @@
 // What bounds it: with up to some 80 rows an expert the bytes of the weights in use
 // (9/16 byte each), above that the tensor core.  48 rows over 31 of 48 experts of
 // 4,096 x 5,120 weights take 62 us, 5.9 TB/s; 16,384 rows over 8 experts of 2,816 x
-// 2,048 take 177 us, 1.07 PFLOP/s.  About 10 us of a call are its start (row counts,
+// 2,048 take 167 us, 1.13 PFLOP/s.  About 10 us of a call are its start (row counts,
 // first rows, first weights: 7 us before the first MMA) and its end.
 #include <cuda_bf16.h>
 
@@ -94,8 +94,10 @@ __host__ __device__ __forceinline__ int64_t row_groups(int a_rows, int E)
 
 constexpr int kRowsThreads = 128;
 constexpr int kRowsUnseen = 512;    // rows that are read before it is known whether they are used
-constexpr int kRowsHeld = 4;        // 16-byte vectors of a row that a thread keeps
-constexpr int kRowsCtas = 8;        // CTAs per SM (16,384 rows of 2,048: 189 us for the call; six 191, four 202)
+constexpr int kRowsCtas = 8;        // CTAs per SM
+// A row per CTA, or with more rows than kRowsWide one per warp, which keeps more bytes
+// in flight (16,384 rows of 2,048: 24 us by warps, 35 by CTAs) but takes longer for one.
+constexpr int kRowsWide = 4096;
 
 // Operand layout of the rows: chunk c of group g at (c * groups + g) * 2048 bytes,
 // so a tile's rows are one bulk copy per chunk; in each of its two 64-column
@@ -142,9 +144,10 @@ __device__ __forceinline__ int run_of(const int32_t *offsets, int E, int r)
     return base + (below2 ? 31 - __clz((int)below2) : 0);
 }
 
-// One CTA per row, `grid` rows apart.  With blocks, candidate q is row q / E of block
-// q % E, so that the rows in use come first; every warp looks 32 candidates over at
-// once.  Also zeroes the arrival counters of k_expert_w4.
+// TEAM threads per row: the CTA's, or a warp's.  With blocks, candidate q is row q / E
+// of block q % E, so that the rows in use come first; every warp looks 32 candidates
+// over at once.  Also zeroes the arrival counters of k_expert_w4.
+template <int TEAM>
 __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) k_w4_rows(
     const int4 *__restrict__ a, int a_rows, const int32_t *__restrict__ offsets,
     const int32_t *__restrict__ counts, int block_rows, int E, int K, uint8_t *__restrict__ x16,
@@ -152,10 +155,11 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) k_w4_rows(
 {
     pdl_wait();
     pdl_trigger();
+    constexpr int kHeld = TEAM == 32 ? 8 : 4;       // vectors of a row that a thread keeps
     __shared__ uint32_t part[kRowsThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int lane = threadIdx.x & 31, tid = threadIdx.x % TEAM;
     if (blockIdx.x == 0)
-        for (int i = tid; i < n_arrivals; i += kRowsThreads) arrivals[i] = 0;
+        for (int i = threadIdx.x; i < n_arrivals; i += kRowsThreads) arrivals[i] = 0;
     const int V = K / 8, padded = 16 * w4_chunks(K);
     const int64_t groups = row_groups(a_rows, E);
     const int candidates = offsets ? a_rows : E * block_rows;
@@ -166,38 +170,41 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) k_w4_rows(
         for (int i = lane; i <= E; i += 32) most = max(most, __ldg(offsets + i));
         end = min(a_rows, __reduce_max_sync(kFull, most));
     }
-    for (int64_t q0 = blockIdx.x; q0 < candidates; q0 += 32 * (int64_t)gridDim.x) {
-        const int64_t mine = q0 + lane * (int64_t)gridDim.x;
+    constexpr int kTeamsHere = kRowsThreads / TEAM;
+    const int64_t stride = (int64_t)gridDim.x * kTeamsHere;
+    for (int64_t q0 = (int64_t)blockIdx.x * kTeamsHere + threadIdx.x / TEAM; q0 < end; q0 += 32 * stride) {
+        const int64_t mine = q0 + lane * stride;
         unsigned used = __ballot_sync(kFull, mine < end && (offsets || (int)mine / E <
                                                                            __ldg(counts + (int)mine % E)));
         for (; used; used &= used - 1) {
-            const int q = (int)(q0 + (__ffs(used) - 1) * (int64_t)gridDim.x);
+            const int q = (int)(q0 + (__ffs(used) - 1) * stride);
             const int at = offsets ? q : q % E * block_rows + q / E;
             const int4 *src = a + (int64_t)at * V;
-            int4 x[kRowsHeld];                      // the row's first vectors
+            int4 x[kHeld];                          // the row's first vectors
 #pragma unroll
-            for (int h = 0; h < kRowsHeld; h++)
-                x[h] = tid + h * kRowsThreads < V ? src[tid + h * kRowsThreads] : make_int4(0, 0, 0, 0);
+            for (int h = 0; h < kHeld; h++)
+                x[h] = tid + h * TEAM < V ? src[tid + h * TEAM] : make_int4(0, 0, 0, 0);
             const int e = offsets ? run_of(offsets, E, q) : q % E;
             int start, count;
             bool bad = false;
             expert_rows(offsets, counts, block_rows, a_rows, e, start, count, bad);
             const int i = at - start;
-            if (i < 0 || i >= count) continue;      // uniform per CTA
+            if (i < 0 || i >= count) continue;      // uniform per team
             const int64_t group = row_group(offsets != nullptr, start, block_rows, e) + (i >> 3);
             const int r8 = i & 7;
             uint32_t top = 0;
 #pragma unroll
-            for (int h = 0; h < kRowsHeld; h++) top = max(top, abs_max_bits(x[h]));
+            for (int h = 0; h < kHeld; h++) top = max(top, abs_max_bits(x[h]));
 #pragma unroll 4
-            for (int v = tid + kRowsHeld * kRowsThreads; v < V; v += kRowsThreads)
-                top = max(top, abs_max_bits(src[v]));
+            for (int v = tid + kHeld * TEAM; v < V; v += TEAM) top = max(top, abs_max_bits(src[v]));
             top = __reduce_max_sync(kFull, top);
-            __syncthreads();                        // the last row's reads of part[] are over
-            if (lane == 0) part[tid >> 5] = top;
-            __syncthreads();
+            if constexpr (TEAM > 32) {
+                __syncthreads();                    // the last row's reads of part[] are over
+                if (lane == 0) part[tid >> 5] = top;
+                __syncthreads();
 #pragma unroll
-            for (int w = 0; w < kRowsThreads / 32; w++) top = max(top, part[w]);
+                for (int w = 0; w < TEAM / 32; w++) top = max(top, part[w]);
+            }
             // 2^shift takes the largest value to [2^14, 2^15); at most 2^127 (rows of
             // bf16's smallest values stay below, where fp16 still holds all their bits)
             const int field = (int)(top >> 7);
@@ -208,11 +215,11 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) k_w4_rows(
                     __uint_as_float(shift == 127 ? 0x00400000u : (uint32_t)(127 - shift) << 23);
             int v = tid;
 #pragma unroll
-            for (int h = 0; h < kRowsHeld; h++, v += kRowsThreads)
+            for (int h = 0; h < kHeld; h++, v += TEAM)
                 if (v < padded)
                     st_cg(row_piece(x16, groups, group, r8, v),
                           v < V ? scale_to_half8(x[h], by) : make_int4(0, 0, 0, 0));
-            for (; v < padded; v += kRowsThreads)               // (from L1 this time)
+            for (; v < padded; v += TEAM)           // (from L1 this time)
                 st_cg(row_piece(x16, groups, group, r8, v),
                       v < V ? scale_to_half8(src[v], by) : make_int4(0, 0, 0, 0));
         }
@@ -944,11 +951,13 @@ cudaError_t launch_expert_w4(const uint16_t *a, int a_rows, const int32_t *offse
     float *partial = (float *)((uint8_t *)row_scale + scale_bytes(a_rows, E));
     int32_t *arrivals = (int32_t *)((uint8_t *)partial + kPartialBytes);
     const int ctas = di.sm_count < kMaxCtas ? di.sm_count : kMaxCtas;
+    const bool by_warp = a_rows > kRowsWide;
+    const int want = by_warp ? (a_rows + kRowsThreads / 32 - 1) / (kRowsThreads / 32) : a_rows;
     const int most = kRowsCtas * di.sm_count;
-    const int grid = a_rows > most ? most : a_rows;
     MOE_TRACED_LAUNCH("k_w4_rows", st,
-        err = launch_pdl(k_w4_rows, dim3(grid), dim3(kRowsThreads), 0, st, (const int4 *)a, a_rows,
-                         offsets, counts, block_rows, E, K, x16, row_scale, arrivals, kMaxCtas));
+        err = launch_pdl(by_warp ? k_w4_rows<32> : k_w4_rows<kRowsThreads>,
+                         dim3(want > most ? most : want), dim3(kRowsThreads), 0, st, (const int4 *)a,
+                         a_rows, offsets, counts, block_rows, E, K, x16, row_scale, arrivals, kMaxCtas));
     if (err != cudaSuccess) return err;
     err = cudaFuncSetAttribute(k_expert_w4, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMmSmem);
     if (err != cudaSuccess) return err;

@@ -122,7 +122,8 @@ CASES = [  # E, N, K, gated, counts
     (3, 72, 144, True, [0, 5, 1]), (5, 136, 400, False, [2, 0, 17, 0, 9]), (2, 256, 2048, True, [1, 1]),
     (4, 328, 1040, True, [16, 15, 0, 33]), (1, 640, 5120, False, [1]), (2, 96, 272, False, [129, 64]),
     (3, 200, 512, True, [300, 1, 128]), (2, 520, 96, False, [513, 127]), (64, 40, 64, True, [3, 0] * 32),
-    (1, 1000, 3600, True, [7]), (6, 24, 7168, False, [1, 0, 0, 2, 8, 1]), (2, 1600, 256, True, [260, 90])]
+    (1, 1000, 3600, True, [7]), (6, 24, 7168, False, [1, 0, 0, 2, 8, 1]), (2, 1600, 256, True, [260, 90]),
+    (3, 40, 96, False, [2100, 0, 2400]), (2, 24, 2320, True, [2060, 2050])]
 
 
 @gpu
