@@ -398,3 +398,56 @@ def test_combine_backward_empty_batch():
                            d_y, e((1, 0, 2), device=DEV),
                            recv_pair=torch.full((5,), -1, dtype=torch.int32, device=DEV))
     assert not d_y.any()
+
+
+# ------------------------------------------------------------------ refusals with GPU tensors
+
+def test_binding_refuses_types_shapes_and_strides():
+    S, T, E, k = 2, 8, 16, 2
+    f = lambda *s: torch.zeros(s, device=DEV)  # noqa: E731
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device=DEV)  # noqa: E731
+    ws = torch.empty(m.moe_balance_loss_workspace_bytes(S, T, E), dtype=torch.uint8, device=DEV)
+    good = [f(S, T, E), i(S, T, k), i(S, E), f(S, E), f(S, T), i(S), f(2), ws]
+
+    def refused(error, match, at, value, **kw):
+        args = list(good)
+        args[at] = value
+        with pytest.raises(error, match=match):
+            m.moe_balance_loss(*args, **kw)
+
+    refused(TypeError, "logits: dtype", 0, f(S, T, E).double())
+    refused(ValueError, "logits: expected 3 dims", 0, f(T, E))
+    refused(ValueError, "logits: must be contiguous", 0, f(S, E, T).transpose(1, 2))
+    refused(TypeError, "topk_ids: dtype", 1, i(S, T, k).long())
+    refused(ValueError, r"topk_ids: expected shape \(2, 8, 2\), got \(2, 7, 2\)", 1, i(S, T - 1, k))
+    refused(ValueError, "counts: expected shape", 2, i(S, E + 1))
+    refused(ValueError, "losses: expected shape", 6, f(3))
+    refused(TypeError, "ws: expected a torch.Tensor", 7, None)
+    refused(ValueError, "token_mask: expected shape", 0, good[0],
+            token_mask=torch.ones(S, T + 1, dtype=torch.uint8, device=DEV))
+    refused(m.MoeError, "ws_bytes", 7, ws[:256])
+    refused(AttributeError, "cuda_stream", 0, good[0], stream=object())
+    m.moe_balance_loss(*good)
+    with pytest.raises(ValueError, match="logits: needed with d_losses"):
+        m.moe_route_backward(None, i(S, T, k), None, None, f(S, T), i(S, E), i(S), f(2), f(S, T, E))
+    with pytest.raises(TypeError, match="logits: dtype"):      # d_logits of another type
+        m.moe_route_backward(f(S, T, E), i(S, T, k), None, None, f(S, T), i(S, E), i(S), f(2),
+                             f(S, T, E).bfloat16())
+    with pytest.raises(m.MoeError, match="no gradient comes in"):
+        m.moe_route_backward(None, i(S, T, k), None, None, None, None, None, None, f(S, T, E))
+    y = torch.zeros(5, 16, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="y: expected shape"):
+        m.moe_combine_backward(f(1, 3, 24).bfloat16(), y, i(1, 3, 2), f(1, 3, 2), y.clone(), f(1, 3, 2))
+    with pytest.raises(ValueError, match="recv_pair: expected shape"):
+        m.moe_combine_backward(f(1, 3, 16).bfloat16(), y, i(1, 3, 2), f(1, 3, 2), y.clone(), f(1, 3, 2),
+                               recv_pair=i(4))
+    w4 = torch.empty(m.moe_w4_bytes(2, 16, 32), dtype=torch.uint8, device=DEV)
+    a = f(4, 32).bfloat16()
+    out = f(4, 16).bfloat16()
+    big = torch.empty(m.moe_expert_product_w4_workspace_bytes(4, 2, 16, 32), dtype=torch.uint8, device=DEV)
+    with pytest.raises(ValueError, match="are not the packed weights"):
+        m.moe_expert_product_w4(a, w4[:-1], f(2), out, big, expert_offsets=i(3))
+    with pytest.raises(ValueError, match="expert_offsets: expected shape"):
+        m.moe_expert_product_w4(a, w4, f(2), out, big, expert_offsets=i(2))
+    with pytest.raises(m.MoeError, match="not both"):
+        m.moe_expert_product_w4(a, w4, f(2), out, big)
