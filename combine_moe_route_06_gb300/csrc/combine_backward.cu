@@ -4,7 +4,8 @@
 //   dy[row(n, j)] = w_nj dout[n]          (bf16, one rounding)
 //   dw_nj         = <y[row(n, j)], dout[n]>  (fp32 sums)
 // Rows of dy that hold no pair (run padding) are set to zero.  The bound is
-// HBM: every received row read and written once, dout read once.
+// HBM: every received row read and written once, dout read once (4,096 tokens x 6 rows
+// of 5,120: 92.7 us, 5.9 TB/s, 0.87 of a plain copy's rate).
 //
 // One warp per token, or with few tokens one CTA, whose warps take the row's
 // columns in turn: a 16-byte vector of dout per lane serves all of the token's

@@ -430,7 +430,7 @@ __device__ __forceinline__ void tile_sums(const Finish &p, int h, int c0,
     for (int j = 0; j < COLS; j++) {
         const float by = __shfl_sync(kFull, mine, (c0 + j) & 31);
 #pragma unroll
-        for (int b = 0; b < BLOCKS; b++) v[b][j] = v[b][j] * by * p.f;
+        for (int b = 0; b < BLOCKS; b++) v[b][j] = v[b][j] * p.f * by;   // (by alone could overflow)
     }
 }
 

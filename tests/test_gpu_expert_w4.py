@@ -196,6 +196,20 @@ def test_row_magnitudes_and_nan(gated):
 
 
 @gpu
+@pytest.mark.parametrize("size,factor", [(1e36, 1e-5), (1e-33, 1e4)])
+def test_sums_past_the_range_of_their_factors(size, factor):
+    """Sums that would leave fp32 before the expert's factor brings them back."""
+    E, N, K = 1, 24, 256
+    codes, scales, _ = make_weights(E, N, K, seed=21)
+    scales[:] = 0x7e if size > 1 else 0x08      # 448 and 2^-6
+    factor = np.array([factor], np.float32)
+    a = rows_of(22, 5, K, size)
+    y, status = product(a, pack(codes, scales, False), factor, N, False, offsets=[0, 5])
+    assert status == 0
+    check(y, a, codes, scales, factor, False, [(0, 5)])
+
+
+@gpu
 def test_bad_row_ranges_are_cut_and_flagged():
     E, N, K = 3, 32, 64
     codes, scales, factor = make_weights(E, N, K, seed=8)
