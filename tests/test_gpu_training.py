@@ -128,7 +128,8 @@ def make(S, T, E, k, seed, mask=None, spread=1.0):
 
 SHAPES = [(1, 1, 1, 1), (1, 128, 16, 2), (3, 33, 33, 5), (2, 65, 64, 8), (1, 700, 384, 6),
           (5, 17, 127, 3), (2, 40, 513, 32), (1, 90, 1024, 10), (70, 5, 20, 4), (310, 3, 8, 2),
-          (2, 301, 128, 8), (3, 50, 100, 7), (1, 61, 36, 9)]
+          (2, 301, 128, 8), (3, 50, 100, 7), (1, 61, 36, 9),
+          (4, 256, 48, 4), (3, 1024, 33, 2), (32, 16, 64, 3), (8, 128, 384, 6), (33, 16, 8, 1)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
