@@ -22,7 +22,7 @@
 // What bounds it: with up to some 80 rows an expert the bytes of the weights in use
 // (9/16 byte each), above that the tensor core.  48 rows over 31 of 48 experts of
 // 4,096 x 5,120 weights take 62 us, 5.9 TB/s; 16,384 rows over 8 experts of 2,816 x
-// 2,048 take 167 to 171 us, 1.1 PFLOP/s.  About 10 us of a call are its start (row counts,
+// 2,048 take 167 to 174 us, 1.1 PFLOP/s.  About 10 us of a call are its start (row counts,
 // first rows, first weights: 7 us before the first MMA) and its end.
 #include <cuda_bf16.h>
 
