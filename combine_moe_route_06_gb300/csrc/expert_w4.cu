@@ -434,6 +434,21 @@ __device__ __forceinline__ void tile_sums(const Finish &p, int h, int c0,
     }
 }
 
+// silu(gate) * up.  With h = exp(-|gate| / 2), silu is gate / (1 + h^2), for a negative
+// gate times h^2, so that nothing leaves fp32 (exp(-gate) itself is past it below -88.7,
+// and its reciprocal below -87.3).  Of h the approximate exp2 takes 2^-22 and the rounded
+// argument |gate| 2^-24, of the result the reciprocal 2^-23: below 2^-15 in all for
+// |gate| <= 120, past which the result leaves bf16's range; its rounding is 2^-9.
+__device__ __forceinline__ float gated_output(float gate, float up)
+{
+    constexpr float kHalfLog2E = 0.72134752044448f;
+    float h, inv;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(-kHalfLog2E * fabsf(gate)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(h, h, 1.f)));
+    const float by = gate < 0.f ? h : 1.f;
+    return (gate * by) * inv * (by * up);
+}
+
 // Outputs of this thread's weight row(s), COLS rows of `a` at a time.  dst: the
 // output of the tile's first row of `a`; `store`: not padding.
 template <int COLS, bool CUT>
@@ -449,8 +464,7 @@ __device__ __forceinline__ void finish_gated(const Finish &p, const float (&scal
 #pragma unroll
             for (int j = 0; j < COLS; j++)
                 if (c0 + j < p.rows)
-                    dst[(int64_t)(c0 + j) * N] =
-                        __float2bfloat16_rn(__fdividef(v[0][j], 1.f + __expf(-v[0][j])) * v[1][j]);
+                    dst[(int64_t)(c0 + j) * N] = __float2bfloat16_rn(gated_output(v[0][j], v[1][j]));
     }
 }
 template <int COLS, bool CUT>
