@@ -25,6 +25,7 @@
 // 2,048 take 167 to 174 us, 1.1 PFLOP/s.  About 10 us of a call are its start (row counts,
 // first rows, first weights: 7 us before the first MMA) and its end.
 #include <cuda_bf16.h>
+#include <float.h>
 
 #include "common.cuh"
 #include "launch.h"
@@ -629,7 +630,14 @@ __device__ __forceinline__ bool finish_segment(const MmArgs &p, MmShared &sh, co
 {
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
     const int row = quarter * 32 + lane;
-    const float f = __ldg(p.factor + g.e);
+    // A sum is below 2^47; of a factor above 1 half the power of two goes to the rows' scales
+    // (at most 2^114), so that neither product leaves fp32 where the result does not.  (A
+    // clamped scale would be that of a row whose results leave fp32, or are 0.)
+    float f = __ldg(p.factor + g.e);
+    const int field = __float_as_int(f) >> 23 & 255;
+    const int half = field > 127 ? (field - 127) >> 1 : 0;
+    const float rest = __int_as_float((127 + half) << 23);
+    f *= __int_as_float((127 - half) << 23);
     const int64_t scale0 =
         (int64_t)row_group(p.offsets != nullptr, sh.start[g.e], p.block_rows, g.e) * 8 + g.row0;
     __nv_bfloat16 *out = p.y + (int64_t)(sh.start[g.e] + g.row0) * p.N;
@@ -641,7 +649,9 @@ __device__ __forceinline__ bool finish_segment(const MmArgs &p, MmShared &sh, co
     float scale[kMaxRowsTile / 32];      // of rows lane, lane + 32, ... of the tile
 #pragma unroll
     for (int i = 0; i < kMaxRowsTile / 32; i++)
-        scale[i] = lane + 32 * i < g.rows ? __ldcg(p.row_scale + scale0 + lane + 32 * i) : 0.f;
+        scale[i] = lane + 32 * i < g.rows
+                       ? fminf(__ldcg(p.row_scale + scale0 + lane + 32 * i) * rest, FLT_MAX)
+                       : 0.f;
     // where the other part of a tile cut in two is in memory already, its first columns
     const bool early = parts > 1 && arrived(p.arrivals + first) == parts - 1;
     const int other = blockIdx.x == first ? first + 1 : first;

@@ -1,17 +1,18 @@
-"""The gated output where exp(-gate) is near fp32's largest value or past it.
+"""moe_expert_product_w4 where parts of a result leave fp32 though the result does not: exp(-gate)
+of low gates, and large factors.
 
-The sums are exact here (one product each), so what is left is the epilogue: the exp of half the
+Low gates: the sums are exact (one product each), so what is left is the epilogue: the exp of half the
 gate, which enters squared, is off by the rounding of its argument, |gate| 2^-24, and by a fast
 exp's few 2^-23, the rest by a fast reciprocal and four products: together below 2^-14 for
 |gate| <= 120.  The rounding to bf16 is 2^-9, so 2^-8 covers both.  Results below bf16's normal
-range have a step of 2^-133."""
+range have a step of 2^-133.  Factors: tolerances as in test_gpu_expert_w4."""
 import numpy as np
 import pytest
 import torch
 
 import combine_moe_route_06_gb300 as m
 import moe_synth as ms
-from test_gpu_expert_w4 import pack, product
+from test_gpu_expert_w4 import check, make_weights, pack, product, rows_of
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +44,17 @@ def test_low_gates_keep_their_precision():
     got = ms.f32_from_bf16_bits(y).astype(np.float64)
     worst = np.abs(got - want) - 2.0 ** -8 * np.abs(want) - 2.0 ** -133
     assert np.all(worst <= 0), (g[(worst > 0).any(1), 0], got[(worst > 0).any(1), 0])
+
+
+@pytest.mark.parametrize("size,factor", [(1e-37, 1e35), (1e-35, -3e37), (1e-30, 1e34), (2e-38, 3e38),
+                                         (1e35, 1e-30), (1e37, 1e-38)])
+@pytest.mark.parametrize("rows", [5, 150])
+def test_factors_of_any_size(size, factor, rows):
+    """Results in range whatever the factor's share of them."""
+    E, N, K = 1, 24, 256
+    codes, scales, _ = make_weights(E, N, K, seed=31)
+    factor = np.array([factor], np.float32)
+    a = rows_of(32, rows, K, size)
+    y, status = product(a, pack(codes, scales, False), factor, N, False, offsets=[0, rows])
+    assert status == 0
+    check(y, a, codes, scales, factor, False, [(0, rows)])
