@@ -105,6 +105,15 @@ int size32(int64_t n, const char *name)
     return (int)n;
 }
 
+int int32(PyObject *o, const char *name)
+{
+    int past = 0;
+    const long n = PyLong_AsLongAndOverflow(o, &past);
+    if (n == -1 && PyErr_Occurred()) throw Refused{};
+    if (past || n != (int)n) refuse(PyExc_ValueError, std::string(name) + ": does not fit 32 bits");
+    return (int)n;
+}
+
 cudaStream_t stream_of(PyObject *o)
 {
     if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
@@ -207,8 +216,7 @@ moe_status_t expert_product_w4(Args a)
     const int64_t E = f.size(0);
     const at::Tensor &p = tensor(a[w4], "w4", kU8);
     const at::Tensor &w = tensor(a[ws], "ws", kU8);
-    const int block = (int)PyLong_AsLong(a[block_rows]);
-    if (block == -1 && PyErr_Occurred()) throw Refused{};
+    const int block = int32(a[block_rows], "block_rows");
     const int two = PyObject_IsTrue(a[gated]) == 1;
     // sizes that the library refuses have no packed size; it says why
     const size_t need = moe_w4_bytes(size32(E, "E"), size32(N, "N"), size32(K, "K"), two);

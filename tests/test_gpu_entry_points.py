@@ -1,0 +1,37 @@
+"""The compiled entry points: arguments that do not fit are refused before anything is enqueued."""
+import pytest
+import torch
+
+import combine_moe_route_06_gb300 as m
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    m.build()
+
+
+def product_args(E=2, N=16, K=32, block=4):
+    """Zero rows and weights, big enough in either layout of the weights."""
+    rows = E * block
+    zeros = lambda *s, **kw: torch.zeros(s, device="cuda", **kw)  # noqa: E731
+    ws = torch.empty(m.moe_expert_product_w4_workspace_bytes(rows, E, N, K), dtype=torch.uint8,
+                     device="cuda")
+    y = torch.full((rows, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    w4 = zeros(m.moe_w4_bytes(E, N, K, True), dtype=torch.uint8)
+    return (zeros(rows, K, dtype=torch.bfloat16), w4, torch.ones(E, device="cuda"), y, ws), \
+        dict(masked_counts=torch.full((E,), block, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("block", [2 ** 32 + 4, 4 - 2 ** 32, 2 ** 31, -2 ** 31 - 1, 2 ** 70, -2 ** 70])
+def test_block_rows_past_32_bits_are_refused(block):
+    args, kw = product_args()
+    with pytest.raises(ValueError, match="block_rows"):
+        m.moe_expert_product_w4(*args, block_rows=block, **kw)
+    torch.cuda.synchronize()
+    assert bool((args[3] == 3).all())
+    m.moe_expert_product_w4(*args, block_rows=4, **kw)
+    assert not args[3].any()
