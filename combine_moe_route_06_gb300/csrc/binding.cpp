@@ -114,6 +114,13 @@ int int32(PyObject *o, const char *name)
     return (int)n;
 }
 
+bool truth(PyObject *o)
+{
+    const int is = PyObject_IsTrue(o);
+    if (is < 0) throw Refused{};
+    return is;
+}
+
 cudaStream_t stream_of(PyObject *o)
 {
     if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
@@ -196,7 +203,7 @@ moe_status_t w4_pack(Args a)
     enum { codes, scales, w4, gated, stream };
     const at::Tensor &c = ranked(a[codes], "codes", kU8, 3);
     const int64_t E = c.size(0), rows = c.size(1), K = 2 * c.size(2);
-    const bool two = PyObject_IsTrue(a[gated]) == 1;
+    const bool two = truth(a[gated]);
     if (two && rows % 2)
         refuse(PyExc_ValueError, "codes: gated weights have an even number of rows, got " +
                                      std::to_string(rows));
@@ -217,7 +224,7 @@ moe_status_t expert_product_w4(Args a)
     const at::Tensor &p = tensor(a[w4], "w4", kU8);
     const at::Tensor &w = tensor(a[ws], "ws", kU8);
     const int block = int32(a[block_rows], "block_rows");
-    const int two = PyObject_IsTrue(a[gated]) == 1;
+    const int two = truth(a[gated]);
     // sizes that the library refuses have no packed size; it says why
     const size_t need = moe_w4_bytes(size32(E, "E"), size32(N, "N"), size32(K, "K"), two);
     if ((size_t)p.numel() < need)

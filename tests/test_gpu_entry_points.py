@@ -35,3 +35,23 @@ def test_block_rows_past_32_bits_are_refused(block):
     assert bool((args[3] == 3).all())
     m.moe_expert_product_w4(*args, block_rows=4, **kw)
     assert not args[3].any()
+
+
+class Unclear:
+    """Neither true nor false."""
+
+    def __bool__(self):
+        raise RuntimeError("unclear")
+
+
+def test_an_error_of_the_gated_argument_is_passed_on():
+    args, kw = product_args()
+    with pytest.raises(RuntimeError, match="unclear"):
+        m.moe_expert_product_w4(*args, block_rows=4, gated=Unclear(), **kw)
+    codes = torch.zeros((2, 32, 16), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((2, 32, 2), dtype=torch.uint8, device="cuda")
+    w4 = torch.full((m.moe_w4_bytes(2, 32, 32),), 7, dtype=torch.uint8, device="cuda")
+    with pytest.raises(RuntimeError, match="unclear"):
+        m.moe_w4_pack(codes, scales, w4, gated=Unclear())
+    torch.cuda.synchronize()
+    assert bool((args[3] == 3).all()) and bool((w4 == 7).all())
