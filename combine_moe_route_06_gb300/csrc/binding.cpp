@@ -136,6 +136,18 @@ int logits_type(const at::Tensor &t) { return t.scalar_type() == at::kFloat ? MO
 
 using Args = PyObject *const *;
 
+// Calls the library with the interpreter given up, as ctypes does: a launch waits when the
+// device's queue is full, perhaps behind a host function that needs the interpreter.  The
+// arguments are all evaluated before; the caller's references keep the tensors.
+template <typename... P, typename... A>
+moe_status_t enqueue(moe_status_t (*call)(P...), A... args)
+{
+    PyThreadState *state = PyEval_SaveThread();
+    const moe_status_t status = call(args...);
+    PyEval_RestoreThread(state);
+    return status;
+}
+
 moe_status_t balance_loss(Args a)
 {
     enum { logits, ids, counts, prob, lse, n_valid, losses, ws, mask, status, stream };
@@ -144,9 +156,9 @@ moe_status_t balance_loss(Args a)
     const int64_t S = l.size(0), T = l.size(1), E = l.size(2), k = i.size(2);
     shaped(a[ids], "topk_ids", kI32, {S, T, k});
     const at::Tensor &w = tensor(a[ws], "ws", kU8);
-    return moe_balance_loss(
-        data<void>(l), logits_type(l), size32(S, "S"), size32(T, "T"), size32(E, "E"), size32(k, "k"),
-        data<int32_t>(i), optional<uint8_t>(a[mask], "token_mask", kU8, {S, T}),
+    return enqueue(
+        moe_balance_loss, data<void>(l), logits_type(l), size32(S, "S"), size32(T, "T"), size32(E, "E"),
+        size32(k, "k"), data<int32_t>(i), optional<uint8_t>(a[mask], "token_mask", kU8, {S, T}),
         at_shape<int32_t>(a[counts], "counts", kI32, {S, E}),
         at_shape<float>(a[prob], "prob_mean", kF32, {S, E}), at_shape<float>(a[lse], "lse", kF32, {S, T}),
         at_shape<int32_t>(a[n_valid], "n_valid", kI32, {S}), at_shape<float>(a[losses], "losses", kF32, {2}),
@@ -167,7 +179,8 @@ moe_status_t route_backward(Args a)
     const bool loss = a[d_losses] != Py_None;
     if (loss && a[logits] == Py_None) refuse(PyExc_ValueError, "logits: needed with d_losses");
     const int like = d.scalar_type() == at::kFloat ? kF32 : kBf16;
-    return moe_route_backward(
+    return enqueue(
+        moe_route_backward,
         loss ? at_shape<void>(a[logits], "logits", like, {S, T, E}) : nullptr, logits_type(d),
         size32(S, "S"), size32(T, "T"), size32(E, "E"), size32(k, "k"),
         optional<int32_t>(a[ids], "topk_ids", kI32, {S, T, k}),
@@ -188,8 +201,8 @@ moe_status_t combine_backward(Args a)
     const int64_t S = g.size(0), T = g.size(1), H = g.size(2), rows = r.size(0);
     const int64_t k = ranked(a[pair_row], "pair_row", kI32, 3).size(2);
     shaped(a[y], "y", kRow, {rows, H});
-    return moe_combine_backward(
-        data<uint16_t>(g), data<uint16_t>(r), size32(rows, "y_rows"),
+    return enqueue(
+        moe_combine_backward, data<uint16_t>(g), data<uint16_t>(r), size32(rows, "y_rows"),
         at_shape<int32_t>(a[pair_row], "pair_row", kI32, {S, T, k}),
         at_shape<float>(a[w], "topk_w", kF32, {S, T, k}),
         optional<int32_t>(a[recv_pair], "recv_pair", kI32, {rows}), size32(S, "S"), size32(T, "T"),
@@ -208,9 +221,10 @@ moe_status_t w4_pack(Args a)
         refuse(PyExc_ValueError, "codes: gated weights have an even number of rows, got " +
                                      std::to_string(rows));
     const at::Tensor &p = tensor(a[w4], "w4", kU8);
-    return moe_w4_pack(data<uint8_t>(c), at_shape<uint8_t>(a[scales], "scales", kU8, {E, rows, K / 16}),
-                       size32(E, "E"), size32(two ? rows / 2 : rows, "N"), size32(K, "K"), two,
-                       data<uint8_t>(p), (size_t)p.numel(), stream_of(a[stream]));
+    return enqueue(moe_w4_pack, data<uint8_t>(c),
+                   at_shape<uint8_t>(a[scales], "scales", kU8, {E, rows, K / 16}), size32(E, "E"),
+                   size32(two ? rows / 2 : rows, "N"), size32(K, "K"), two, data<uint8_t>(p),
+                   (size_t)p.numel(), stream_of(a[stream]));
 }
 
 moe_status_t expert_product_w4(Args a)
@@ -231,8 +245,8 @@ moe_status_t expert_product_w4(Args a)
         refuse(PyExc_ValueError, "w4: " + std::to_string(p.numel()) + " bytes are not the packed weights of E=" +
                                      std::to_string(E) + ", N=" + std::to_string(N) + ", K=" +
                                      std::to_string(K) + ", gated=" + std::to_string(two));
-    return moe_expert_product_w4(
-        data<uint16_t>(r), size32(rows, "a_rows"),
+    return enqueue(
+        moe_expert_product_w4, data<uint16_t>(r), size32(rows, "a_rows"),
         optional<int32_t>(a[offsets], "expert_offsets", kI32, {E + 1}),
         optional<int32_t>(a[counts], "masked_counts", kI32, {E}), block, data<uint8_t>(p),
         data<float>(f), (int)E, (int)N, (int)K, two, at_shape<uint16_t>(a[y], "y", kRow, {rows, N}),

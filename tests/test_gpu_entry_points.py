@@ -1,4 +1,8 @@
-"""The compiled entry points: arguments that do not fit are refused before anything is enqueued."""
+"""The compiled entry points: arguments that do not fit are refused before anything is enqueued,
+and other Python threads run while a call enqueues."""
+import sys
+import threading
+
 import pytest
 import torch
 
@@ -55,3 +59,40 @@ def test_an_error_of_the_gated_argument_is_passed_on():
         m.moe_w4_pack(codes, scales, w4, gated=Unclear())
     torch.cuda.synchronize()
     assert bool((args[3] == 3).all()) and bool((w4 == 7).all())
+
+
+def test_other_threads_run_while_a_call_enqueues():
+    """With a switch interval longer than the test a thread gets the interpreter only from one that
+    gives it up, which the loop below does nowhere but inside the call."""
+    S, T, E, k = 2, 256, 64, 4
+    f = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = torch.empty(m.moe_balance_loss_workspace_bytes(S, T, E), dtype=torch.uint8, device="cuda")
+    args = [f(S, T, E), i(S, T, k), i(S, E), f(S, E), f(S, T), i(S), f(2), ws]
+    m.moe_balance_loss(*args)
+    torch.cuda.synchronize()
+    go, ready, ran = threading.Lock(), threading.Event(), []
+
+    def other():
+        ready.set()
+        go.acquire()
+        ran.append(True)
+
+    go.acquire()
+    thread = threading.Thread(target=other, daemon=True)
+    interval = sys.getswitchinterval()
+    sys.setswitchinterval(1000)
+    try:
+        thread.start()
+        ready.wait()
+        go.release()
+        for _ in range(6000):
+            m.moe_balance_loss(*args)
+            if ran:
+                break
+        there = bool(ran)
+    finally:
+        sys.setswitchinterval(interval)
+    thread.join(10)
+    torch.cuda.synchronize()
+    assert there
