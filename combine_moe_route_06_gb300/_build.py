@@ -4,7 +4,9 @@ Each .cu translation unit compiles in its own nvcc process (in parallel),
 then one nvcc link produces the shared library.  The CUDA runtime is linked
 statically, so loading the library needs no GPU driver (only calls do).
 The Python entry points of csrc/binding.cpp become _moe_ops.so beside it (g++,
-torch's headers and libraries of the installation that runs the build).
+torch's headers and libraries of the installation that runs the build).  Where
+that fails, as with a torch without CUDA, the library is there all the same: a
+warning says why, and only the calls that go through _moe_ops.so are missing.
 """
 from __future__ import annotations
 
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 import torch
 
@@ -48,70 +51,83 @@ def _sources():
 
 def _deps():
     return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
-        sorted(glob.glob(os.path.join(CSRC, "*.h"))) + [BINDING, HEADER]
+        sorted(glob.glob(os.path.join(CSRC, "*.h"))) + [HEADER]
+
+
+def _older(path, deps) -> bool:
+    return not os.path.exists(path) or any(os.path.getmtime(d) > os.path.getmtime(path) for d in deps)
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(OPS_PATH):
-        return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(OPS_PATH))
-    return any(os.path.getmtime(d) > t for d in _deps())
+    return _older(LIB_PATH, _deps())
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
-    """Compile (if stale or forced) and return the path of libmoeroute.so."""
-    if not force and not is_stale():
-        return LIB_PATH
-    os.makedirs(OUT_DIR, exist_ok=True)
-    nvcc = nvcc_path()
-    flags = NVCC_FLAGS + (extra_flags or [])
-    objs = []
+def ops_stale() -> bool:
+    return _older(OPS_PATH, [BINDING, HEADER])
 
-    def compile_one(src):
-        obj = os.path.join(OUT_DIR, os.path.basename(src)[:-3] + ".o")
-        cmd = [nvcc, *ARCH, *flags, "-I", os.path.join(ROOT, "include"), "-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
-        if verbose and (r.stdout or r.stderr):
-            print(r.stdout + r.stderr)
-        return obj
 
-    def compile_binding():
-        base = os.path.dirname(torch.__file__)
-        obj = os.path.join(OUT_DIR, "binding.o")
-        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-c", BINDING, "-o", obj,
-               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
-               "-I", os.path.join(base, "include"),
-               "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include"),
-               "-I", sysconfig.get_paths()["include"]]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed for {BINDING}:\n{r.stdout}\n{r.stderr}")
-        return obj
-
-    srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
-        binding = ex.submit(compile_binding)
-        objs = list(ex.map(compile_one, srcs))
-        binding_obj = binding.result()
-    tmp = LIB_PATH + f".{os.getpid()}.tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
+def _run(cmd, what):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+    return r
+
+
+def _compile_ops(nvcc):
+    base = os.path.dirname(torch.__file__)
+    obj = os.path.join(OUT_DIR, "binding.o")
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-c", BINDING, "-o", obj,
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+          "-I", os.path.join(base, "include"),
+          "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include"),
+          "-I", sysconfig.get_paths()["include"]], f"g++ failed for {BINDING}")
+    return obj
+
+
+def _link_ops(obj):
     # torch's libraries are in the process when the module is imported; libmoeroute.so is
     # found beside it and is the copy that ctypes loads from the same path
     torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = OPS_PATH + f".{os.getpid()}.tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, binding_obj, "-L", torch_lib,
-           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", OUT_DIR, "-l:libmoeroute.so",
-           "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ link failed:\n{r.stdout}\n{r.stderr}")
+    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", torch_lib,
+          "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", OUT_DIR, "-l:libmoeroute.so",
+          "-Wl,-rpath,$ORIGIN"], "g++ link failed")
     os.replace(tmp, OPS_PATH)
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
+    """Compile what is stale (or forced) and return the path of libmoeroute.so."""
+    library, ops = force or is_stale(), force or ops_stale()
+    if not library and not ops:
+        return LIB_PATH
+    os.makedirs(OUT_DIR, exist_ok=True)
+    nvcc = nvcc_path()
+    flags = NVCC_FLAGS + (extra_flags or [])
+
+    def compile_one(src):
+        obj = os.path.join(OUT_DIR, os.path.basename(src)[:-3] + ".o")
+        r = _run([nvcc, *ARCH, *flags, "-I", os.path.join(ROOT, "include"), "-c", src, "-o", obj],
+                 f"nvcc failed for {src}")
+        if verbose and (r.stdout or r.stderr):
+            print(r.stdout + r.stderr)
+        return obj
+
+    srcs = _sources()
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_ops, nvcc) if ops else None
+        if library:
+            objs = list(ex.map(compile_one, srcs))
+            tmp = LIB_PATH + f".{os.getpid()}.tmp"
+            _run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs], "nvcc link failed")
+            os.replace(tmp, LIB_PATH)
+    if ops:
+        try:
+            _link_ops(binding.result())
+        except Exception as e:
+            if os.path.exists(OPS_PATH):    # what an older build left there does not fit any more
+                os.remove(OPS_PATH)
+            warnings.warn(f"the Python entry points of {BINDING} were not built: {e}", RuntimeWarning,
+                          stacklevel=2)
     return LIB_PATH
 
 
