@@ -229,6 +229,10 @@ def _ops():
         if not os.path.exists(_build.OPS_PATH):
             raise MoeLibraryMissing(
                 f"{_build.OPS_PATH} is not built; run `python -c 'import __graft_entry__ as g; g.build()'`")
+        if _build.ops_built_for() != _build.ops_for():
+            raise MoeLibraryMissing(
+                f"{_build.OPS_PATH} was built for {_build.ops_built_for()}, this is {_build.ops_for()}; "
+                "run `python -c 'import __graft_entry__ as g; g.build()'`")
         spec = importlib.util.spec_from_file_location("_moe_ops", _build.OPS_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

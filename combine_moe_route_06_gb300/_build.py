@@ -26,6 +26,8 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libmoeroute.so")
 OPS_PATH = os.path.join(OUT_DIR, "_moe_ops.so")
+# what _moe_ops.so was built for: its layout of a tensor is torch's, its entry points are Python's
+OPS_FOR_PATH = os.path.join(OUT_DIR, "_moe_ops.for")
 BINDING = os.path.join(CSRC, "binding.cpp")
 HEADER = os.path.join(ROOT, "include", "moe_route.h")
 
@@ -62,8 +64,21 @@ def is_stale() -> bool:
     return _older(LIB_PATH, _deps())
 
 
+def ops_for() -> str:
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
+def ops_built_for() -> str:
+    """What ops_for() was when _moe_ops.so was built."""
+    try:
+        with open(OPS_FOR_PATH) as f:
+            return f.read()
+    except OSError:
+        return "an unknown torch"
+
+
 def ops_stale() -> bool:
-    return _older(OPS_PATH, [BINDING, HEADER])
+    return ops_built_for() != ops_for() or _older(OPS_PATH, [BINDING, HEADER])
 
 
 def _run(cmd, what):
@@ -93,6 +108,8 @@ def _link_ops(obj):
           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", OUT_DIR, "-l:libmoeroute.so",
           "-Wl,-rpath,$ORIGIN"], "g++ link failed")
     os.replace(tmp, OPS_PATH)
+    with open(OPS_FOR_PATH, "w") as f:
+        f.write(ops_for())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:

@@ -28,6 +28,7 @@ def tree(tmp_path, monkeypatch):
     monkeypatch.setattr(b, "OUT_DIR", str(out))
     monkeypatch.setattr(b, "LIB_PATH", str(out / "libmoeroute.so"))
     monkeypatch.setattr(b, "OPS_PATH", str(out / "_moe_ops.so"))
+    monkeypatch.setattr(b, "OPS_FOR_PATH", str(out / "_moe_ops.for"), raising=False)
     monkeypatch.setattr(m, "_ops_module", None)
     monkeypatch.setattr(m, "load_library", lambda: None)     # (what is built here is no library)
 
@@ -84,3 +85,21 @@ def test_entry_points_that_no_longer_build_do_not_stay(tree):
     with pytest.warns(RuntimeWarning, match="were not built"):
         b.build()
     assert not os.path.exists(b.OPS_PATH)
+
+
+def test_entry_points_of_another_torch_are_built_again_and_not_loaded(tree, monkeypatch):
+    b, _ = tree
+    monkeypatch.setattr(b.torch, "__version__", "1.0")
+    b.build()
+    monkeypatch.setattr(b.torch, "__version__", "1.1")
+    with pytest.raises(m.MoeLibraryMissing, match="torch 1.0.*torch 1.1"):
+        m._ops()
+    before = stamp(b.LIB_PATH)
+    with open(b.OPS_PATH, "w") as f:
+        f.write("of torch 1.0")
+    b.build()
+    with open(b.OPS_PATH) as f:
+        assert f.read() == "built\n"
+    assert stamp(b.LIB_PATH) == before
+    with pytest.raises(ImportError):            # (what the writer wrote is no module)
+        m._ops()
