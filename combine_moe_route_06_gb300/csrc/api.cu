@@ -11,6 +11,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "common.cuh"
+#include "grid_cache.h"
 #include "launch.h"
 #include "w4.cuh"
 
@@ -85,33 +86,21 @@ moe_status_t check_sizes(const char *fn, int S, int T, int k, int E, int P)
 
 int resident_grid(const void *kernel, int threads, size_t smem)
 {
-    struct Key {
-        const void *k;
-        int dev, threads;
-        size_t smem;
-    };
     static std::mutex mu;
-    static Key keys[64];
-    static int vals[64];
-    static int used = 0;
+    static GridCache cache;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const GridKey key{kernel, dev, threads, smem};
     std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < used; i++)
-        if (keys[i].k == kernel && keys[i].dev == dev && keys[i].threads == threads &&
-            keys[i].smem == smem)
-            return vals[i];
+    const int known = cache.find(key);
+    if (known > 0) return known;
     DeviceInfo di;
     int per_sm = 0;
     if (device_info(&di) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess)
         return 0;
     const int v = (per_sm > 0 ? per_sm : 1) * di.sm_count;
-    if (used < 64) {
-        keys[used] = {kernel, dev, threads, smem};
-        vals[used] = v;
-        used++;
-    }
+    cache.add(key, v);
     return v;
 }
 
