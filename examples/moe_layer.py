@@ -23,7 +23,8 @@ def quantize(w):
     """Weights [E, rows, K] to E2M1 codes, an E4M3 scale per 16 columns and a factor per expert."""
     E, rows, K = w.shape
     factor = w.abs().amax((1, 2)).float() / (448 * 6)
-    groups = w.float().view(E, rows, K // 16, 16) / factor[:, None, None, None]
+    whole = torch.where(factor > 0, factor, 1.0)             # (an expert of zeros stays one)
+    groups = w.float().view(E, rows, K // 16, 16) / whole[:, None, None, None]
     scales = (groups.abs().amax(-1) / 6).to(torch.float8_e4m3fn)
     q = groups / scales.float().clamp(min=2.0 ** -9).unsqueeze(-1)
     mids = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], device=w.device)
