@@ -166,3 +166,28 @@ def test_combine_backward(N, k, H, share, spare):
         assert np.array_equal(bf16_host(d_y), want)
         assert np.all(np.abs(host(dw).reshape(-1) - dot) <= H * U * mag)
         assert int(st.item()) == 0
+
+
+def test_gradients_on_another_stream():
+    """The same bytes on a stream that is not the current one."""
+    r = np.random.default_rng(1)
+    S, T, E, k, H = 2, 700, 48, 4, 256
+    N = S * T
+    lt = f32_dev(r.standard_normal((S, T, E), np.float32))
+    ids, w = i32_dev(r.integers(0, E, (S, T, k))), f32_dev(r.random((S, T, k), np.float32))
+    dw_in, lse = f32_dev(r.standard_normal((S, T, k), np.float32)), torch.logsumexp(lt, -1)
+    counts, n, d = i32_dev(r.integers(0, 99, (S, E))), i32_dev([T, T]), f32_dev([0.7, -0.3])
+    y, g = (torch.randn(rows, H, device=DEV).bfloat16() for rows in (N * k, N))
+    pair_row = torch.randperm(N * k, device=DEV).int().view(S, T, k)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    results = []
+    for stream in (None, side):
+        out, d_y, dw = torch.full_like(lt, -7), torch.full_like(y, -7), torch.full_like(w, -7)
+        torch.cuda.synchronize()
+        m.moe_route_backward(lt, ids, w, dw_in, lse, counts, n, d, out, stream=stream)
+        m.moe_combine_backward(g.view(S, T, H), y, pair_row, w, d_y, dw, stream=stream)
+        torch.cuda.synchronize()
+        results.append((out, d_y, dw))
+    for one, other in zip(*results):
+        assert torch.equal(one, other) and not bool((one == -7).all())
