@@ -24,10 +24,12 @@ namespace {
 constexpr int kCbThreads = 256;
 constexpr int kCbWarps = kCbThreads / 32;
 constexpr int kCbCtas = 2;    // CTAs per SM: 128 registers a thread
-// Rows of a token taken at once, where a token has more than two rows on average
-// or not.  4,096 tokens x 6 rows of 5,120: 92.9 us at eight, 102.7 at two; 16,384
+// Rows of a token taken at once, where the buffer has more than two rows a token or not
+// (how many of them are in use only the device knows).  4,096 tokens x 6 rows of 5,120: 92.9 us at eight, 102.7 at two; 16,384
 // tokens x one row of 2,048 (of 8 picks): 37.4 us at two, 59.7 at eight (34.0 at two
-// since warps take tokens as they come free).
+// since warps take tokens as they come free).  A buffer much larger than its rows takes the
+// form for many and has every unused row set to zero: the same tokens take 127 us in one of
+// 131,072 rows.
 constexpr int kManyRows = 8, kFewRows = 2;
 
 __device__ __forceinline__ float dot_bf16x8(int4 a, int4 b, float acc)

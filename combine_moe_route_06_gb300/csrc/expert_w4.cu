@@ -22,7 +22,7 @@
 // What bounds it: with up to some 80 rows an expert the bytes of the weights in use
 // (9/16 byte each), above that the tensor core.  48 rows over 31 of 48 experts of
 // 4,096 x 5,120 weights take 62 us, 5.9 TB/s; 16,384 rows over 8 experts of 2,816 x
-// 2,048 take 167 to 174 us, 1.1 PFLOP/s.  About 10 us of a call are its start (row counts,
+// 2,048 take 165 to 174 us, 1.1 PFLOP/s.  About 10 us of a call are its start (row counts,
 // first rows, first weights: 7 us before the first MMA) and its end.
 #include <cuda_bf16.h>
 #include <float.h>
@@ -96,7 +96,7 @@ __host__ __device__ __forceinline__ int64_t row_groups(int a_rows, int E)
 constexpr int kRowsThreads = 128;
 constexpr int kRowsUnseen = 512;    // rows that are read before it is known whether they are used
 constexpr int kRowsCtas = 8;        // CTAs per SM
-// A row per CTA, or with more rows than kRowsWide one per warp, which keeps more bytes
+// A row per CTA, or where `a` has more rows than kRowsWide (in use or not) one per warp, which keeps more bytes
 // in flight (16,384 rows of 2,048: 24 us by warps, 35 by CTAs) but takes longer for one.
 constexpr int kRowsWide = 4096;
 

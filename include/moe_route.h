@@ -739,7 +739,9 @@ moe_status_t moe_w4_pack(const uint8_t *codes, const uint8_t *scales, int E, int
  *   gated 0:  y[r][n] = bf16_rne( sum_k a[r][k] W_e[n][k] ),              n < N
  *   gated 1:  y[r][n] = bf16_rne( silu(sum_k a[r][k] W_e[n][k])
  *                                 * sum_k a[r][k] W_e[N + n][k] )
- * with silu(v) = v / (1 + exp(-v)), sums in fp32 and one rounding at the end.
+ * with silu(v) = v / (1 + exp(-v)), sums in fp32 and one rounding at the end.  A row of
+ * `a` enters as fp16 with a power of two of its own: values down to 2^-28 of the row's
+ * largest keep all their bits, smaller ones a step of 2^-39 of it.
  *   a        [a_rows][K] bf16 in, y [a_rows][N] bf16 out, apart from each other.
  *   expert_offsets  [E+1] int32: expert e's rows are [offsets[e], offsets[e+1])
  *            (moe_permute_to_experts; for one partition its slice of the E+1
@@ -825,8 +827,10 @@ moe_status_t moe_route_backward(const void *logits, int logits_type, int S, int 
  * MOE_ERR_INVALID_ARG).  No two pairs share a row (moe_permute_to_experts and
  * the masked layout give every pair its own).
  *   d_out, y   [S][T][H], [y_rows][H] bf16 in; pair_row, topk_w as moe_combine.
- *   recv_pair  [y_rows] int32 or NULL: rows of d_y with recv_pair < 0 (padding)
- *              are set to zero; with NULL they are not written.
+ *   recv_pair  [y_rows] int32 or NULL: rows of d_y with recv_pair < 0 (padding, and
+ *              what lies past the last run) are set to zero; with NULL they are not
+ *              written.  The time follows y_rows: a caller that knows how many rows
+ *              of a large buffer are in use gives that number.
  *   d_y        [y_rows][H] bf16 out, apart from the inputs; d_topk_w [S][T][k] out.
  * With one receiving partition this is that partition's part; the d_topk_w of
  * all partitions add up.  The gradient of dispatch (one row copied to several)
