@@ -3,8 +3,8 @@
 The five calls of the MoE token path (route, dispatch layout, pack, receiver
 permute, combine) run in hand-written sm_103a kernels behind a C ABI
 (``include/moe_route.h``).  This module only marshals torch tensors (device
-pointers, sizes, the current CUDA stream) through ctypes, or for the training
-and 4-bit expert calls through compiled entry points; PyTorch supplies
+pointers, sizes, the current CUDA stream) through ctypes, or for the training,
+expert and norm calls through compiled entry points; PyTorch supplies
 device memory and streams.  There is no fallback: if the library is not
 built, importing works but every call raises ``MoeLibraryMissing``.
 
@@ -43,6 +43,9 @@ __all__ = [
     "MOE_TYPE_F32", "MOE_TYPE_BF16", "moe_balance_loss", "moe_balance_loss_workspace_bytes",
     "moe_route_backward", "moe_combine_backward", "moe_w4_bytes", "moe_w4_pack",
     "moe_expert_product_w4", "moe_expert_product_w4_workspace_bytes",
+    "moe_expert_product", "moe_expert_product_workspace_bytes", "moe_expert_product_backward",
+    "moe_expert_product_backward_workspace_bytes", "moe_rms_norm", "moe_rms_norm_backward",
+    "moe_rms_norm_backward_workspace_bytes",
     "MoePath", "trace_enable", "trace_disable", "trace_reset", "trace_records",
 ]
 
@@ -99,7 +102,7 @@ def load_library() -> ctypes.CDLL:
             raise MoeLibraryMissing(
                 f"{path} is not built; run `python -c 'import __graft_entry__ as g; g.build()'`")
         lib = ctypes.CDLL(path)
-        P, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+        P, i32, sz, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
         sigs = {
             "moe_version": ([], ctypes.c_int),
             "moe_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -167,6 +170,16 @@ def load_library() -> ctypes.CDLL:
                                       ctypes.c_int),
             "moe_w4_bytes": ([i32, i32, i32, i32], sz),
             "moe_expert_product_w4_workspace_bytes": ([i32, i32, i32, i32], sz),
+            "moe_expert_product_workspace_bytes": ([i32, i32, i32, i32, i32], sz),
+            "moe_expert_product": ([P, i32, P, P, i32, P, i32, i32, i32, i32, P, P, P, sz, P, P],
+                                   ctypes.c_int),
+            "moe_expert_product_backward_workspace_bytes": ([i32, i32, i32, i32], sz),
+            "moe_expert_product_backward": ([P, P, i32, P, P, i32, P, P, i32, i32, i32, P, P, i32, P,
+                                             sz, P, P], ctypes.c_int),
+            "moe_rms_norm": ([P, P, i32, P, i32, i64, i32, ctypes.c_float, P, P, P, P], ctypes.c_int),
+            "moe_rms_norm_backward_workspace_bytes": ([i64, i32], sz),
+            "moe_rms_norm_backward": ([P, P, i32, P, i32, P, i64, i32, ctypes.c_float, P, P, P, P, sz,
+                                       P], ctypes.c_int),
             "moe_trace_enable": ([ctypes.c_char_p, i32], ctypes.c_int),
             "moe_trace_disable": ([], None),
             "moe_trace_reset": ([], None),
@@ -222,7 +235,7 @@ _ops_module = None
 
 
 def _ops():
-    """The compiled entry points (csrc/binding.cpp) of the training and 4-bit expert calls."""
+    """The compiled entry points (csrc/binding.cpp) of the training, expert and norm calls."""
     global _ops_module
     if _ops_module is None:
         load_library()
@@ -809,6 +822,61 @@ def moe_expert_product_w4(a, w4, w_factor, y, ws, expert_offsets=None, masked_co
     rows by expert_offsets i32 [E+1] or by masked_counts i32 [E] with block_rows; w_factor f32 [E]."""
     rc = _ops().expert_product_w4(a, w4, w_factor, y, ws, expert_offsets, masked_counts, block_rows,
                                   gated, dev_status, stream)
+    if rc:
+        _check(rc)
+
+
+def moe_expert_product_workspace_bytes(a_rows: int, E: int, N: int, K: int, gated: bool = False) -> int:
+    return int(load_library().moe_expert_product_workspace_bytes(a_rows, E, N, K, int(gated)))
+
+
+def moe_expert_product(a, w, y, ws, expert_offsets=None, masked_counts=None, block_rows=0, gated=False,
+                       pre=None, dev_status=None, stream=None):
+    """a bf16 [rows,K] times every expert's bf16 weights w [E,N,K] (gated: [E,2N,K], gate rows, then
+    up rows) -> y bf16 [rows,N]; the experts' rows by expert_offsets i32 [E+1] or by masked_counts
+    i32 [E] with block_rows.  pre bf16 [rows,2N] (gated) takes gate and up for the way back."""
+    rc = _ops().expert_product(a, w, y, ws, expert_offsets, masked_counts, block_rows, gated, pre,
+                               dev_status, stream)
+    if rc:
+        _check(rc)
+
+
+def moe_expert_product_backward_workspace_bytes(a_rows: int, E: int, N: int, K: int) -> int:
+    return int(load_library().moe_expert_product_backward_workspace_bytes(a_rows, E, N, K))
+
+
+def moe_expert_product_backward(d_y, a, w, ws, d_a=None, d_w=None, expert_offsets=None,
+                                masked_counts=None, block_rows=0, pre=None, dev_status=None,
+                                stream=None):
+    """Gradient of y = a W^T: d_y bf16 [rows,N], a bf16 [rows,K], w bf16 [E,N,K] -> d_a bf16 [rows,K]
+    and d_w f32 or bf16 [E,N,K], each where it is given (a may be None without d_w).  With pre bf16
+    [rows,2K], a was silu(gate) * up of it and d_a [rows,2K] is the gradient in gate and up."""
+    rc = _ops().expert_product_backward(d_y, a, w, ws, d_a, d_w, expert_offsets, masked_counts,
+                                        block_rows, pre, dev_status, stream)
+    if rc:
+        _check(rc)
+
+
+def moe_rms_norm(x, weight, y=None, record=None, residual=None, residual_out=None, eps=1e-6,
+                 stream=None):
+    """RMS norm of x + residual: x bf16 [...,H], residual f32 or bf16 [...,H], weight f32 or bf16 [H]
+    -> y bf16 [...,H], record uint8 [...,H+H/32] (the MXFP8 records of y; H % 32 == 0), residual_out
+    (the sum, of the residual's type; may be the residual itself), each where it is given."""
+    rc = _ops().rms_norm(x, weight, y, record, residual, residual_out, eps, stream)
+    if rc:
+        _check(rc)
+
+
+def moe_rms_norm_backward_workspace_bytes(rows: int, H: int) -> int:
+    return int(load_library().moe_rms_norm_backward_workspace_bytes(rows, H))
+
+
+def moe_rms_norm_backward(d_y, h, weight, d_h, ws=None, d_weight=None, d_residual=None, d_x=None,
+                          eps=1e-6, stream=None):
+    """Gradient of moe_rms_norm: d_y bf16 [...,H], h f32 or bf16 [...,H] (what was normed:
+    residual_out, or x) -> d_h of h's type (+ d_residual of that type), d_x its bf16 copy, d_weight
+    f32 [H] (with ws), each but d_h where it is given."""
+    rc = _ops().rms_norm_backward(d_y, h, weight, d_h, ws, d_weight, d_residual, d_x, eps, stream)
     if rc:
         _check(rc)
 

@@ -1081,4 +1081,175 @@ moe_status_t moe_expert_product_w4(const uint16_t *a, int a_rows, const int32_t 
                        __func__);
 }
 
+static moe_status_t check_product(const char *fn, int a_rows, int E, int N, int K)
+{
+    REQUIRE(a_rows >= 0, "%s: a_rows=%d must be >= 0", fn, a_rows);
+    REQUIRE(E >= 1 && E <= kMaxE, "%s: E=%d must be in [1, %d]", fn, E, kMaxE);
+    REQUIRE(N >= 8 && N % 8 == 0 && N <= (1 << 20), "%s: N=%d must be a multiple of 8 in [8, 2^20]",
+            fn, N);
+    REQUIRE(K >= 8 && K % 8 == 0 && K <= (1 << 20), "%s: K=%d must be a multiple of 8 in [8, 2^20]",
+            fn, K);
+    // the steps of the call, 64 long at 128 x 128 outputs or more, are numbered in 32 bits
+    const int64_t rows = (int64_t)a_rows / 64 + 2 * E, n = (N + 63) / 64, k = (K + 63) / 64;
+    REQUIRE(E * n * k < ((int64_t)1 << 31) && rows * n < ((int64_t)1 << 31) / k,
+            "%s: a_rows=%d rows of E=%d experts of %d x %d weights are too many for one call", fn,
+            a_rows, E, N, K);
+    return MOE_OK;
+}
+
+static moe_status_t check_rows_by(const char *fn, int a_rows, const int32_t *expert_offsets,
+                                  const int32_t *masked_counts, int block_rows, int E)
+{
+    REQUIRE((expert_offsets != nullptr) != (masked_counts != nullptr),
+            "%s: give `expert_offsets` or `masked_counts`, not both", fn);
+    REQUIRE(aligned(expert_offsets, 4), "%s: `expert_offsets` is not 4-byte aligned", fn);
+    REQUIRE(aligned(masked_counts, 4), "%s: `masked_counts` is not 4-byte aligned", fn);
+    if (masked_counts) {
+        REQUIRE(block_rows >= 1, "%s: block_rows=%d must be >= 1", fn, block_rows);
+        REQUIRE((int64_t)E * block_rows <= a_rows, "%s: a_rows=%d < E * block_rows=%lld", fn, a_rows,
+                (long long)E * block_rows);
+    }
+    return MOE_OK;
+}
+
+size_t moe_expert_product_workspace_bytes(int a_rows, int E, int N, int K, int gated)
+{
+    static const char fn[] = "moe_expert_product_workspace_bytes";
+    if (gated != 0 && gated != 1) {
+        fail(MOE_ERR_INVALID_ARG, "%s: gated=%d must be 0 or 1", fn, gated);
+        return 0;
+    }
+    if (check_product(fn, a_rows, E, N, K) != MOE_OK) return 0;
+    return expert_product_ws_bytes();
+}
+
+moe_status_t moe_expert_product(const uint16_t *a, int a_rows, const int32_t *expert_offsets,
+                                const int32_t *masked_counts, int block_rows, const uint16_t *w,
+                                int E, int N, int K, int gated, uint16_t *y, uint16_t *pre, void *ws,
+                                size_t ws_bytes, uint32_t *dev_status, cudaStream_t stream)
+{
+    MOE_CALL_RANGE();
+    REQUIRE(gated == 0 || gated == 1, "%s: gated=%d must be 0 or 1", __func__, gated);
+    moe_status_t st = check_product(__func__, a_rows, E, N, K);
+    if (st != MOE_OK) return st;
+    st = check_rows_by(__func__, a_rows, expert_offsets, masked_counts, block_rows, E);
+    if (st != MOE_OK) return st;
+    REQUIRE(gated || !pre, "%s: `pre` is of gated products", __func__);
+    REQUIRE_ARR(a, (int64_t)a_rows * K, 16);
+    REQUIRE_ARR(w, 1, 16);
+    REQUIRE_ARR(y, (int64_t)a_rows * N, 16);
+    REQUIRE(aligned(pre, 16), "%s: `pre` is not 16-byte aligned", __func__);
+    REQUIRE_STATUS(dev_status);
+    const size_t need = expert_product_ws_bytes();
+    REQUIRE_ARR(ws, need, 256);
+    REQUIRE(ws_bytes >= need, "%s: ws_bytes=%zu < required %zu", __func__, ws_bytes, need);
+    return cuda_status(launch_expert_product(a, a_rows, expert_offsets, masked_counts, block_rows, w,
+                                             E, N, K, gated != 0, y, pre, ws, dev_status, stream),
+                       __func__);
+}
+
+size_t moe_expert_product_backward_workspace_bytes(int a_rows, int E, int N, int K)
+{
+    if (check_product("moe_expert_product_backward_workspace_bytes", a_rows, E, N, K) != MOE_OK) return 0;
+    return expert_product_ws_bytes();
+}
+
+moe_status_t moe_expert_product_backward(const uint16_t *d_y, const uint16_t *a, int a_rows,
+                                         const int32_t *expert_offsets, const int32_t *masked_counts,
+                                         int block_rows, const uint16_t *w, const uint16_t *pre,
+                                         int E, int N, int K, uint16_t *d_a, void *d_w, int d_w_type,
+                                         void *ws, size_t ws_bytes, uint32_t *dev_status,
+                                         cudaStream_t stream)
+{
+    MOE_CALL_RANGE();
+    moe_status_t st = check_product(__func__, a_rows, E, N, K);
+    if (st != MOE_OK) return st;
+    st = check_rows_by(__func__, a_rows, expert_offsets, masked_counts, block_rows, E);
+    if (st != MOE_OK) return st;
+    REQUIRE(d_w_type == MOE_TYPE_F32 || d_w_type == MOE_TYPE_BF16, "%s: d_w_type=%d", __func__, d_w_type);
+    // (rows of d_a have no address where there are no rows)
+    REQUIRE(d_a || d_w || a_rows == 0, "%s: neither `d_a` nor `d_w` is wanted", __func__);
+    REQUIRE(d_a || !pre, "%s: `pre` without `d_a`", __func__);
+    REQUIRE_ARR(d_y, (int64_t)a_rows * N, 16);
+    if (d_w) REQUIRE_ARR(a, (int64_t)a_rows * K, 16);
+    if (d_a) REQUIRE_ARR(w, 1, 16);
+    REQUIRE(aligned(pre, 16), "%s: `pre` is not 16-byte aligned", __func__);
+    REQUIRE(aligned(d_a, 16), "%s: `d_a` is not 16-byte aligned", __func__);
+    REQUIRE(aligned(d_w, 16), "%s: `d_w` is not 16-byte aligned", __func__);
+    REQUIRE_STATUS(dev_status);
+    const size_t need = expert_product_ws_bytes();
+    REQUIRE_ARR(ws, need, 256);
+    REQUIRE(ws_bytes >= need, "%s: ws_bytes=%zu < required %zu", __func__, ws_bytes, need);
+    return cuda_status(launch_expert_product_backward(d_y, a, a_rows, expert_offsets, masked_counts,
+                                                      block_rows, w, pre, E, N, K, d_a, d_w, d_w_type,
+                                                      ws, dev_status, stream),
+                       __func__);
+}
+
+static moe_status_t check_norm(const char *fn, int64_t rows, int H, int weight_type, float eps)
+{
+    REQUIRE(rows >= 0 && rows < ((int64_t)1 << 31), "%s: rows=%lld must be in [0, 2^31)", fn,
+            (long long)rows);
+    REQUIRE(H >= 8 && H % 8 == 0 && H <= 32768, "%s: H=%d must be a multiple of 8 in [8, 32768]", fn, H);
+    REQUIRE(weight_type == MOE_TYPE_F32 || weight_type == MOE_TYPE_BF16, "%s: weight_type=%d", fn,
+            weight_type);
+    REQUIRE(eps > 0.f && eps <= 1e30f, "%s: eps=%g must be positive", fn, (double)eps);
+    return MOE_OK;
+}
+
+moe_status_t moe_rms_norm(const uint16_t *x, const void *residual, int residual_type,
+                          const void *weight, int weight_type, int64_t rows, int H, float eps,
+                          void *residual_out, uint16_t *y, uint8_t *record, cudaStream_t stream)
+{
+    MOE_CALL_RANGE();
+    moe_status_t st = check_norm(__func__, rows, H, weight_type, eps);
+    if (st != MOE_OK) return st;
+    REQUIRE(residual_type == MOE_TYPE_F32 || residual_type == MOE_TYPE_BF16, "%s: residual_type=%d",
+            __func__, residual_type);
+    REQUIRE_ARR(weight, H, 16);
+    REQUIRE_ARR(x, rows * H, 16);
+    REQUIRE(residual || !residual_out || rows == 0, "%s: `residual_out` without `residual`", __func__);
+    REQUIRE(y || record || rows == 0, "%s: neither `y` nor `record` is wanted", __func__);
+    REQUIRE(!record || H % 32 == 0, "%s: H=%d must be a multiple of 32 for records", __func__, H);
+    REQUIRE(aligned(residual, 16), "%s: `residual` is not 16-byte aligned", __func__);
+    REQUIRE(aligned(residual_out, 16), "%s: `residual_out` is not 16-byte aligned", __func__);
+    REQUIRE(aligned(y, 16), "%s: `y` is not 16-byte aligned", __func__);
+    REQUIRE(aligned(record, 8), "%s: `record` is not 8-byte aligned", __func__);
+    return cuda_status(launch_rms_norm(x, residual, residual_type, weight, weight_type, rows, H, eps,
+                                       residual_out, y, record, stream),
+                       __func__);
+}
+
+size_t moe_rms_norm_backward_workspace_bytes(int64_t rows, int H)
+{
+    if (check_norm("moe_rms_norm_backward_workspace_bytes", rows, H, MOE_TYPE_F32, 1.f) != MOE_OK) return 0;
+    return rms_norm_backward_ws_bytes(rows, H);
+}
+
+moe_status_t moe_rms_norm_backward(const uint16_t *d_y, const void *h, int h_type, const void *weight,
+                                   int weight_type, const void *d_residual, int64_t rows, int H,
+                                   float eps, void *d_h, uint16_t *d_x, float *d_weight, void *ws,
+                                   size_t ws_bytes, cudaStream_t stream)
+{
+    MOE_CALL_RANGE();
+    moe_status_t st = check_norm(__func__, rows, H, weight_type, eps);
+    if (st != MOE_OK) return st;
+    REQUIRE(h_type == MOE_TYPE_F32 || h_type == MOE_TYPE_BF16, "%s: h_type=%d", __func__, h_type);
+    REQUIRE_ARR(weight, H, 16);
+    REQUIRE_ARR(d_y, rows * H, 16);
+    REQUIRE_ARR(h, rows * H, 16);
+    REQUIRE_ARR(d_h, rows * H, 16);
+    REQUIRE(aligned(d_residual, 16), "%s: `d_residual` is not 16-byte aligned", __func__);
+    REQUIRE(aligned(d_x, 16), "%s: `d_x` is not 16-byte aligned", __func__);
+    REQUIRE(aligned(d_weight, 4), "%s: `d_weight` is not 4-byte aligned", __func__);
+    if (d_weight) {
+        const size_t need = rms_norm_backward_ws_bytes(rows, H);
+        REQUIRE_ARR(ws, need, 256);
+        REQUIRE(ws_bytes >= need, "%s: ws_bytes=%zu < required %zu", __func__, ws_bytes, need);
+    }
+    return cuda_status(launch_rms_norm_backward(d_y, h, h_type, weight, weight_type, d_residual, rows, H,
+                                                eps, d_h, d_x, d_weight, ws, stream),
+                       __func__);
+}
+
 }  // extern "C"

@@ -1,4 +1,4 @@
-// binding.cpp -- Python entry points of the training and 4-bit expert calls.
+// binding.cpp -- Python entry points of the training, expert and norm calls.
 //
 // They check torch tensors and call the C ABI on the current stream, like the
 // ctypes functions of the package, but read a tensor's type, sizes and address
@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -253,6 +254,165 @@ moe_status_t expert_product_w4(Args a)
         data<void>(w), (size_t)w.numel(), status_word(a[status]), stream_of(a[stream]));
 }
 
+// The calls below also see to it that all tensors are on the current device.
+void here(const at::Tensor &t, const char *name, const at::Tensor &first)
+{
+    if (t.device() != first.device())
+        refuse(PyExc_ValueError, std::string(name) + ": is on another device than the other tensors");
+}
+template <typename T>
+T *here_shaped(PyObject *o, const char *name, int types, at::IntArrayRef shape, const at::Tensor &first)
+{
+    if (o == Py_None) return nullptr;
+    const at::Tensor &t = shaped(o, name, types, shape);
+    here(t, name, first);
+    return data<T>(t);
+}
+void current(const at::Tensor &first, const char *name)
+{
+    if (first.device().index() != c10::cuda::current_device())
+        refuse(PyExc_ValueError, std::string(name) + ": is not on the current device");
+}
+
+struct ProductShape {
+    int rows, E, N, K;
+    const int32_t *offsets, *counts;
+    int block_rows;
+    void *ws;
+    size_t ws_bytes;
+};
+
+// What both products have: the sizes by the rows' and the weights' shapes, the experts'
+// rows and the workspace.
+ProductShape product_shape(const at::Tensor &w, int64_t rows, PyObject *offsets, PyObject *counts,
+                           PyObject *block_rows, PyObject *ws)
+{
+    current(w, "w");
+    const at::Tensor &s = tensor(ws, "ws", kU8);
+    here(s, "ws", w);
+    const int64_t E = w.size(0);
+    return {size32(rows, "a_rows"), size32(E, "E"), size32(w.size(1), "N"), size32(w.size(2), "K"),
+            here_shaped<int32_t>(offsets, "expert_offsets", kI32, {E + 1}, w),
+            here_shaped<int32_t>(counts, "masked_counts", kI32, {E}, w), int32(block_rows, "block_rows"),
+            data<void>(s), (size_t)s.numel()};
+}
+
+moe_status_t expert_product(Args a)
+{
+    enum { x, w, y, ws, offsets, counts, block_rows, gated, pre, status, stream };
+    const at::Tensor &t = ranked(a[w], "w", kRow, 3);
+    const int64_t rows = ranked(a[x], "a", kRow, 2).size(0);
+    const bool two = truth(a[gated]);
+    if (two && t.size(1) % 2)
+        refuse(PyExc_ValueError, "w: gated weights have an even number of rows, got " +
+                                     std::to_string(t.size(1)));
+    const ProductShape p = product_shape(t, rows, a[offsets], a[counts], a[block_rows], a[ws]);
+    const int N = two ? p.N / 2 : p.N;
+    uint16_t *const out = here_shaped<uint16_t>(a[y], "y", kRow, {rows, N}, t);
+    if (a[y] == Py_None) refuse(PyExc_TypeError, "y: expected a torch.Tensor");
+    return enqueue(moe_expert_product, here_shaped<uint16_t>(a[x], "a", kRow, {rows, p.K}, t), p.rows,
+                   p.offsets, p.counts, p.block_rows, data<uint16_t>(t), p.E, N, p.K, (int)two, out,
+                   here_shaped<uint16_t>(a[pre], "pre", kRow, {rows, 2 * (int64_t)N}, t), p.ws, p.ws_bytes,
+                   status_word(a[status]), stream_of(a[stream]));
+}
+
+moe_status_t expert_product_backward(Args a)
+{
+    enum { d_y, x, w, ws, d_a, d_w, offsets, counts, block_rows, pre, status, stream };
+    const at::Tensor &t = ranked(a[w], "w", kRow, 3);
+    const int64_t rows = ranked(a[d_y], "d_y", kRow, 2).size(0);
+    const ProductShape p = product_shape(t, rows, a[offsets], a[counts], a[block_rows], a[ws]);
+    const bool gate = a[pre] != Py_None;
+    if (a[d_w] != Py_None && a[x] == Py_None) refuse(PyExc_ValueError, "a: needed with d_w");
+    if (gate && a[d_a] == Py_None) refuse(PyExc_ValueError, "d_a: needed with pre");
+    if (a[d_a] == Py_None && a[d_w] == Py_None)
+        refuse(PyExc_ValueError, "d_a, d_w: neither is wanted");
+    void *const weights = here_shaped<void>(a[d_w], "d_w", kF32 | kBf16, t.sizes(), t);
+    const int type = weights && THPVariable_Unpack(a[d_w]).scalar_type() == at::kFloat ? MOE_TYPE_F32 : MOE_TYPE_BF16;
+    return enqueue(moe_expert_product_backward, here_shaped<uint16_t>(a[d_y], "d_y", kRow, {rows, p.N}, t),
+                   here_shaped<uint16_t>(a[x], "a", kRow, {rows, p.K}, t), p.rows, p.offsets, p.counts,
+                   p.block_rows, data<uint16_t>(t),
+                   here_shaped<uint16_t>(a[pre], "pre", kRow, {rows, 2 * (int64_t)p.K}, t), p.E, p.N, p.K,
+                   here_shaped<uint16_t>(a[d_a], "d_a", kRow, {rows, (gate ? 2 : 1) * (int64_t)p.K}, t),
+                   weights, type, p.ws, p.ws_bytes, status_word(a[status]), stream_of(a[stream]));
+}
+
+int norm_type(const at::Tensor &t) { return t.scalar_type() == at::kFloat ? MOE_TYPE_F32 : MOE_TYPE_BF16; }
+
+float positive(PyObject *o, const char *name)
+{
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Refused{};
+    if (!(v > 0)) refuse(PyExc_ValueError, std::string(name) + ": must be positive");
+    return (float)v;
+}
+
+// Rows [..., H] of a norm: any leading sizes, the same for all of its tensors.
+int64_t row_count(const at::Tensor &t, const char *name)
+{
+    if (t.dim() < 1 || t.size(-1) == 0)
+        refuse(PyExc_ValueError, std::string(name) + ": expected rows, got shape " + shape_text(t.sizes()));
+    return t.numel() / t.size(-1);
+}
+
+moe_status_t rms_norm(Args a)
+{
+    enum { x, weight, y, record, residual, residual_out, eps, stream };
+    const at::Tensor &t = tensor(a[x], "x", kRow);
+    const int64_t rows = row_count(t, "x"), H = t.size(-1);
+    current(t, "x");
+    const at::Tensor &w = shaped(a[weight], "weight", kF32 | kBf16, {H});
+    here(w, "weight", t);
+    const bool add = a[residual] != Py_None;
+    const int kind = add && tensor(a[residual], "residual", kF32 | kBf16).scalar_type() == at::kFloat ? kF32 : kBf16;
+    if (!add && a[residual_out] != Py_None) refuse(PyExc_ValueError, "residual_out: without a residual");
+    if (a[y] == Py_None && a[record] == Py_None) refuse(PyExc_ValueError, "y, record: neither is wanted");
+    uint8_t *bytes = nullptr;
+    if (a[record] != Py_None) {
+        const at::Tensor &r = tensor(a[record], "record", kU8);
+        here(r, "record", t);
+        if (r.dim() < 1 || r.size(-1) != H + H / 32 || r.numel() != rows * (H + H / 32))
+            refuse(PyExc_ValueError, "record: expected " + std::to_string(rows) + " rows of " +
+                                         std::to_string(H + H / 32) + " bytes, got shape " +
+                                         shape_text(r.sizes()));
+        bytes = data<uint8_t>(r);
+    }
+    return enqueue(moe_rms_norm, data<uint16_t>(t), here_shaped<void>(a[residual], "residual", kind, t.sizes(), t),
+                   kind == kF32 ? MOE_TYPE_F32 : MOE_TYPE_BF16, data<void>(w), norm_type(w), rows,
+                   size32(H, "H"), positive(a[eps], "eps"),
+                   here_shaped<void>(a[residual_out], "residual_out", kind, t.sizes(), t),
+                   here_shaped<uint16_t>(a[y], "y", kRow, t.sizes(), t), bytes, stream_of(a[stream]));
+}
+
+moe_status_t rms_norm_backward(Args a)
+{
+    enum { d_y, h, weight, d_h, ws, d_weight, d_residual, d_x, eps, stream };
+    const at::Tensor &t = tensor(a[d_y], "d_y", kRow);
+    const int64_t rows = row_count(t, "d_y"), H = t.size(-1);
+    current(t, "d_y");
+    const at::Tensor &w = shaped(a[weight], "weight", kF32 | kBf16, {H});
+    here(w, "weight", t);
+    const at::Tensor &r = shaped(a[h], "h", kF32 | kBf16, t.sizes());
+    here(r, "h", t);
+    const int kind = r.scalar_type() == at::kFloat ? kF32 : kBf16;
+    if (a[d_h] == Py_None) refuse(PyExc_TypeError, "d_h: expected a torch.Tensor");
+    void *scratch = nullptr;
+    size_t bytes = 0;
+    if (a[d_weight] != Py_None) {
+        const at::Tensor &s = tensor(a[ws], "ws", kU8);
+        here(s, "ws", t);
+        scratch = data<void>(s);
+        bytes = (size_t)s.numel();
+    }
+    return enqueue(moe_rms_norm_backward, data<uint16_t>(t), data<void>(r), norm_type(r), data<void>(w),
+                   norm_type(w), here_shaped<void>(a[d_residual], "d_residual", kind, t.sizes(), t), rows,
+                   size32(H, "H"), positive(a[eps], "eps"),
+                   here_shaped<void>(a[d_h], "d_h", kind, t.sizes(), t),
+                   here_shaped<uint16_t>(a[d_x], "d_x", kRow, t.sizes(), t),
+                   here_shaped<float>(a[d_weight], "d_weight", kF32, {H}, t), scratch, bytes,
+                   stream_of(a[stream]));
+}
+
 template <moe_status_t (*CALL)(Args), int COUNT>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
@@ -282,6 +442,10 @@ PyMethodDef methods[] = {
     method<combine_backward, 9>("combine_backward"),
     method<w4_pack, 5>("w4_pack"),
     method<expert_product_w4, 11>("expert_product_w4"),
+    method<expert_product, 11>("expert_product"),
+    method<expert_product_backward, 12>("expert_product_backward"),
+    method<rms_norm, 8>("rms_norm"),
+    method<rms_norm_backward, 10>("rms_norm_backward"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -28,6 +28,7 @@
 #include <float.h>
 
 #include "common.cuh"
+#include "gate.cuh"
 #include "launch.h"
 #include "tensor.cuh"
 #include "trace.h"
@@ -433,21 +434,6 @@ __device__ __forceinline__ void tile_sums(const Finish &p, int h, int c0,
 #pragma unroll
         for (int b = 0; b < BLOCKS; b++) v[b][j] = v[b][j] * p.f * by;   // (by alone could overflow)
     }
-}
-
-// silu(gate) * up.  With h = exp(-|gate| / 2), silu is gate / (1 + h^2), for a negative
-// gate times h^2, so that nothing leaves fp32 (exp(-gate) itself is past it below -88.7,
-// and its reciprocal below -87.3).  Of h the approximate exp2 takes 2^-22 and the rounded
-// argument |gate| 2^-24, of the result the reciprocal 2^-23: below 2^-15 in all for
-// |gate| <= 120, past which the result leaves bf16's range; its rounding is 2^-9.
-__device__ __forceinline__ float gated_output(float gate, float up)
-{
-    constexpr float kHalfLog2E = 0.72134752044448f;
-    float h, inv;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(-kHalfLog2E * fabsf(gate)));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(h, h, 1.f)));
-    const float by = gate < 0.f ? h : 1.f;
-    return (gate * by) * inv * (by * up);
 }
 
 // Outputs of this thread's weight row(s), COLS rows of `a` at a time.  dst: the

@@ -229,4 +229,27 @@ cudaError_t launch_expert_w4(const uint16_t *a, int a_rows, const int32_t *offse
                              const float *factor, int E, int N, int K, bool gated, uint16_t *y,
                              void *ws, uint32_t *dev_status, cudaStream_t st);
 
+// The experts' products with bf16 weights and their gradients (expert_product.cu).
+size_t expert_product_ws_bytes();
+cudaError_t launch_expert_product(const uint16_t *a, int a_rows, const int32_t *offsets,
+                                  const int32_t *counts, int block_rows, const uint16_t *w, int E,
+                                  int N, int K, bool gated, uint16_t *y, uint16_t *pre, void *ws,
+                                  uint32_t *dev_status, cudaStream_t st);
+cudaError_t launch_expert_product_backward(const uint16_t *d_y, const uint16_t *a, int a_rows,
+                                           const int32_t *offsets, const int32_t *counts,
+                                           int block_rows, const uint16_t *w, const uint16_t *pre,
+                                           int E, int N, int K, uint16_t *d_a, void *d_w,
+                                           int d_w_type, void *ws, uint32_t *dev_status,
+                                           cudaStream_t st);
+
+// RMS norm and its gradient (norm.cu).
+size_t rms_norm_backward_ws_bytes(int64_t rows, int H);
+cudaError_t launch_rms_norm(const uint16_t *x, const void *residual, int residual_type,
+                            const void *weight, int weight_type, int64_t rows, int H, float eps,
+                            void *residual_out, uint16_t *y, uint8_t *record, cudaStream_t st);
+cudaError_t launch_rms_norm_backward(const uint16_t *d_y, const void *h, int h_type,
+                                     const void *weight, int weight_type, const void *d_residual,
+                                     int64_t rows, int H, float eps, void *d_h, uint16_t *d_x,
+                                     float *d_weight, void *ws, cudaStream_t st);
+
 }  // namespace moe

@@ -1,0 +1,438 @@
+// norm.cu -- RMS norm with the residual's addition, rows out in bf16 and as MXFP8
+// records, and its gradient.
+//
+//   h = x + residual,   inv = 1 / sqrt(mean(h^2) + eps),   y = h inv w
+//
+// Forward: a row is held in registers between the sum of squares and the output, so
+// every input is read once and every output written once.  The record is the MXFP8
+// form of the row in bf16 (quant.cuh), the bytes that the quantized pack makes of y.
+//
+// Backward, with q = d_y w:
+//   d_h = d_residual + inv (q - h inv^2 mean(q h)),   d_w = sum over rows of d_y h inv
+// sum(h^2) and sum(q h) come out of one pass over the row in registers.  A CTA adds its
+// rows' parts of d_w in registers, writes them to the workspace, and a second kernel
+// sums the CTAs' parts in their order.
+//
+// Both are bound by HBM.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "launch.h"
+#include "quant.cuh"
+#include "trace.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kRowsThreads = 256;       // CTA of one-warp teams
+constexpr int kMaxParts = 640;          // CTAs of the backward pass, and parts of d_w
+
+// A row is shared by a team of WARPS warps, each thread with NV vectors of 8 values:
+// vector i of thread t is columns 8 (t + i * 32 WARPS) on.  Teams of one warp share a
+// CTA of kRowsThreads, larger ones have their own.
+template <int WARPS>
+constexpr int kTeams = WARPS == 1 ? kRowsThreads / 32 : 1;
+template <int WARPS>
+constexpr int kThreads = WARPS == 1 ? kRowsThreads : 32 * WARPS;
+
+__device__ __forceinline__ void unpack8(int4 v, float (&f)[8])
+{
+    const uint32_t u[4] = {(uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        f[2 * i] = __uint_as_float(u[i] << 16);
+        f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ int4 pack8(const float (&f)[8])
+{
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        r[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return make_int4((int)r[0], (int)r[1], (int)r[2], (int)r[3]);
+}
+
+// Eight values at vector `v` of an array of fp32 or bf16, as loaded: two 16-byte words
+// or one.
+template <bool F32>
+struct Raw8 {
+    int4 w[F32 ? 2 : 1];
+    __device__ void load(const void *p, int64_t v)
+    {
+#pragma unroll
+        for (int i = 0; i < (F32 ? 2 : 1); i++) w[i] = ld_stream((const int4 *)p + v * (F32 ? 2 : 1) + i);
+    }
+    __device__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < (F32 ? 2 : 1); i++) w[i] = make_int4(0, 0, 0, 0);
+    }
+    __device__ void values(float (&f)[8]) const
+    {
+        if constexpr (F32) {
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                f[4 * i] = __int_as_float(w[i].x);
+                f[4 * i + 1] = __int_as_float(w[i].y);
+                f[4 * i + 2] = __int_as_float(w[i].z);
+                f[4 * i + 3] = __int_as_float(w[i].w);
+            }
+        } else {
+            unpack8(w[0], f);
+        }
+    }
+};
+template <bool F32>
+__device__ __forceinline__ void store8(void *p, int64_t v, const float (&f)[8])
+{
+    if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            st_stream((int4 *)p + 2 * v + i,
+                      make_int4(__float_as_int(f[4 * i]), __float_as_int(f[4 * i + 1]),
+                                __float_as_int(f[4 * i + 2]), __float_as_int(f[4 * i + 3])));
+    } else {
+        st_stream((int4 *)p + v, pack8(f));
+    }
+}
+
+// Eight weights (read again for every row, from L1).
+__device__ __forceinline__ void load_weight(const void *w, bool f32, int v, float (&f)[8])
+{
+    if (f32) {
+        const float4 a = __ldg((const float4 *)w + 2 * v), b = __ldg((const float4 *)w + 2 * v + 1);
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+        f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    } else {
+        unpack8(__ldg((const int4 *)w + v), f);
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+    return v;
+}
+
+// The team's sums of COUNT values, the same for all of its threads.  `turn` alternates
+// between a CTA's rows, so that one barrier a row is enough.
+template <int WARPS, int COUNT>
+__device__ __forceinline__ void team_sum(float (&v)[COUNT], int turn)
+{
+#pragma unroll
+    for (int c = 0; c < COUNT; c++) v[c] = warp_sum(v[c]);
+    if constexpr (WARPS > 1) {
+        __shared__ float part[2][COUNT][WARPS];
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int c = 0; c < COUNT; c++)
+            if (lane == 0) part[turn][c][threadIdx.x >> 5] = v[c];
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < COUNT; c++) v[c] = warp_sum(lane < WARPS ? part[turn][c][lane] : 0.f);
+    }
+}
+
+struct NormArgs {
+    const int4 *x;
+    const void *residual, *weight;
+    bool weight_f32;
+    int64_t rows;
+    int V;                       // vectors of a row
+    float by_width, eps;         // 1 / H
+    void *residual_out;
+    int4 *y;
+    uint8_t *record;
+};
+
+template <int NV, int WARPS, bool F32>
+__global__ void __launch_bounds__(kThreads<WARPS>) k_rms_norm(const __grid_constant__ NormArgs p)
+{
+    pdl_wait();
+    pdl_trigger();
+    constexpr int kTeam = 32 * WARPS;
+    const int t = threadIdx.x % kTeam;
+    const int64_t step = (int64_t)gridDim.x * kTeams<WARPS>;
+    const int record_bytes = 8 * p.V + p.V / 4;
+    int turn = 0;
+    for (int64_t r = (int64_t)blockIdx.x * kTeams<WARPS> + threadIdx.x / kTeam; r < p.rows; r += step) {
+        int4 x[NV];
+        Raw8<F32> res[NV];
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int v = t + i * kTeam;
+            x[i] = make_int4(0, 0, 0, 0);
+            if (v < p.V) x[i] = ld_stream(p.x + r * p.V + v);
+            res[i].zero();
+            if (p.residual && v < p.V) res[i].load(p.residual, r * p.V + v);
+        }
+        float h[NV][8], sum[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            float add[8];
+            unpack8(x[i], h[i]);
+            res[i].values(add);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                if (p.residual) h[i][j] += add[j];      // (-0 stays -0 without a residual)
+                sum[0] = fmaf(h[i][j], h[i][j], sum[0]);
+            }
+            const int v = t + i * kTeam;
+            if (p.residual_out && v < p.V) store8<F32>(p.residual_out, r * p.V + v, h[i]);
+        }
+        team_sum<WARPS, 1>(sum, turn);
+        turn ^= 1;
+        const float inv = 1.f / sqrtf(fmaf(sum[0], p.by_width, p.eps));
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int v = t + i * kTeam;
+            float w[8] = {};
+            if (v < p.V) load_weight(p.weight, p.weight_f32, v, w);
+#pragma unroll
+            for (int j = 0; j < 8; j++) w[j] *= h[i][j] * inv;
+            const int4 out = pack8(w);
+            if (p.y && v < p.V) st_stream(p.y + r * p.V + v, out);
+            if (p.record) {                             // whole warps: shuffles
+                uint2 code;
+                uint8_t scale;
+                mxfp8_quantize(out, code, scale);
+                uint8_t *to = p.record + r * record_bytes;
+                if (v < p.V) {
+                    if (record_bytes % 8 == 0) {
+                        *(uint2 *)(to + 8 * v) = code;
+                    } else {
+#pragma unroll
+                        for (int b = 0; b < 8; b++)
+                            to[8 * v + b] = (uint8_t)((b < 4 ? code.x : code.y) >> (8 * (b & 3)));
+                    }
+                    if (v % 4 == 0) to[8 * p.V + v / 4] = scale;
+                }
+            }
+        }
+    }
+}
+
+struct NormBackArgs {
+    const int4 *d_y;
+    const void *h, *weight, *d_residual;
+    bool weight_f32;
+    int64_t rows;
+    int V;
+    float by_width, eps;
+    void *d_h;
+    int4 *d_x;
+    float *parts;                // [CTAs][8 V], or null: d_w is not wanted
+};
+
+template <int NV, int WARPS, bool F32>
+__global__ void __launch_bounds__(kThreads<WARPS>) k_rms_norm_backward(const __grid_constant__ NormBackArgs p)
+{
+    pdl_wait();
+    pdl_trigger();
+    constexpr int kTeam = 32 * WARPS;
+    const int t = threadIdx.x % kTeam;
+    const int64_t step = (int64_t)gridDim.x * kTeams<WARPS>;
+    float acc[NV][8] = {};
+    int turn = 0;
+    for (int64_t r = (int64_t)blockIdx.x * kTeams<WARPS> + threadIdx.x / kTeam; r < p.rows; r += step) {
+        int4 d[NV];
+        Raw8<F32> raw[NV], res[NV];
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int v = t + i * kTeam;
+            d[i] = make_int4(0, 0, 0, 0);
+            raw[i].zero();
+            res[i].zero();
+            if (v < p.V) {
+                d[i] = ld_stream(p.d_y + r * p.V + v);
+                raw[i].load(p.h, r * p.V + v);
+                if (p.d_residual) res[i].load(p.d_residual, r * p.V + v);
+            }
+        }
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int v = t + i * kTeam;
+            float h[8], dy[8], w[8] = {};
+            raw[i].values(h);
+            unpack8(d[i], dy);
+            if (v < p.V) load_weight(p.weight, p.weight_f32, v, w);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                sum[0] = fmaf(h[j], h[j], sum[0]);
+                sum[1] = fmaf(dy[j] * w[j], h[j], sum[1]);
+            }
+        }
+        team_sum<WARPS, 2>(sum, turn);
+        turn ^= 1;
+        const float inv = 1.f / sqrtf(fmaf(sum[0], p.by_width, p.eps));
+        const float along = sum[1] * p.by_width * inv;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int v = t + i * kTeam;
+            float h[8], dy[8], w[8] = {}, add[8], out[8];
+            raw[i].values(h);
+            unpack8(d[i], dy);
+            res[i].values(add);
+            if (v < p.V) load_weight(p.weight, p.weight_f32, v, w);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                out[j] = inv * (dy[j] * w[j] - h[j] * inv * along);
+                if (p.d_residual) out[j] += add[j];
+                acc[i][j] = fmaf(dy[j], h[j] * inv, acc[i][j]);
+            }
+            if (v < p.V) {
+                store8<F32>(p.d_h, r * p.V + v, out);
+                if (p.d_x) st_stream(p.d_x + r * p.V + v, pack8(out));
+            }
+        }
+    }
+    if (!p.parts) return;
+    // the CTA's part of d_w: the teams' sums in their order
+    if constexpr (kTeams<WARPS> > 1) {
+        __shared__ float own[kTeams<WARPS>][NV * 32 * 8];
+        const int team = threadIdx.x / kTeam;
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+#pragma unroll
+            for (int j = 0; j < 8; j++) own[team][(i * 8 + j) * 32 + t] = acc[i][j];
+        __syncthreads();
+        for (int at = threadIdx.x; at < NV * 32 * 8; at += kThreads<WARPS>) {
+            float s = 0.f;
+#pragma unroll
+            for (int m = 0; m < kTeams<WARPS>; m++) s += own[m][at];
+            const int v = at % 32 + at / 256 * 32, j = at / 32 % 8;
+            if (v < p.V) p.parts[(int64_t)blockIdx.x * 8 * p.V + 8 * v + j] = s;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int v = t + i * kTeam;
+            if (v < p.V) {
+                float4 *to = (float4 *)(p.parts + (int64_t)blockIdx.x * 8 * p.V) + 2 * v;
+                to[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+                to[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+            }
+        }
+    }
+}
+
+// d_w[c] = the sum of column c over the parts: 32 columns a CTA, its 8 warps take the
+// parts in turn, and their sums are added in order.
+constexpr int kSumThreads = 256;
+__global__ void __launch_bounds__(kSumThreads) k_sum_parts(const float *__restrict__ parts, int count, int H,
+                                                           float *__restrict__ d_w)
+{
+    pdl_wait();
+    pdl_trigger();
+    __shared__ float own[kSumThreads / 32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    float s = 0.f;
+    if (c < H)
+#pragma unroll 8
+        for (int i = warp; i < count; i += kSumThreads / 32) s += __ldcg(parts + (int64_t)i * H + c);
+    own[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < H) {
+        s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSumThreads / 32; w++) s += own[w][lane];
+        d_w[c] = s;
+    }
+}
+
+template <int NV, int WARPS, bool F32>
+cudaError_t norm(const NormArgs &p, cudaStream_t st)
+{
+    const int64_t want = (p.rows + kTeams<WARPS> - 1) / kTeams<WARPS>;
+    const int64_t fit = resident_grid((const void *)k_rms_norm<NV, WARPS, F32>, kThreads<WARPS>, 0);
+    const int64_t grid = fit > 0 && want > fit ? fit : want;
+    cudaError_t err;
+    MOE_TRACED_LAUNCH("k_rms_norm", st,
+        err = launch_pdl(k_rms_norm<NV, WARPS, F32>, dim3((unsigned)grid), dim3(kThreads<WARPS>), 0, st, p));
+    return err;
+}
+
+template <int NV, int WARPS, bool F32>
+cudaError_t norm_backward(const NormBackArgs &p, float *d_w, cudaStream_t st)
+{
+    const int64_t want = (p.rows + kTeams<WARPS> - 1) / kTeams<WARPS>;
+    int64_t fit = resident_grid((const void *)k_rms_norm_backward<NV, WARPS, F32>, kThreads<WARPS>, 0);
+    if (fit <= 0 || fit > kMaxParts) fit = kMaxParts;
+    const int64_t grid = want > fit ? fit : want;
+    cudaError_t err = cudaSuccess;
+    if (grid > 0) {
+        MOE_TRACED_LAUNCH("k_rms_norm_backward", st,
+            err = launch_pdl(k_rms_norm_backward<NV, WARPS, F32>, dim3((unsigned)grid),
+                             dim3(kThreads<WARPS>), 0, st, p));
+        if (err != cudaSuccess) return err;
+    }
+    if (!d_w) return err;
+    const int H = 8 * p.V;
+    MOE_TRACED_LAUNCH("k_sum_parts", st,
+        err = launch_pdl(k_sum_parts, dim3((unsigned)((H + 31) / 32)), dim3(kSumThreads), 0, st,
+                         (const float *)p.parts, (int)grid, H, d_w));
+    return err;
+}
+
+// The smallest team that holds a row of V vectors: CALL(NV, WARPS).
+#define BY_WIDTH(V, CALL)              \
+    if ((V) <= 32) return CALL(1, 1);  \
+    if ((V) <= 64) return CALL(2, 1);  \
+    if ((V) <= 128) return CALL(4, 1); \
+    if ((V) <= 256) return CALL(2, 4); \
+    if ((V) <= 512) return CALL(4, 4); \
+    if ((V) <= 640) return CALL(5, 4); \
+    if ((V) <= 1024) return CALL(4, 8); \
+    if ((V) <= 2048) return CALL(4, 16); \
+    return CALL(4, 32)
+
+}  // namespace
+
+size_t rms_norm_backward_ws_bytes(int64_t rows, int H)
+{
+    const int64_t parts = rows < 1 ? 1 : rows < kMaxParts ? rows : kMaxParts;
+    return ((size_t)parts * H * 4 + 255) / 256 * 256;
+}
+
+cudaError_t launch_rms_norm(const uint16_t *x, const void *residual, int residual_type,
+                            const void *weight, int weight_type, int64_t rows, int H, float eps,
+                            void *residual_out, uint16_t *y, uint8_t *record, cudaStream_t st)
+{
+    if (rows == 0) return cudaSuccess;
+    const NormArgs p{(const int4 *)x, residual, weight, weight_type == MOE_TYPE_F32, rows, H / 8,
+                     (float)(1.0 / H), eps, residual_out, (int4 *)y, record};
+#define CALL(NV, WARPS) norm<NV, WARPS, true>(p, st)
+    if (residual && residual_type == MOE_TYPE_F32) {
+        BY_WIDTH(p.V, CALL);
+    }
+#undef CALL
+#define CALL(NV, WARPS) norm<NV, WARPS, false>(p, st)
+    BY_WIDTH(p.V, CALL);
+#undef CALL
+}
+
+cudaError_t launch_rms_norm_backward(const uint16_t *d_y, const void *h, int h_type,
+                                     const void *weight, int weight_type, const void *d_residual,
+                                     int64_t rows, int H, float eps, void *d_h, uint16_t *d_x,
+                                     float *d_weight, void *ws, cudaStream_t st)
+{
+    const NormBackArgs p{(const int4 *)d_y, h, weight, d_residual, weight_type == MOE_TYPE_F32, rows,
+                         H / 8, (float)(1.0 / H), eps, d_h, (int4 *)d_x,
+                         d_weight ? (float *)ws : nullptr};
+#define CALL(NV, WARPS) norm_backward<NV, WARPS, true>(p, d_weight, st)
+    if (h_type == MOE_TYPE_F32) {
+        BY_WIDTH(p.V, CALL);
+    }
+#undef CALL
+#define CALL(NV, WARPS) norm_backward<NV, WARPS, false>(p, d_weight, st)
+    BY_WIDTH(p.V, CALL);
+#undef CALL
+}
+
+}  // namespace moe

@@ -35,11 +35,18 @@
  *   moe_w4_pack                     4-bit weights into the library's layout, once
  *   moe_expert_product_w4           rows of every expert times its 4-bit weights,
  *                                   plain or silu(gate) * up
+ *   moe_expert_product              the same with bf16 weights
+ *
+ * Between one layer's combine and the next one's router:
+ *   moe_rms_norm                    residual addition and RMS norm, rows out in bf16
+ *                                   and as the records that dispatch moves
  *
  * The training direction of the path, declared after the forward calls:
  *   moe_balance_loss                balance and z loss, per-expert counts
  *   moe_route_backward              gradient of the routing weights and losses
  *   moe_combine_backward            gradient of the weighted combine
+ *   moe_expert_product_backward     gradient of the experts' products
+ *   moe_rms_norm_backward           gradient of the norm
  * (the gradient of dispatch is moe_combine with weights of one).
  *
  *   moe_trace_*                     optional CUDA-event timing of launches
@@ -82,7 +89,7 @@
  *                                           written out of bounds (section 4.3,
  *                                           9.2: the cap)
  *     MOE_STATUS_BIT(MOE_ERR_BAD_EXPERT_ID) an id >= E was skipped
- *     MOE_STATUS_BIT(MOE_ERR_TIMEOUT)       moe_expert_product_w4 only: a wait inside
+ *     MOE_STATUS_BIT(MOE_ERR_TIMEOUT)       the experts' products only: a wait inside
  *                                           the kernel gave up after 5 s and its
  *                                           outputs are not to be used
  *   The library only sets bits; the caller clears the word when it wants.
@@ -120,7 +127,8 @@ typedef enum {
 #define MOE_FORMAT_MXFP8 1
 #define MOE_FORMAT_NVFP4 2
 
-/* Element types of the router logits in the training calls. */
+/* Element types: router logits in the training calls, the residual stream, norm weights,
+ * gradients of expert weights. */
 #define MOE_TYPE_F32 0
 #define MOE_TYPE_BF16 1
 
@@ -765,6 +773,52 @@ moe_status_t moe_expert_product_w4(const uint16_t *a, int a_rows, const int32_t 
                                    uint32_t *dev_status, cudaStream_t stream);
 
 /*
+ * The experts' products with bf16 weights, as they are trained.  For every row r of expert e:
+ *   gated 0:  y[r][n] = bf16_rne( sum_k a[r][k] W_e[n][k] ),              n < N
+ *   gated 1:  y[r][n] = bf16_rne( silu(sum_k a[r][k] W_e[n][k])
+ *                                 * sum_k a[r][k] W_e[N + n][k] )
+ * with silu(v) = v / (1 + exp(-v)), sums in fp32 and one rounding at the end.
+ *   a        [a_rows][K] bf16 in, y [a_rows][N] bf16 out, apart from each other.
+ *   expert_offsets / masked_counts, block_rows  as moe_expert_product_w4.
+ *   w        [E][N][K] bf16, or [E][2N][K] for gated weights: the N gate rows, then the N
+ *            up rows of every expert.
+ *   pre      [a_rows][2N] bf16 out or NULL, gated only: the two sums of every output, rounded
+ *            (gate in the first N columns, up in the others), for the way back.
+ *   ws       moe_expert_product_workspace_bytes(a_rows, E, N, K, gated) bytes, 256-byte aligned.
+ * N and K multiples of 8.  Rows of y and pre outside the experts' rows are not written, and
+ * what `a` holds there reaches nothing.  Row ranges that leave [0, a_rows) are cut to it and
+ * flag MOE_ERR_INVALID_ARG; offsets that fall flag it too, and then what y holds in the runs is
+ * not to be used.  A NaN or infinity in a row of `a` reaches only that row of y.
+ */
+size_t moe_expert_product_workspace_bytes(int a_rows, int E, int N, int K, int gated);
+moe_status_t moe_expert_product(const uint16_t *a, int a_rows, const int32_t *expert_offsets,
+                                const int32_t *masked_counts, int block_rows, const uint16_t *w,
+                                int E, int N, int K, int gated, uint16_t *y, uint16_t *pre, void *ws,
+                                size_t ws_bytes, uint32_t *dev_status, cudaStream_t stream);
+
+/*
+ * RMS norm of rows, after the residual's addition (what stands between moe_combine of one
+ * layer and the router and dispatch of the next):
+ *   h = x + residual,   y = bf16_rne( h / sqrt(mean over the row of h^2 + eps) * weight )
+ * computed in fp32; y is of h before it is rounded to residual_out.
+ *   x            [rows][H] bf16 in.
+ *   residual     [rows][H] of residual_type (MOE_TYPE_F32 or MOE_TYPE_BF16) in, or NULL: h = x.
+ *   residual_out [rows][H] of residual_type out or NULL: h.  May be `residual` itself.
+ *   weight       [H] of weight_type, 16-byte aligned.
+ *   y            [rows][H] bf16 out or NULL.
+ *   record       [rows][H + H/32] uint8 out or NULL, 8-byte aligned, H a multiple of 32: the
+ *                MXFP8 record of y, the bytes that moe_dispatch_pack_mxfp8 makes of it.  Rows
+ *                quantized here once are dispatched as rows of (H + H/32) / 2 bf16 values
+ *                (moe_dispatch, moe_dispatch_pack_permute; H a multiple of 512) instead of
+ *                being quantized on the way.
+ * One of y and record at least.  All arrays apart from each other but for residual_out.
+ * H a multiple of 8, at most 32768; eps > 0.  A row whose mean square leaves fp32 is 0.
+ */
+moe_status_t moe_rms_norm(const uint16_t *x, const void *residual, int residual_type,
+                          const void *weight, int weight_type, int64_t rows, int H, float eps,
+                          void *residual_out, uint16_t *y, uint8_t *record, cudaStream_t stream);
+
+/*
  * Balance loss, z loss and per-expert counts of a router, source by source.
  * A source is what is balanced: S sequences of T tokens balance each sequence
  * by itself, S = 1 the whole batch.  With V_s the valid tokens of source s,
@@ -841,6 +895,58 @@ moe_status_t moe_combine_backward(const uint16_t *d_out, const uint16_t *y, int 
                                   const int32_t *recv_pair, int S, int T, int k, int H,
                                   uint16_t *d_y, float *d_topk_w, uint32_t *dev_status,
                                   cudaStream_t stream);
+
+/*
+ * Gradient of the experts' plain products y = a W_e^T in the rows and in the weights.  For
+ * every expert e and the rows r of its run:
+ *   d_a[r][k]    = bf16_rne( sum_n d_y[r][n] W_e[n][k] )
+ *   d_w[e][n][k] = sum over r of d_y[r][n] a[r][k], rounded once to d_w_type; 0 for an expert
+ *                  without rows
+ * and where `a` was silu(g) * u with pre = [g | u] (moe_expert_product), d_a is their gradient
+ * instead, [a_rows][2K] like pre: with d = sum_n d_y W (in fp32) and s = 1 / (1 + exp(-g))
+ *   d_a[r][k]     = bf16_rne( d u s (1 + g (1 - s)) )
+ *   d_a[r][K + k] = bf16_rne( d g s )
+ * which is the d_y, with N = 2K, of the call for the gate and up weights.
+ *   d_y [a_rows][N], a [a_rows][K] bf16 in; expert_offsets / masked_counts, block_rows, w
+ *   [E][N][K] bf16 as moe_expert_product.
+ *   pre  [a_rows][2K] bf16 in, or NULL.
+ *   d_a  bf16 out, or NULL where it is not wanted (w is not read then).
+ *   d_w  [E][N][K] of d_w_type (MOE_TYPE_F32 or MOE_TYPE_BF16) out, 16-byte aligned, or NULL
+ *        where it is not wanted (a is not read then).
+ *   ws   moe_expert_product_backward_workspace_bytes(a_rows, E, N, K) bytes, 256-byte aligned.
+ * All arrays apart from each other.  Rows outside the experts' rows are not read and rows of
+ * d_a outside them not written; padding rows inside a run count, with what they hold (the
+ * permute calls and moe_combine_backward write zeros there).  Ranges as moe_expert_product.
+ */
+size_t moe_expert_product_backward_workspace_bytes(int a_rows, int E, int N, int K);
+moe_status_t moe_expert_product_backward(const uint16_t *d_y, const uint16_t *a, int a_rows,
+                                         const int32_t *expert_offsets, const int32_t *masked_counts,
+                                         int block_rows, const uint16_t *w, const uint16_t *pre,
+                                         int E, int N, int K, uint16_t *d_a, void *d_w, int d_w_type,
+                                         void *ws, size_t ws_bytes, uint32_t *dev_status,
+                                         cudaStream_t stream);
+
+/*
+ * Gradient of moe_rms_norm in its rows and in the weight.  With h as the norm took it
+ * (residual_out, or x without a residual), inv = 1 / sqrt(mean h^2 + eps), q = d_y weight:
+ *   d_h      = d_residual + inv (q - h inv^2 mean over the row of (q h))
+ *   d_weight = sum over the rows of d_y h inv
+ * d_h is the gradient of x and of residual alike.
+ *   d_y        [rows][H] bf16 in.
+ *   h          [rows][H] of h_type (MOE_TYPE_F32 or MOE_TYPE_BF16) in.
+ *   d_residual [rows][H] of h_type in or NULL: the gradient that reaches residual_out from
+ *              elsewhere.  May be d_h itself.
+ *   d_h        [rows][H] of h_type out; d_x [rows][H] bf16 out or NULL: the same, rounded.
+ *   d_weight   [H] float32 out or NULL; sums in fp32 in a fixed order.
+ *   ws         moe_rms_norm_backward_workspace_bytes(rows, H) bytes, 256-byte aligned, for
+ *              d_weight.
+ * All arrays apart from each other but for d_residual.  Sizes and eps as moe_rms_norm.
+ */
+size_t moe_rms_norm_backward_workspace_bytes(int64_t rows, int H);
+moe_status_t moe_rms_norm_backward(const uint16_t *d_y, const void *h, int h_type, const void *weight,
+                                   int weight_type, const void *d_residual, int64_t rows, int H,
+                                   float eps, void *d_h, uint16_t *d_x, float *d_weight, void *ws,
+                                   size_t ws_bytes, cudaStream_t stream);
 
 /*
  * Per-kernel timing (tracing aid; off by default).  While enabled, every
