@@ -2,15 +2,30 @@
 //
 // Three products over the rows of each expert e (W_e [N][K]):
 //   y[r][n]   = sum_k a[r][k] W_e[n][k]      (gated: silu of one sum times another)
-//   d_a[r][k] = sum_n d_y[r][n] W_e[n][k]    (or the gradient in gate and up)
+//   d_a[r][k] = sum_n d_y[r][n] W_e[n][k]    (or, with gate and up, their gradient)
 //   d_w[n][k] = sum_r d_y[r][n] a[r][k]
-// each a sum over l of X(i, l) Y(j, l): one kernel of 64 x 64 outputs a CTA in turn, both
-// operands staged in shared memory, sums in fp32 registers.
+// by one kernel, tcgen05.mma of CTA pairs: D[256][n] += A[256][64] B[n][64]^T a step.
+// A is of the weights (for d_w: of d_y, across its rows), B of the rows (for d_w: of a): a
+// tile's rows follow the expert's, in steps of 32 up to 256, so that few rows cost few, while
+// the weights, which then are the bound, always fill their side.  Each CTA of a pair
+// loads half of A and of B by TMA, holds 128 rows of D in tensor memory and finishes them.
+// Gated: A has 8 gate rows and the 8 up rows of the same outputs in turn, so that the two
+// factors of an output are eight lanes apart.
+//
+// The work is a list of steps (expert, tile, 64 of the summed index), cut evenly over the
+// pairs, one per two SMs: with few rows every SM streams the same number of weights.  A
+// tile that is cut is summed from its parts, in pair order, by the one that arrives last.
+//
+// A tensor map fills what lies outside the matrix with zeros, so N and K need no padding;
+// rows of B behind an expert's give columns of D that nobody reads.  Only for d_w are rows summed
+// over, and those behind the expert's are cleared in shared memory (they may hold anything).
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "common.cuh"
 #include "gate.cuh"
 #include "launch.h"
+#include "tensor.cuh"
 #include "trace.h"
 #include "w4.cuh"
 
@@ -18,127 +33,756 @@ namespace moe {
 
 namespace {
 
-constexpr int kTile = 64, kStep = 16, kMmThreads = 256;
-
 enum Form { kPlain, kGated, kRowGrad, kGateGrad, kWeightGrad };
 
+constexpr int kStep = 64;                        // of the summed index, 128 bytes
+constexpr int kTileRows = 256;                   // rows of A and D, most rows of B
+constexpr int kStages = 6;
+constexpr int kABytes = 128 * kStep * 2, kBBytes = 128 * kStep * 2, kStageBytes = kABytes + kBBytes;
+constexpr int kFinishWarps = 8;
+constexpr int kWarpLoad = kFinishWarps, kWarpMma = kFinishWarps + 1, kWarpClear = kFinishWarps + 2;
+constexpr int kMmThreads = 32 * (kFinishWarps + 3);
+constexpr int kTmemColumns = 512;                // two tiles of 256 columns of sums
+constexpr int kMinPart = 8;                      // steps worth a part of their own
+constexpr int64_t kPart = (int64_t)kTileRows * 128;   // sums of one part of a tile, in one CTA
+constexpr int kMaxCtas = 160;
+constexpr int kCols = 16;                        // columns of D that a warp finishes at once
+constexpr int kStaging = 4 * kCols * 32;         // bytes of shared memory a warp has for that
+
+struct Shared {
+    uint64_t full[kStages], empty[kStages], landed[kStages];
+    uint64_t sums_full[2], sums_empty[2];
+    int before[kMaxE + 1];           // steps of the experts before e
+    int start[kMaxE], count[kMaxE];
+    uint32_t tmem;
+    int total, parts;                // steps of the call, pairs that share them
+    int base, more;                  // the first `more` pairs have base + 1 steps, the rest base
+    int last;
+    volatile int dead;               // a wait gave up
+};
+constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kFinishWarps * kStaging + sizeof(Shared);
+
+struct Maps {
+    CUtensorMap a, b[3];             // b: boxes of 16, 64 and 128 rows (d_w: the first, of 64)
+};
 struct Args {
-    const __nv_bfloat16 *x, *y;     // the operands: i is a row or an output, j likewise
     const int32_t *offsets, *counts;
     int block_rows, a_rows, E, N, K;
-    __nv_bfloat16 *out;
-    const __nv_bfloat16 *pre;       // in (gradient in gate and up)
-    __nv_bfloat16 *keep;            // out (gated)
+    int rows_a, sums;                // rows of the A side (outputs of a row), length of the sum
+    __nv_bfloat16 *out, *keep;
+    const __nv_bfloat16 *pre;
     void *d_w;
     bool d_w_f32;
+    float *partial;
+    int32_t *arrivals;
     uint32_t *dev_status;
 };
 
-template <int FORM>
-__global__ void __launch_bounds__(kMmThreads) k_expert_product(const __grid_constant__ Args p)
+// Rows of an expert in units of 32, their tiles of at most 8 units, and where tile i starts.
+__device__ __forceinline__ int row_tiles(int count) { return (int)(((unsigned)count + kTileRows - 1) / kTileRows); }
+__device__ __forceinline__ int tile_start(int count, int tiles, int i)
 {
-    pdl_wait();
-    pdl_trigger();
-    __shared__ float xs[kStep][kTile + 1], ys[FORM == kGated ? 2 : 1][kStep][kTile + 1];
-    const int e = blockIdx.y, tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-    int start, count;
-    bool bad = false;
-    expert_rows(p.offsets, p.counts, p.block_rows, p.a_rows, e, start, count, bad);
-    if (p.offsets && p.offsets[e + 1] < p.offsets[e]) bad = true;
-    if (bad && blockIdx.x == 0 && blockIdx.z == 0 && tid == 0) flag_status(p.dev_status, MOE_ERR_INVALID_ARG);
-    // outputs I x J, sums over L; element (i, l) of x at xi * i + xl * l, of y likewise
-    const bool grad = FORM == kRowGrad || FORM == kGateGrad, weights = FORM == kWeightGrad;
-    const int I = weights ? p.N : count, J = weights || grad ? p.K : p.N;
-    const int L = weights ? count : grad ? p.N : p.K;
-    const int64_t xi = weights ? 1 : grad ? p.N : p.K, xl = weights ? p.N : 1;
-    const int64_t yj = weights || grad ? 1 : p.K, yl = weights || grad ? p.K : 1;
-    const __nv_bfloat16 *x = p.x + (int64_t)start * (weights || grad ? p.N : p.K);
-    const __nv_bfloat16 *y = p.y + (weights ? (int64_t)start * p.K
-                                            : (int64_t)e * (FORM == kGated ? 2 : 1) * p.N * p.K);
-    const int j0 = blockIdx.x * kTile;
-    for (int i0 = blockIdx.z * kTile; i0 < I; i0 += gridDim.z * kTile) {
-        float acc[FORM == kGated ? 2 : 1][4][4] = {};
-        for (int l0 = 0; l0 < L; l0 += kStep) {
-            for (int at = tid; at < kTile * kStep; at += kMmThreads) {
-                const int l = weights ? at / kTile : at % kStep, i = weights ? at % kTile : at / kStep;
-                xs[l][i] = i0 + i < I && l0 + l < L ? __bfloat162float(x[(i0 + i) * xi + (l0 + l) * xl]) : 0.f;
-            }
-            for (int at = tid; at < kTile * kStep; at += kMmThreads) {
-                const int l = yj == 1 ? at / kTile : at % kStep, j = yj == 1 ? at % kTile : at / kStep;
-                for (int h = 0; h < (FORM == kGated ? 2 : 1); h++)
-                    ys[h][l][j] = j0 + j < J && l0 + l < L
-                                      ? __bfloat162float(y[((int64_t)h * p.N + j0 + j) * yj + (l0 + l) * yl])
-                                      : 0.f;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int l = 0; l < kStep; l++)
-#pragma unroll
-                for (int u = 0; u < 4; u++)
-#pragma unroll
-                    for (int v = 0; v < 4; v++)
-#pragma unroll
-                        for (int h = 0; h < (FORM == kGated ? 2 : 1); h++)
-                            acc[h][u][v] = fmaf(xs[l][ty + 16 * u], ys[h][l][tx + 16 * v], acc[h][u][v]);
-            __syncthreads();
+    return (int)((int64_t)i * (((unsigned)count + 31) / 32) / tiles) * 32;
+}
+
+struct Shape {
+    int E, tiles;                    // tiles of the A side
+    int steps;                       // of a tile (0: by the expert's rows)
+    int tiles_b;                     // d_w: tiles of the B side
+};
+
+template <int FORM>
+__device__ __forceinline__ Shape shape_of(const Args &p)
+{
+    if (FORM == kWeightGrad)
+        return {p.E, (p.N + kTileRows - 1) / kTileRows, 0, (p.K + kTileRows - 1) / kTileRows};
+    return {p.E, (p.rows_a + kTileRows - 1) / kTileRows, (p.sums + kStep - 1) / kStep, 0};
+}
+// (an expert without rows has one step of zeros, which writes the zeros of its gradient)
+__device__ __forceinline__ int steps_of(const Shape &w, int count)
+{
+    return w.steps ? w.steps : max(1, (int)(((unsigned)count + kStep - 1) / kStep));
+}
+
+// The steps of this pair, one tile after the other; for whole warps.
+struct Segment {
+    int e, tile;                     // expert, tile of the A side
+    int row0, rows, cols;            // d_w: first column, columns in the matrix, columns of the MMA;
+                                     // else first row of the tile, its rows, and those rounded up
+    int c0, c1, steps;               // steps of the segment, of the whole tile
+    int unit;                        // first step of the tile
+};
+
+template <int FORM>
+struct Walk {
+    const Shared &sh;
+    const Args &p;
+    const Shape &w;
+    int at, to;
+    __device__ Walk(const Shared &s, const Args &a, const Shape &shape) : sh(s), p(a), w(shape)
+    {
+        const int b = blockIdx.x / 2;
+        at = b < sh.parts ? b * sh.base + min(b, sh.more) : 0;
+        to = b < sh.parts ? at + sh.base + (b < sh.more) : 0;
+    }
+    // The last e with before[e] <= at: two ballots over at most 32 values each (E <= 1024).
+    // Experts without steps share their `before` with the next one, which is taken.
+    __device__ int expert() const
+    {
+        const int lane = threadIdx.x & 31, step = (w.E + 31) / 32;
+        const unsigned below = __ballot_sync(kFull, lane * step < w.E && sh.before[lane * step] <= at);
+        const int base = (31 - __clz((int)below)) * step;         // before[0] = 0: some bit is set
+        if (step == 1) return base;
+        const unsigned below2 =
+            __ballot_sync(kFull, lane < step && base + lane < w.E && sh.before[base + lane] <= at);
+        return base + 31 - __clz((int)below2);
+    }
+    __device__ bool next(Segment &g)
+    {
+        if (at >= to) return false;
+        g.e = expert();
+        const int count = sh.count[g.e];
+        g.steps = steps_of(w, count);
+        const int local = at - sh.before[g.e], task = local / g.steps;
+        g.c0 = local - task * g.steps;
+        g.c1 = min(g.steps, g.c0 + to - at);
+        g.unit = at - g.c0;
+        at += g.c1 - g.c0;
+        if constexpr (FORM == kWeightGrad) {
+            g.tile = task / w.tiles_b;
+            g.row0 = (task - g.tile * w.tiles_b) * kTileRows;
+            g.rows = min(kTileRows, p.K - g.row0);
+        } else {
+            const int nt = row_tiles(count);
+            g.tile = task / nt;
+            const int i = task - g.tile * nt;
+            g.row0 = tile_start(count, nt, i);
+            g.rows = min(count, tile_start(count, nt, i + 1)) - g.row0;
         }
-        for (int u = 0; u < 4; u++)
-            for (int v = 0; v < 4; v++) {
-                const int i = i0 + ty + 16 * u, j = j0 + tx + 16 * v;
-                if (i >= I || j >= J) continue;
-                const float s = acc[0][u][v];
-                const int64_t r = start + i;
-                if constexpr (FORM == kGated) {
-                    const float up = acc[1][u][v];
-                    p.out[r * J + j] = __float2bfloat16_rn(gated_output(s, up));
-                    if (p.keep) {
-                        p.keep[r * 2 * J + j] = __float2bfloat16_rn(s);
-                        p.keep[r * 2 * J + J + j] = __float2bfloat16_rn(up);
+        g.cols = (g.rows + 31) / 32 * 32;
+        return true;
+    }
+};
+__device__ __forceinline__ int owner_of(const Shared &sh, int unit)
+{
+    const int longer = sh.more * (sh.base + 1);
+    return unit < longer ? unit / (sh.base + 1) : sh.more + (unit - longer) / sh.base;
+}
+
+// By one warp: the experts' rows, and before[e], the steps of those before e.  Runs could only
+// overlap where the offsets fall: from there on no expert has rows.
+template <int FORM>
+__device__ __forceinline__ void scan_experts(Shared &sh, const Args &p, const Shape &w)
+{
+    constexpr int kAhead = 4;            // loads in flight
+    const int lane = threadIdx.x & 31;
+    int before = 0, tasks = 0;
+    bool fell = false, bad = false;
+    for (int e0 = 0; e0 < p.E; e0 += 32 * kAhead) {
+        int start[kAhead], count[kAhead];
+        bool falls[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; i++) {
+            const int e = e0 + 32 * i + lane;
+            start[i] = count[i] = 0;
+            falls[i] = false;
+            if (e < p.E) {
+                expert_rows(p.offsets, p.counts, p.block_rows, p.a_rows, e, start[i], count[i], bad);
+                falls[i] = p.offsets && __ldg(p.offsets + e + 1) < __ldg(p.offsets + e);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; i++) {
+            const int e = e0 + 32 * i + lane;
+            if (e0 + 32 * i >= p.E) break;
+            const unsigned fall = __ballot_sync(kFull, falls[i]);
+            if (fell || (fall & (lanemask_lt() | 1u << lane))) count[i] = 0;
+            fell = fell || fall;
+            const int n = e >= p.E ? 0 : FORM == kWeightGrad ? w.tiles * w.tiles_b : w.tiles * row_tiles(count[i]);
+            const int units = n * steps_of(w, count[i]);
+            const int inc = warp_inclusive_scan(units);
+            if (e < p.E) {
+                sh.start[e] = start[i];
+                sh.count[e] = count[i];
+                sh.before[e] = before + inc - units;
+            }
+            before += __shfl_sync(kFull, inc, 31);
+            tasks += n;
+        }
+    }
+    tasks = __reduce_add_sync(kFull, tasks);
+    if (lane == 0) {
+        sh.before[p.E] = before;
+        // every pair takes part where that leaves it kMinPart steps or a tile
+        const int pairs = gridDim.x / 2;
+        const int parts = min(pairs, max(tasks, before / kMinPart));
+        sh.total = before;
+        sh.parts = parts;
+        sh.base = parts ? before / parts : 0;
+        sh.more = parts ? before - sh.base * parts : 0;
+    }
+    if (bad && blockIdx.x == 0) flag_status(p.dev_status, MOE_ERR_INVALID_ARG);
+    __syncwarp();
+}
+
+__device__ __forceinline__ int arrived(const int32_t *p)
+{
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// ---------------------------------------------------------------- loads
+
+// Rows of B that a CTA loads for `half` rows: by 16 up to 32, else 64 or 128.
+__device__ __forceinline__ int loaded_rows(int half) { return half <= 32 ? half : half <= 64 ? 64 : 128; }
+
+template <int FORM>
+__device__ __forceinline__ void load_steps(Shared &sh, uint8_t *ring, const Args &p, const Maps &maps, const Shape &w)
+{
+    const uint32_t rank = cluster_rank();
+    Walk<FORM> walk(sh, p, w);
+    Segment g;
+    int s = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    while (ok && walk.next(g)) {
+        const int half = g.cols / 2;
+        const int a0 = g.tile * kTileRows + rank * 128;      // first row of A
+        const int start = sh.start[g.e], count = sh.count[g.e];
+        const int b_bytes = FORM == kWeightGrad ? (half > 64 ? 2 : 1) * 8192 : loaded_rows(half) * 128;
+        for (int c = g.c0; c < g.c1; c++) {
+            if (!(ok = mbar_wait_cluster(&sh.empty[s], phase ^ 1, &sh.dead))) break;
+            if (elect_lane()) {
+                uint8_t *at = ring + s * kStageBytes, *bt = at + kABytes;
+                uint32_t bar = cluster_addr(&sh.full[s], 0);
+                if constexpr (FORM == kWeightGrad) {
+                    // the last rows of an expert go to this CTA's warp that clears what is behind
+                    // them, and on to the pair's barrier from there
+                    if (count == 0 || (c == g.steps - 1 && count % kStep != 0)) {
+                        bar = smem_addr(&sh.landed[s]);
+                        mbar_expect(&sh.landed[s], kABytes + b_bytes);
+                    } else {
+                        mbar_expect_at(bar, kABytes + b_bytes);
                     }
-                } else if constexpr (FORM == kGateGrad) {
-                    const float g = __bfloat162float(p.pre[r * 2 * J + j]);
-                    const float up = __bfloat162float(p.pre[r * 2 * J + J + j]);
-                    float d_gate, d_up;
-                    gated_gradient(g, up, s, d_gate, d_up);
-                    p.out[r * 2 * J + j] = __float2bfloat16_rn(d_gate);
-                    p.out[r * 2 * J + J + j] = __float2bfloat16_rn(d_up);
-                } else if constexpr (FORM == kWeightGrad) {
-                    const int64_t at = ((int64_t)e * I + i) * J + j;
-                    if (p.d_w_f32) ((float *)p.d_w)[at] = s;
-                    else ((__nv_bfloat16 *)p.d_w)[at] = __float2bfloat16_rn(s);
+                    const int r = start + c * kStep;
+                    tile_load2(at, &maps.a, a0, r, bar);
+                    tile_load2(at + 8192, &maps.a, a0 + 64, r, bar);
+                    const int b0 = g.row0 + rank * half;
+                    tile_load2(bt, &maps.b[0], b0, r, bar);
+                    if (half > 64) tile_load2(bt + 8192, &maps.b[0], b0 + 64, r, bar);
                 } else {
-                    p.out[r * J + j] = __float2bfloat16_rn(s);
+                    if (rank == 0) mbar_expect(&sh.full[s], 2 * (kABytes + b_bytes));
+                    const int l = c * kStep;
+                    if constexpr (FORM == kPlain) {
+                        tile_load3(at, &maps.a, l, a0, g.e, bar);
+                    } else if constexpr (FORM == kGated) {
+                        tile_load5(at, &maps.a, l, 0, 0, a0 / 16, g.e, bar);
+                    } else {
+                        tile_load3(at, &maps.a, a0, l, g.e, bar);
+                        tile_load3(at + 8192, &maps.a, a0 + 64, l, g.e, bar);
+                    }
+                    const int r = start + g.row0 + rank * half;
+                    if (half <= 32) {
+                        tile_load2(bt, &maps.b[0], l, r, bar);
+                        if (half > 16) tile_load2(bt + 2048, &maps.b[0], l, r + 16, bar);
+                    } else {
+                        tile_load2(bt, half <= 64 ? &maps.b[1] : &maps.b[2], l, r, bar);
+                    }
                 }
+            }
+            __syncwarp();
+            if (++s == kStages) {
+                s = 0;
+                phase ^= 1;
+            }
+        }
+    }
+    // the stages in use come free before the CTA ends: then no copy, MMA or arrival is under way
+    for (int i = 0; ok && i < kStages; i++) {
+        ok = mbar_wait_cluster(&sh.empty[s], phase ^ 1, &sh.dead);
+        if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+    if (!ok) {      // a wait gave up: the copies in flight are given a hundred times what one takes
+        const uint64_t now = global_ns();
+        while (global_ns() - now < 200000) {}
+    }
+}
+
+// The stages of d_w that hold the last rows of an expert: the rows behind them, up to the MMA's
+// next 16, are cleared in both operands.
+__device__ __forceinline__ int valid_rows(const Segment &g, int count, int c) { return min(kStep, count - c * kStep); }
+__device__ __forceinline__ int mma_steps(int valid) { return max(1, (valid + 15) / 16); }
+
+__device__ __forceinline__ void clear_steps(Shared &sh, uint8_t *ring, const Args &p, const Shape &w)
+{
+    const int lane = threadIdx.x & 31;
+    Walk<kWeightGrad> walk(sh, p, w);
+    Segment g;
+    int s = 0;
+    uint32_t phases = 0;
+    bool ok = true;
+    while (ok && walk.next(g)) {
+        const int count = sh.count[g.e];
+        const int ahead = g.c1 - g.c0;
+        if (g.c1 == g.steps && (count % kStep != 0 || count == 0)) {
+            const int last = (s + ahead - 1) % kStages;
+            if (!(ok = mbar_wait_warp(&sh.landed[last], phases >> last & 1, &sh.dead))) break;
+            phases ^= 1u << last;
+            const int valid = valid_rows(g, count, g.c1 - 1), to = 16 * mma_steps(valid);
+            // row r of the operands' four atoms, 128 bytes each
+            uint8_t *stage = ring + last * kStageBytes;
+            for (int i = lane; i < (to - valid) * 32; i += 32) {
+                const int r = valid + (i >> 5), atom = i >> 3 & 3;
+                *(int4 *)(stage + atom * 8192 + r * 128 + (i & 7) * 16) = make_int4(0, 0, 0, 0);
+            }
+            async_proxy_fence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(cluster_addr(&sh.full[last], 0));
+        }
+        s = (s + ahead) % kStages;
+    }
+}
+
+// ---------------------------------------------------------------- MMA
+
+template <int FORM>
+__device__ __forceinline__ void issue_steps(Shared &sh, uint8_t *ring, const Args &p, const Shape &w)
+{
+    constexpr bool kAByK = FORM == kPlain || FORM == kGated, kBByK = FORM != kWeightGrad;
+    Walk<FORM> walk(sh, p, w);
+    Segment g;
+    int s = 0, d = 0;
+    uint32_t phase = 0, sums_phase = 0;
+    bool ok = true;
+    while (ok && walk.next(g)) {
+        const uint32_t word = mma_pair_word(g.cols, kAByK, kBByK);
+        if (!(ok = mbar_wait_cluster(&sh.sums_empty[d], sums_phase ^ 1, &sh.dead))) break;
+        tmem_fence_after();
+        const uint32_t sums = sh.tmem + d * kTileRows;
+        for (int c = g.c0; c < g.c1; c++) {
+            if (!(ok = mbar_wait_cluster(&sh.full[s], phase, &sh.dead))) break;
+            tmem_fence_after();
+            const uint32_t at = smem_addr(ring) + s * kStageBytes, bt = at + kABytes;
+            const uint64_t a = kAByK ? mma_smem_word(at, 1024) : mma_across_word(at, 8192);
+            const uint64_t b = kBByK ? mma_smem_word(bt, 1024) : mma_across_word(bt, 8192);
+            const int n = FORM == kWeightGrad ? mma_steps(valid_rows(g, sh.count[g.e], c)) : 4;
+            if (elect_lane()) {
+#pragma unroll
+                for (int i = 0; i < 4; i++)     // 16 of the sum: 32 bytes along it, 2 KiB across
+                    if (FORM != kWeightGrad || i < n)
+                        mma_bf16_pair(sums, a + (uint64_t)(i * (kAByK ? 2 : 128)),
+                                      b + (uint64_t)(i * (kBByK ? 2 : 128)), word, c > g.c0 || i > 0);
+                mma_commit_pair(&sh.empty[s]);
+                if (c == g.c1 - 1) mma_commit_pair(&sh.sums_full[d]);
+            }
+            __syncwarp();
+            if (++s == kStages) {
+                s = 0;
+                phase ^= 1;
+            }
+        }
+        d ^= 1;
+        if (d == 0) sums_phase ^= 1;
+    }
+}
+
+// ---------------------------------------------------------------- the end of a tile
+
+struct Finish {
+    uint32_t sums;             // the tile's sums in tensor memory, at this warp's lanes
+    const float *from;         // parts of a cut tile: at this thread's row of the first one
+    int parts, here;           // how many, and which of them is in tensor memory only (-1: none)
+};
+
+__device__ __forceinline__ void tile_sums(const Finish &f, int c0, float (&v)[kCols])
+{
+    if (f.parts == 1 || f.here >= 0) tmem_load(f.sums + c0, v);
+    if (f.parts == 1) return;
+    float sum[kCols] = {};
+    for (int q = 0; q < f.parts; q++) {
+        // a part that starts the tile is its pair's last, any other its first
+        const float *part = f.from + (4 * q + (q == 0)) * kPart + c0 * 128;
+#pragma unroll
+        for (int j = 0; j < kCols; j++) sum[j] += q == f.here ? v[j] : __ldcg(part + j * 128);
+    }
+#pragma unroll
+    for (int j = 0; j < kCols; j++) v[j] = sum[j];
+}
+
+__device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+
+// WIDTH outputs of kCols rows from the warp's staging [row][WIDTH] to rows `pitch` values apart,
+// the first `rows` of them and their first `width` outputs.
+template <int WIDTH>
+__device__ __forceinline__ void rows_out(const uint8_t *staging, __nv_bfloat16 *to, int64_t pitch, int rows, int width)
+{
+    constexpr int kPieces = WIDTH / 8;           // of 16 bytes
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < kCols * kPieces / 32; i++) {
+        const int at = i * 32 + lane, row = at / kPieces, piece = at % kPieces;
+        if (row < rows && piece * 8 < width)
+            *(int4 *)(to + row * pitch + piece * 8) = *(const int4 *)(staging + at * 16);
+    }
+}
+
+// Rows c0 .. c0 + 15 of a tile, whose sums for this lane's output are v.  `first`: the tile's
+// first row, n0: the warp's first output.
+template <int FORM>
+__device__ __forceinline__ void finish_rows(const Args &p, uint8_t *staging, const float (&v)[kCols], int64_t first,
+                                            int rows, int n0, const int4 (&gates)[4])
+{
+    const int lane = threadIdx.x & 31;
+    uint16_t *const st = (uint16_t *)staging;
+    __syncwarp();
+    if constexpr (FORM == kGated) {
+        // lanes l and l ^ 8 have gate and up of output n0 + o; each finishes every other row
+        const bool up_lane = lane & 8;
+        const int o = (lane >> 4) * 8 + (lane & 7);
+#pragma unroll
+        for (int j = 0; j < kCols; j += 2) {
+            const float other = __shfl_xor_sync(kFull, up_lane ? v[j] : v[j + 1], 8);
+            const float gate = up_lane ? other : v[j], up = up_lane ? v[j + 1] : other;
+            st[(j + up_lane) * 16 + o] = bf16_bits(gated_output(gate, up));
+        }
+        __syncwarp();
+        rows_out<16>(staging, p.out + first * p.N + n0, p.N, rows, p.N - n0);
+        if (p.keep) {
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < kCols; j++) st[(up_lane * kCols + j) * 16 + o] = bf16_bits(v[j]);
+            __syncwarp();
+            rows_out<16>(staging, p.keep + first * 2 * p.N + n0, 2 * p.N, rows, p.N - n0);
+            rows_out<16>(staging + kCols * 32, p.keep + first * 2 * p.N + p.N + n0, 2 * p.N, rows, p.N - n0);
+        }
+    } else if constexpr (FORM == kGateGrad) {
+        const int K = p.K;
+#pragma unroll
+        for (int i = 0; i < 4; i++) *(int4 *)(staging + (i * 32 + lane) * 16) = gates[i];
+        __syncwarp();
+        uint32_t both[kCols];
+#pragma unroll
+        for (int j = 0; j < kCols; j++) {
+            float d_gate, d_up;
+            gated_gradient(__uint_as_float((uint32_t)st[j * 32 + lane] << 16),
+                           __uint_as_float((uint32_t)st[(kCols + j) * 32 + lane] << 16), v[j], d_gate, d_up);
+            both[j] = bf16_bits(d_gate) | (uint32_t)bf16_bits(d_up) << 16;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kCols; j++) {
+            st[j * 32 + lane] = (uint16_t)both[j];
+            st[(kCols + j) * 32 + lane] = (uint16_t)(both[j] >> 16);
+        }
+        __syncwarp();
+        rows_out<32>(staging, p.out + first * 2 * K + n0, 2 * K, rows, K - n0);
+        rows_out<32>(staging + kCols * 64, p.out + first * 2 * K + K + n0, 2 * K, rows, K - n0);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kCols; j++) st[j * 32 + lane] = bf16_bits(v[j]);
+        __syncwarp();
+        rows_out<32>(staging, p.out + first * p.rows_a + n0, p.rows_a, rows, p.rows_a - n0);
+    }
+}
+
+// Gate and up of 16 rows for the warp's 32 outputs, as they go into the staging.
+__device__ __forceinline__ void load_gates(const Args &p, int64_t first, int rows, int n0, int4 (&gates)[4])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int at = (i & 1) * 32 + lane, row = at / 4, piece = at % 4;
+        gates[i] = make_int4(0, 0, 0, 0);
+        if (row < rows && n0 + piece * 8 < p.K)
+            gates[i] = ld_stream((const int4 *)(p.pre + (first + row) * 2 * p.K + (i >> 1) * p.K + n0 + piece * 8));
+    }
+}
+
+// d_w: 16 columns of this lane's row.
+__device__ __forceinline__ void finish_weights(const Args &p, const float (&v)[kCols], int64_t at, int cols)
+{
+    if (p.d_w_f32) {
+        float *to = (float *)p.d_w + at;
+#pragma unroll
+        for (int j = 0; j < kCols; j += 4)
+            if (j < cols)
+                st_stream((int4 *)(to + j), make_int4(__float_as_int(v[j]), __float_as_int(v[j + 1]),
+                                                      __float_as_int(v[j + 2]), __float_as_int(v[j + 3])));
+    } else {
+        __nv_bfloat16 *to = (__nv_bfloat16 *)p.d_w + at;
+#pragma unroll
+        for (int j = 0; j < kCols; j += 8)
+            if (j < cols) {
+                uint32_t r[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    r[i] = bf16_bits(v[j + 2 * i]) | (uint32_t)bf16_bits(v[j + 2 * i + 1]) << 16;
+                st_stream((int4 *)(to + j), make_int4((int)r[0], (int)r[1], (int)r[2], (int)r[3]));
             }
     }
 }
 
 template <int FORM>
-cudaError_t product(const Args &p, int J, int I, cudaStream_t st)
+__device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const Args &p, const Shape &w)
 {
-    const int deep = (I + kTile - 1) / kTile;
-    const dim3 grid((J + kTile - 1) / kTile, p.E, deep < 1 ? 1 : deep < 64 ? deep : 64);
-    cudaError_t err;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3, half = warp >> 2;
+    const uint32_t rank = cluster_rank();
+    const int row = quarter * 32 + lane;                 // of this CTA's 128 rows of D
+    staging += warp * kStaging;
+    Walk<FORM> walk(sh, p, w);
+    Segment g;
+    int d = 0;
+    uint32_t phase = 0;
+    pdl_wait();                                          // the counters, and what was written to y before
+    while (walk.next(g)) {
+        const int a_row = g.tile * kTileRows + rank * 128 + quarter * 32;    // the warp's first row of A
+        const int64_t first = sh.start[g.e] + g.row0;
+        int from = 0, parts = 1;
+        if (g.c1 - g.c0 < g.steps) {
+            from = owner_of(sh, g.unit);
+            parts = owner_of(sh, g.unit + g.steps - 1) - from + 1;
+        }
+        int4 gates[4];
+        if constexpr (FORM == kGateGrad)
+            load_gates(p, first + half * kCols, g.rows - half * kCols, a_row, gates);
+        const bool ok = mbar_wait_cluster(&sh.sums_full[d], phase, &sh.dead);
+        if (!named_all(1, kFinishWarps * 32, ok)) return;
+        tmem_fence_after();
+        const uint32_t sums = sh.tmem + ((uint32_t)(quarter * 32) << 16) + d * kTileRows;
+        Finish f{sums, p.partial + (int64_t)(4 * from + 2 * rank) * kPart + row, parts, (int)(blockIdx.x / 2) - from};
+        bool finish = true;
+        if (parts > 1) {
+            // the part that is done last adds the others, from memory, to its own
+            int32_t *const count = p.arrivals + 2 * from + rank;
+            finish = named_all(1, kFinishWarps * 32, arrived(count) == parts - 1);
+            if (!finish) {
+                f.here = -1;
+                float *slot = p.partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * kPart + row;
+                for (int c0 = half * kCols; c0 < g.rows; c0 += 2 * kCols) {
+                    float v[kCols];
+                    tmem_load(sums + c0, v);
+#pragma unroll
+                    for (int j = 0; j < kCols; j++) __stcg(slot + (c0 + j) * 128, v[j]);
+                }
+                __threadfence();
+                named_barrier(1, kFinishWarps * 32);
+                if (threadIdx.x == 0) sh.last = atomicAdd(count, 1) == parts - 1;
+                named_barrier(1, kFinishWarps * 32);
+                finish = sh.last;
+                __threadfence();
+            }
+        }
+        if (finish) {
+#pragma unroll 1
+            for (int c0 = half * kCols; c0 < g.rows; c0 += 2 * kCols) {
+                float v[kCols];
+                tile_sums(f, c0, v);
+                if constexpr (FORM == kWeightGrad) {
+                    if (a_row + lane < p.N)
+                        finish_weights(p, v, ((int64_t)g.e * p.N + a_row + lane) * p.K + g.row0 + c0, g.rows - c0);
+                } else {
+                    int4 next[4];
+                    if constexpr (FORM == kGateGrad)
+                        load_gates(p, first + c0 + 2 * kCols, g.rows - c0 - 2 * kCols, a_row, next);
+                    finish_rows<FORM>(p, staging, v, first + c0, g.rows - c0, FORM == kGated ? a_row / 2 : a_row, gates);
+                    if constexpr (FORM == kGateGrad)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) gates[i] = next[i];
+                }
+            }
+        }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(cluster_addr(&sh.sums_empty[d], 0));
+        d ^= 1;
+        if (d == 0) phase ^= 1;
+    }
+}
+
+template <int FORM>
+__global__ void __launch_bounds__(kMmThreads, 1)
+    k_expert_product(const __grid_constant__ Maps maps, const __grid_constant__ Args p)
+{
+    extern __shared__ uint8_t raw[];
+    uint8_t *ring = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
+    uint8_t *staging = ring + kStages * kStageBytes;
+    Shared &sh = *(Shared *)(staging + kFinishWarps * kStaging);
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
+    const Shape shape = shape_of<FORM>(p);
+
+    // The inputs are older than the kernel before, which has passed its own wait when this one
+    // starts; what that one writes is read after pdl_wait.
+    pdl_trigger();
+    if (warp == kWarpLoad) {
+        if (lane == 0) {
+            sh.dead = 0;
+            map_prefetch(&maps.a);
+            map_prefetch(&maps.b[0]);
+        }
+        scan_experts<FORM>(sh, p, shape);
+    } else if (warp == kWarpMma) {
+        if (lane < kStages) {
+            mbar_init(&sh.full[lane], FORM == kWeightGrad ? 2 : 1);
+            mbar_init(&sh.empty[lane], 1);
+            mbar_init(&sh.landed[lane], 1);
+        }
+        if (lane < 2) {
+            mbar_init(&sh.sums_full[lane], 1);
+            mbar_init(&sh.sums_empty[lane], 2 * kFinishWarps);
+        }
+        mbar_init_fence();
+    } else if (warp == kWarpClear) {
+        tmem_alloc_pair(&sh.tmem, kTmemColumns);
+        tmem_fence_before();
+    }
+    __syncthreads();
+    cluster_barrier();
+    tmem_fence_after();
+
+    if (warp == kWarpLoad) {
+        load_steps<FORM>(sh, ring, p, maps, shape);
+    } else if (warp == kWarpMma) {
+        if (cluster_rank() == 0) issue_steps<FORM>(sh, ring, p, shape);
+    } else if (warp == kWarpClear) {
+        if constexpr (FORM == kWeightGrad) clear_steps(sh, ring, p, shape);
+    } else {
+        finish_steps<FORM>(sh, staging, p, shape);
+    }
+    tmem_fence_before();
+    __syncthreads();
+    cluster_barrier();
+    if (warp == kWarpClear) {
+        if (sh.dead && lane == 0) flag_status(p.dev_status, MOE_ERR_TIMEOUT);
+        tmem_fence_after();
+        tmem_free_pair(sh.tmem, kTmemColumns);
+    }
+}
+
+// Clears the arrival counters of cut tiles.
+__global__ void __launch_bounds__(kMaxCtas) k_product_begin(int32_t *arrivals)
+{
+    pdl_wait();
+    pdl_trigger();
+    arrivals[threadIdx.x] = 0;
+}
+
+// ---------------------------------------------------------------- launch
+
+// A tensor map of bf16 values: `dims` sizes, strides in values from the second dimension on.
+struct MapSpec {
+    const void *base;
+    int dims;
+    uint64_t size[5], stride[4];
+    uint32_t box[5];
+};
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+cudaError_t encode_fn(EncodeFn *out)
+{
+    static EncodeFn known = [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult got;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &got) !=
+                cudaSuccess ||
+            got != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return (EncodeFn)fn;
+    }();
+    *out = known;
+    return known ? cudaSuccess : cudaErrorNotSupported;
+}
+
+cudaError_t encode(CUtensorMap *map, const MapSpec &m)
+{
+    EncodeFn fn;
+    const cudaError_t err = encode_fn(&fn);
+    if (err != cudaSuccess) return err;
+    cuuint64_t strides[4];
+    cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+    for (int i = 0; i + 1 < m.dims; i++) strides[i] = m.stride[i] * 2;
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)m.dims, const_cast<void *>(m.base), m.size, strides,
+              m.box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+// [rows][width] in boxes of 64 columns.
+MapSpec rows_map(const void *base, int64_t rows, int64_t width, uint32_t box_rows)
+{
+    return {base, 2, {(uint64_t)width, (uint64_t)rows}, {(uint64_t)width}, {64, box_rows}};
+}
+// [E][N][K] weights in boxes of 64 columns.
+MapSpec weights_map(const void *base, int64_t E, int64_t N, int64_t K, uint32_t box_rows)
+{
+    return {base, 3, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, {(uint64_t)K, (uint64_t)(N * K)}, {64, box_rows, 1}};
+}
+// [E][gate, up][N][K] weights as (K, 8 rows, gate or up, groups of 8 rows, E): a box is 8 groups
+// of 8 gate rows and their 8 up rows.
+MapSpec gated_map(const void *base, int64_t E, int64_t N, int64_t K)
+{
+    return {base,
+            5,
+            {(uint64_t)K, 8, 2, (uint64_t)(N / 8), (uint64_t)E},
+            {(uint64_t)K, (uint64_t)(N * K), (uint64_t)(8 * K), (uint64_t)(2 * N * K)},
+            {64, 8, 2, 8, 1}};
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+constexpr size_t kPartialBytes = (size_t)2 * kMaxCtas * kPart * 4;
+
+template <int FORM>
+cudaError_t product(const Maps &maps, Args p, void *ws, cudaStream_t st)
+{
+    DeviceInfo di;
+    cudaError_t err = device_info(&di);
+    if (err != cudaSuccess) return err;
+    if ((size_t)di.max_smem_optin < kSmem) return cudaErrorInvalidConfiguration;
+    p.partial = (float *)ws;
+    p.arrivals = (int32_t *)((uint8_t *)ws + kPartialBytes);
+    const int ctas = (di.sm_count < kMaxCtas ? di.sm_count : kMaxCtas) / 2 * 2;
+    MOE_TRACED_LAUNCH("k_product_begin", st,
+        err = launch_pdl(k_product_begin, dim3(1), dim3(kMaxCtas), 0, st, p.arrivals));
+    if (err != cudaSuccess) return err;
+    err = cudaFuncSetAttribute(k_expert_product<FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (err != cudaSuccess) return err;
     MOE_TRACED_LAUNCH("k_expert_product", st,
-        err = launch_pdl(k_expert_product<FORM>, grid, dim3(kMmThreads), 0, st, p));
+        err = launch_pdl_cluster(k_expert_product<FORM>, dim3(ctas), dim3(kMmThreads), kSmem, 2, st, maps, p));
+    return err;
+}
+
+// The maps of the rows in boxes of 16, 64 and 128.
+cudaError_t row_boxes(Maps &maps, const void *rows, int64_t a_rows, int64_t width)
+{
+    const uint32_t box[3] = {16, 64, 128};
+    cudaError_t err = cudaSuccess;
+    for (int i = 0; i < 3 && err == cudaSuccess; i++) err = encode(&maps.b[i], rows_map(rows, a_rows, width, box[i]));
     return err;
 }
 
 }  // namespace
 
-size_t expert_product_ws_bytes() { return 256; }
+size_t expert_product_ws_bytes() { return kPartialBytes + align256(kMaxCtas * 4); }
 
 cudaError_t launch_expert_product(const uint16_t *a, int a_rows, const int32_t *offsets,
                                   const int32_t *counts, int block_rows, const uint16_t *w, int E,
                                   int N, int K, bool gated, uint16_t *y, uint16_t *pre, void *ws,
                                   uint32_t *dev_status, cudaStream_t st)
 {
-    (void)ws;
     if (a_rows == 0) return cudaSuccess;
-    const Args p{(const __nv_bfloat16 *)a, (const __nv_bfloat16 *)w, offsets, counts, block_rows,
-                 a_rows, E, N, K, (__nv_bfloat16 *)y, nullptr, (__nv_bfloat16 *)pre, nullptr, false,
-                 dev_status};
-    return gated ? product<kGated>(p, N, a_rows, st) : product<kPlain>(p, N, a_rows, st);
+    Maps maps;
+    cudaError_t err = encode(&maps.a, gated ? gated_map(w, E, N, K) : weights_map(w, E, N, K, 128));
+    if (err == cudaSuccess) err = row_boxes(maps, a, a_rows, K);
+    if (err != cudaSuccess) return err;
+    const Args p{offsets, counts, block_rows, a_rows, E, N, K, gated ? 2 * N : N, K, (__nv_bfloat16 *)y,
+                 (__nv_bfloat16 *)pre, nullptr, nullptr, false, nullptr, nullptr, dev_status};
+    return gated ? product<kGated>(maps, p, ws, st) : product<kPlain>(maps, p, ws, st);
 }
 
 cudaError_t launch_expert_product_backward(const uint16_t *d_y, const uint16_t *a, int a_rows,
@@ -148,15 +792,25 @@ cudaError_t launch_expert_product_backward(const uint16_t *d_y, const uint16_t *
                                            int d_w_type, void *ws, uint32_t *dev_status,
                                            cudaStream_t st)
 {
-    (void)ws;
-    Args p{(const __nv_bfloat16 *)d_y, (const __nv_bfloat16 *)w, offsets, counts, block_rows,
-           a_rows, E, N, K, (__nv_bfloat16 *)d_a, (const __nv_bfloat16 *)pre, nullptr, d_w,
-           d_w_type == MOE_TYPE_F32, dev_status};
+    if (a_rows == 0)        // no rows: the weights' gradient is zero
+        return d_w ? cudaMemsetAsync(d_w, 0, (size_t)E * N * K * (d_w_type == MOE_TYPE_F32 ? 4 : 2), st)
+                   : cudaSuccess;
+    Maps maps;
     cudaError_t err = cudaSuccess;
-    if (d_a && a_rows > 0) err = pre ? product<kGateGrad>(p, K, a_rows, st) : product<kRowGrad>(p, K, a_rows, st);
+    Args p{offsets, counts, block_rows, a_rows, E, N, K, K, N, (__nv_bfloat16 *)d_a, nullptr,
+           (const __nv_bfloat16 *)pre, d_w, d_w_type == MOE_TYPE_F32, nullptr, nullptr, dev_status};
+    if (d_a) {
+        err = encode(&maps.a, weights_map(w, E, N, K, 64));
+        if (err == cudaSuccess) err = row_boxes(maps, d_y, a_rows, N);
+        if (err == cudaSuccess)
+            err = pre ? product<kGateGrad>(maps, p, ws, st) : product<kRowGrad>(maps, p, ws, st);
+    }
     if (err != cudaSuccess || !d_w) return err;
-    p.y = (const __nv_bfloat16 *)a;
-    return product<kWeightGrad>(p, K, N, st);
+    err = encode(&maps.a, rows_map(d_y, a_rows, N, 64));
+    if (err == cudaSuccess) err = encode(&maps.b[0], rows_map(a, a_rows, K, 64));
+    if (err != cudaSuccess) return err;
+    maps.b[1] = maps.b[2] = maps.b[0];
+    return product<kWeightGrad>(maps, p, ws, st);
 }
 
 }  // namespace moe

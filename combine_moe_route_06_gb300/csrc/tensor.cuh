@@ -235,4 +235,136 @@ __device__ __forceinline__ bool named_all(int id, int threads, bool mine)
     return all != 0;
 }
 
+// ---- pairs of CTAs (a cluster of two): the one of rank 0 leads
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// All threads of the cluster.
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address, in the shared memory of the cluster, of the CTA `rank`'s object that here is at `p`.
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_at(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+// mbar_try and mbar_wait_warp for a barrier that the other CTA arrives at too.
+__device__ __forceinline__ bool mbar_try_cluster(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(smem_addr(bar)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *dead)
+{
+    bool ok = mbar_try_cluster(bar, parity);
+    if (!ok) {
+        const uint64_t start = global_ns();
+        while (!ok) {
+            for (int i = 0; i < 64 && !ok; i++) ok = mbar_try_cluster(bar, parity);
+            if (ok || *dead) break;
+            if (global_ns() - start > kWaitLimitNs) *dead = 1;
+        }
+    }
+    return __all_sync(kFull, ok);
+}
+
+// A tile of a tensor map into this CTA's shared memory; the barrier, here or in the other
+// CTA of the pair, counts its bytes.
+__device__ __forceinline__ void tile_load2(void *dst, const void *map, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4}], [%2];" ::"r"(smem_addr(dst)),
+                 "l"(map), "r"(bar), "r"(x), "r"(y)
+                 : "memory");
+}
+__device__ __forceinline__ void tile_load3(void *dst, const void *map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
+                 "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void tile_load5(void *dst, const void *map, int x, int y, int z, int u, int v, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_addr(dst)),
+                 "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v)
+                 : "memory");
+}
+__device__ __forceinline__ void map_prefetch(const void *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+// What this thread wrote to shared memory becomes visible to copies and MMAs.
+__device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Both CTAs of a pair call these.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *out, uint32_t columns)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(out)),
+                 "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t addr, uint32_t columns)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+}
+
+// ---- tcgen05.mma of a pair, bf16 operands in shared memory, fp32 sums:
+// D[256][n] (+)= A[256][16] B[n][16]^T.  Each CTA holds 128 rows of A and D and n / 2 rows of B.
+
+// Instruction word; *_by_k: a row's consecutive values are along k, else consecutive rows are
+// next to each other in memory.
+__host__ __device__ __forceinline__ uint32_t mma_pair_word(int n, bool a_by_k, bool b_by_k)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)!a_by_k << 15) | ((uint32_t)!b_by_k << 16) |
+           ((uint32_t)(n >> 3) << 17) | (16u << 24);
+}
+// Operand along k: 8-row groups 1 KiB apart (mma_smem_word(addr, 1024)).  Operand across k: atoms
+// of 64 rows (128 bytes, 16-byte pieces XOR-ed by k % 8) times any number of k, a k 128 bytes
+// after the other; `atom_bytes` from an atom to the next 64 rows'.
+__device__ __forceinline__ uint64_t mma_across_word(uint32_t addr, uint32_t atom_bytes)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(atom_bytes >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t word, bool add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(word), "r"((uint32_t)add)
+                 : "memory");
+}
+// mma_commit at this barrier's place in both CTAs.
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+                 "[%0], %1;" ::"r"(smem_addr(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
 }  // namespace moe
