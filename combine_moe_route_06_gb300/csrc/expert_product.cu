@@ -12,9 +12,11 @@
 // Gated: A has 8 gate rows and the 8 up rows of the same outputs in turn, so that the two
 // factors of an output are eight lanes apart.
 //
-// The work is a list of steps (expert, tile, 64 of the summed index), cut evenly over the
-// pairs, one per two SMs: with few rows every SM streams the same number of weights.  A
-// tile that is cut is summed from its parts, in pair order, by the one that arrives last.
+// The work is a list of steps (expert, tile, 64 of the summed index).  Where there are many
+// tiles the pairs, one per two SMs, take them in turn; the last one or two per pair, or all of
+// few, are cut evenly over the pairs: with few rows every SM streams the same number of
+// weights.  A tile that is cut is summed from its parts, in pair order, by the one that
+// arrives last.
 //
 // A tensor map fills what lies outside the matrix with zeros, so N and K need no padding;
 // rows of B behind an expert's give columns of D that nobody reads.  Only for d_w are rows summed
@@ -55,7 +57,9 @@ struct Shared {
     int before[kMaxE + 1];           // steps of the experts before e
     int start[kMaxE], count[kMaxE];
     uint32_t tmem;
-    int total, parts;                // steps of the call, pairs that share them
+    int waves;                       // tiles that each pair takes whole, in turn
+    int shared;                      // first step of the rest, which is cut evenly
+    int parts;                       // pairs that share it
     int base, more;                  // the first `more` pairs have base + 1 steps, the rest base
     int last;
     volatile int dead;               // a wait gave up
@@ -118,16 +122,17 @@ struct Walk {
     const Shared &sh;
     const Args &p;
     const Shape &w;
-    int at, to;
+    int wave, at, to;
     __device__ Walk(const Shared &s, const Args &a, const Shape &shape) : sh(s), p(a), w(shape)
     {
         const int b = blockIdx.x / 2;
-        at = b < sh.parts ? b * sh.base + min(b, sh.more) : 0;
-        to = b < sh.parts ? at + sh.base + (b < sh.more) : 0;
+        wave = 0;
+        at = sh.shared + (b < sh.parts ? b * sh.base + min(b, sh.more) : 0);
+        to = at + (b < sh.parts ? sh.base + (b < sh.more) : 0);
     }
     // The last e with before[e] <= at: two ballots over at most 32 values each (E <= 1024).
     // Experts without steps share their `before` with the next one, which is taken.
-    __device__ int expert() const
+    __device__ int expert(int at) const
     {
         const int lane = threadIdx.x & 31, step = (w.E + 31) / 32;
         const unsigned below = __ballot_sync(kFull, lane * step < w.E && sh.before[lane * step] <= at);
@@ -139,15 +144,34 @@ struct Walk {
     }
     __device__ bool next(Segment &g)
     {
-        if (at >= to) return false;
-        g.e = expert();
-        const int count = sh.count[g.e];
-        g.steps = steps_of(w, count);
-        const int local = at - sh.before[g.e], task = local / g.steps;
-        g.c0 = local - task * g.steps;
-        g.c1 = min(g.steps, g.c0 + to - at);
-        g.unit = at - g.c0;
-        at += g.c1 - g.c0;
+        int task, count;
+        if (wave < sh.waves) {
+            task = wave * (int)(gridDim.x / 2) + blockIdx.x / 2;
+            wave++;
+            if constexpr (FORM == kWeightGrad) {
+                g.e = task / (w.tiles * w.tiles_b);
+                task -= g.e * (w.tiles * w.tiles_b);
+            } else {
+                g.e = expert(task * w.steps);
+                task -= sh.before[g.e] / w.steps;
+            }
+            count = sh.count[g.e];
+            g.steps = steps_of(w, count);
+            g.c0 = 0;
+            g.c1 = g.steps;
+            g.unit = 0;
+        } else {
+            if (at >= to) return false;
+            g.e = expert(at);
+            count = sh.count[g.e];
+            g.steps = steps_of(w, count);
+            const int local = at - sh.before[g.e];
+            task = local / g.steps;
+            g.c0 = local - task * g.steps;
+            g.c1 = min(g.steps, g.c0 + to - at);
+            g.unit = at - g.c0;
+            at += g.c1 - g.c0;
+        }
         if constexpr (FORM == kWeightGrad) {
             g.tile = task / w.tiles_b;
             g.row0 = (task - g.tile * w.tiles_b) * kTileRows;
@@ -166,6 +190,7 @@ struct Walk {
 __device__ __forceinline__ int owner_of(const Shared &sh, int unit)
 {
     const int longer = sh.more * (sh.base + 1);
+    unit -= sh.shared;
     return unit < longer ? unit / (sh.base + 1) : sh.more + (unit - longer) / sh.base;
 }
 
@@ -176,7 +201,7 @@ __device__ __forceinline__ void scan_experts(Shared &sh, const Args &p, const Sh
 {
     constexpr int kAhead = 4;            // loads in flight
     const int lane = threadIdx.x & 31;
-    int before = 0, tasks = 0;
+    int before = 0, tasks = 0, longest = 0;
     bool fell = false, bad = false;
     for (int e0 = 0; e0 < p.E; e0 += 32 * kAhead) {
         int start[kAhead], count[kAhead];
@@ -200,6 +225,7 @@ __device__ __forceinline__ void scan_experts(Shared &sh, const Args &p, const Sh
             fell = fell || fall;
             const int n = e >= p.E ? 0 : FORM == kWeightGrad ? w.tiles * w.tiles_b : w.tiles * row_tiles(count[i]);
             const int units = n * steps_of(w, count[i]);
+            longest = max(longest, e < p.E ? steps_of(w, count[i]) : 0);
             const int inc = warp_inclusive_scan(units);
             if (e < p.E) {
                 sh.start[e] = start[i];
@@ -211,15 +237,29 @@ __device__ __forceinline__ void scan_experts(Shared &sh, const Args &p, const Sh
         }
     }
     tasks = __reduce_add_sync(kFull, tasks);
+    longest = __reduce_max_sync(kFull, longest);
+    __syncwarp();
     if (lane == 0) {
         sh.before[p.E] = before;
-        // every pair takes part where that leaves it kMinPart steps or a tile
+        // Whole tiles in turn while that leaves one for every pair to share (not where a few
+        // experts have most of the steps): the pairs then work on neighbouring tiles at the
+        // same time, whose operands come from L2.
         const int pairs = gridDim.x / 2;
-        const int parts = min(pairs, max(tasks, before / kMinPart));
-        sh.total = before;
+        const int waves = tasks >= 2 * pairs && (int64_t)longest * tasks <= 2 * (int64_t)before ? tasks / pairs - 1 : 0;
+        const int task = waves * pairs;                  // the first one of the rest
+        int shared = task * w.steps;
+        if constexpr (FORM == kWeightGrad) {
+            const int per = w.tiles * w.tiles_b, e = task / per;
+            if (waves) shared = sh.before[e] + (task - e * per) * steps_of(w, sh.count[e]);
+        }
+        const int rest = before - shared;
+        // every pair takes part where that leaves it kMinPart steps or a tile
+        const int parts = min(pairs, max(tasks - task, rest / kMinPart));
+        sh.waves = waves;
+        sh.shared = shared;
         sh.parts = parts;
-        sh.base = parts ? before / parts : 0;
-        sh.more = parts ? before - sh.base * parts : 0;
+        sh.base = parts ? rest / parts : 0;
+        sh.more = parts ? rest - sh.base * parts : 0;
     }
     if (bad && blockIdx.x == 0) flag_status(p.dev_status, MOE_ERR_INVALID_ARG);
     __syncwarp();
