@@ -46,18 +46,19 @@ constexpr int kWarpLoad = kFinishWarps, kWarpMma = kFinishWarps + 1, kWarpClear 
 constexpr int kMmThreads = 32 * (kFinishWarps + 3);
 constexpr int kTmemColumns = 512;                // two tiles of 256 columns of sums
 constexpr int kMinPart = 8;                      // steps worth a part of their own
+constexpr int kCutSteps = 40;                    // steps that the parts of cut tiles take to be joined
 constexpr int64_t kPart = (int64_t)kTileRows * 128;   // sums of one part of a tile, in one CTA
 constexpr int kMaxCtas = 160;
 constexpr int kCols = 16;                        // columns of D that a warp finishes at once
 constexpr int kStaging = 4 * kCols * 32;         // bytes of shared memory a warp has for that
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages], landed[kStages];
+    uint64_t full[kStages], empty[kStages], landed[kStages], cleared[kStages];
     uint64_t sums_full[2], sums_empty[2];
     int before[kMaxE + 1];           // steps of the experts before e
     int start[kMaxE], count[kMaxE];
     uint32_t tmem;
-    int waves;                       // tiles that each pair takes whole, in turn
+    int tasks, waves;                // tiles, and how many of them a pair takes whole, in turn
     int shared;                      // first step of the rest, which is cut evenly
     int parts;                       // pairs that share it
     int base, more;                  // the first `more` pairs have base + 1 steps, the rest base
@@ -79,6 +80,7 @@ struct Args {
     bool d_w_f32;
     float *partial;
     int32_t *arrivals;
+    bool late;                       // the kernel before has waited for the inputs, and is not waited for
     uint32_t *dev_status;
 };
 
@@ -148,6 +150,7 @@ struct Walk {
         if (wave < sh.waves) {
             task = wave * (int)(gridDim.x / 2) + blockIdx.x / 2;
             wave++;
+            if (task >= sh.tasks) return false;
             if constexpr (FORM == kWeightGrad) {
                 g.e = task / (w.tiles * w.tiles_b);
                 task -= g.e * (w.tiles * w.tiles_b);
@@ -241,20 +244,24 @@ __device__ __forceinline__ void scan_experts(Shared &sh, const Args &p, const Sh
     __syncwarp();
     if (lane == 0) {
         sh.before[p.E] = before;
-        // Whole tiles in turn while that leaves one for every pair to share (not where a few
-        // experts have most of the steps): the pairs then work on neighbouring tiles at the
-        // same time, whose operands come from L2.
-        const int pairs = gridDim.x / 2;
-        const int waves = tasks >= 2 * pairs && (int64_t)longest * tasks <= 2 * (int64_t)before ? tasks / pairs - 1 : 0;
-        const int task = waves * pairs;                  // the first one of the rest
+        // Whole tiles in turn, so that the pairs work on neighbouring tiles at the same time, whose
+        // operands come from L2.  Cutting the last ones evenly takes kCutSteps, and there is nothing
+        // to gain where the pairs' last tiles wait for less; nor are all tiles taken in turn
+        // where a few experts have most of the steps.
+        const int pairs = gridDim.x / 2, turns = (tasks + pairs - 1) / pairs;
+        const bool whole = ((int64_t)turns * pairs - tasks) * longest <= (int64_t)kCutSteps * pairs;
+        const bool even = (int64_t)longest * tasks <= 2 * (int64_t)before;
+        const int waves = longest <= kCutSteps ? turns : !even ? 0 : whole ? turns : max(0, tasks / pairs - 1);
+        const int task = min(tasks, waves * pairs);      // the first one of the rest
         int shared = task * w.steps;
         if constexpr (FORM == kWeightGrad) {
             const int per = w.tiles * w.tiles_b, e = task / per;
-            if (waves) shared = sh.before[e] + (task - e * per) * steps_of(w, sh.count[e]);
+            shared = task == tasks ? before : sh.before[e] + (task - e * per) * steps_of(w, sh.count[e]);
         }
         const int rest = before - shared;
         // every pair takes part where that leaves it kMinPart steps or a tile
         const int parts = min(pairs, max(tasks - task, rest / kMinPart));
+        sh.tasks = tasks;
         sh.waves = waves;
         sh.shared = shared;
         sh.parts = parts;
@@ -273,6 +280,15 @@ __device__ __forceinline__ int arrived(const int32_t *p)
 }
 
 // ---------------------------------------------------------------- loads
+
+// d_w: rows of the expert in step c, steps of the MMA that they take, and whether rows of
+// others are in the last one.
+__device__ __forceinline__ int valid_rows(int count, int c) { return min(kStep, count - c * kStep); }
+__device__ __forceinline__ int mma_steps(int valid) { return max(1, (valid + 15) / 16); }
+__device__ __forceinline__ bool ragged_step(const Segment &g, int count, int c)
+{
+    return c == g.steps - 1 && (count % kStep != 0 || count == 0);
+}
 
 // Rows of B that a CTA loads for `half` rows: by 16 up to 32, else 64 or 128.
 __device__ __forceinline__ int loaded_rows(int half) { return half <= 32 ? half : half <= 64 ? 64 : 128; }
@@ -297,13 +313,15 @@ __device__ __forceinline__ void load_steps(Shared &sh, uint8_t *ring, const Args
                 uint8_t *at = ring + s * kStageBytes, *bt = at + kABytes;
                 uint32_t bar = cluster_addr(&sh.full[s], 0);
                 if constexpr (FORM == kWeightGrad) {
-                    // the last rows of an expert go to this CTA's warp that clears what is behind
-                    // them, and on to the pair's barrier from there
-                    if (count == 0 || (c == g.steps - 1 && count % kStep != 0)) {
+                    // the last rows of an expert go by this CTA's warp that clears what is behind
+                    // them.  (A barrier of the pair that both CTAs arrive at in every step took
+                    // twice the time: 242 us for 116.)
+                    if (ragged_step(g, count, c)) {
                         bar = smem_addr(&sh.landed[s]);
                         mbar_expect(&sh.landed[s], kABytes + b_bytes);
-                    } else {
-                        mbar_expect_at(bar, kABytes + b_bytes);
+                        if (rank == 0) mbar_arrive(&sh.full[s]);
+                    } else if (rank == 0) {
+                        mbar_expect(&sh.full[s], 2 * (kABytes + b_bytes));
                     }
                     const int r = start + c * kStep;
                     tile_load2(at, &maps.a, a0, r, bar);
@@ -354,9 +372,6 @@ __device__ __forceinline__ void load_steps(Shared &sh, uint8_t *ring, const Args
 
 // The stages of d_w that hold the last rows of an expert: the rows behind them, up to the MMA's
 // next 16, are cleared in both operands.
-__device__ __forceinline__ int valid_rows(const Segment &g, int count, int c) { return min(kStep, count - c * kStep); }
-__device__ __forceinline__ int mma_steps(int valid) { return max(1, (valid + 15) / 16); }
-
 __device__ __forceinline__ void clear_steps(Shared &sh, uint8_t *ring, const Args &p, const Shape &w)
 {
     const int lane = threadIdx.x & 31;
@@ -368,11 +383,11 @@ __device__ __forceinline__ void clear_steps(Shared &sh, uint8_t *ring, const Arg
     while (ok && walk.next(g)) {
         const int count = sh.count[g.e];
         const int ahead = g.c1 - g.c0;
-        if (g.c1 == g.steps && (count % kStep != 0 || count == 0)) {
+        if (ragged_step(g, count, g.c1 - 1)) {
             const int last = (s + ahead - 1) % kStages;
             if (!(ok = mbar_wait_warp(&sh.landed[last], phases >> last & 1, &sh.dead))) break;
             phases ^= 1u << last;
-            const int valid = valid_rows(g, count, g.c1 - 1), to = 16 * mma_steps(valid);
+            const int valid = valid_rows(count, g.c1 - 1), to = 16 * mma_steps(valid);
             // row r of the operands' four atoms, 128 bytes each
             uint8_t *stage = ring + last * kStageBytes;
             for (int i = lane; i < (to - valid) * 32; i += 32) {
@@ -381,7 +396,7 @@ __device__ __forceinline__ void clear_steps(Shared &sh, uint8_t *ring, const Arg
             }
             async_proxy_fence();
             __syncwarp();
-            if (lane == 0) mbar_arrive_at(cluster_addr(&sh.full[last], 0));
+            if (lane == 0) mbar_arrive_at(cluster_addr(&sh.cleared[last], 0));
         }
         s = (s + ahead) % kStages;
     }
@@ -396,7 +411,7 @@ __device__ __forceinline__ void issue_steps(Shared &sh, uint8_t *ring, const Arg
     Walk<FORM> walk(sh, p, w);
     Segment g;
     int s = 0, d = 0;
-    uint32_t phase = 0, sums_phase = 0;
+    uint32_t phase = 0, sums_phase = 0, cleared = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
         const uint32_t word = mma_pair_word(g.cols, kAByK, kBByK);
@@ -405,11 +420,15 @@ __device__ __forceinline__ void issue_steps(Shared &sh, uint8_t *ring, const Arg
         const uint32_t sums = sh.tmem + d * kTileRows;
         for (int c = g.c0; c < g.c1; c++) {
             if (!(ok = mbar_wait_cluster(&sh.full[s], phase, &sh.dead))) break;
+            if (FORM == kWeightGrad && ragged_step(g, sh.count[g.e], c)) {
+                if (!(ok = mbar_wait_cluster(&sh.cleared[s], cleared >> s & 1, &sh.dead))) break;
+                cleared ^= 1u << s;
+            }
             tmem_fence_after();
             const uint32_t at = smem_addr(ring) + s * kStageBytes, bt = at + kABytes;
             const uint64_t a = kAByK ? mma_smem_word(at, 1024) : mma_across_word(at, 8192);
             const uint64_t b = kBByK ? mma_smem_word(bt, 1024) : mma_across_word(bt, 8192);
-            const int n = FORM == kWeightGrad ? mma_steps(valid_rows(g, sh.count[g.e], c)) : 4;
+            const int n = FORM == kWeightGrad ? mma_steps(valid_rows(sh.count[g.e], c)) : 4;
             if (elect_lane()) {
 #pragma unroll
                 for (int i = 0; i < 4; i++)     // 16 of the sum: 32 bytes along it, 2 KiB across
@@ -438,16 +457,41 @@ struct Finish {
     int parts, here;           // how many, and which of them is in tensor memory only (-1: none)
 };
 
-__device__ __forceinline__ void tile_sums(const Finish &f, int c0, float (&v)[kCols])
+// A part's sums: [column / 4][row][column % 4], so that a thread moves 16 bytes at a time.
+__device__ __forceinline__ void store_part(float *part, int c0, const float (&v)[kCols])
+{
+#pragma unroll
+    for (int j = 0; j < kCols; j += 4)
+        __stcg((float4 *)(part + (c0 + j) * 128), make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
+}
+__device__ __forceinline__ void load_part(const Finish &f, int q, int c0, float (&v)[kCols])
+{
+    // a part that starts the tile is its pair's last, any other its first
+    const float *part = f.from + (4 * q + (q == 0)) * kPart;
+#pragma unroll
+    for (int j = 0; j < kCols; j += 4) {
+        const float4 x = __ldcg((const float4 *)(part + (c0 + j) * 128));
+        v[j] = x.x, v[j + 1] = x.y, v[j + 2] = x.z, v[j + 3] = x.w;
+    }
+}
+
+// Columns c0 .. c0 + 15 of the tile, of a cut one over all of its parts in their order;
+// `other` holds part f.here ^ 1 of a tile of two.
+__device__ __forceinline__ void tile_sums(const Finish &f, int c0, const float (&other)[kCols], float (&v)[kCols])
 {
     if (f.parts == 1 || f.here >= 0) tmem_load(f.sums + c0, v);
     if (f.parts == 1) return;
+    if (f.parts == 2 && f.here >= 0) {
+#pragma unroll
+        for (int j = 0; j < kCols; j++) v[j] += other[j];       // (the same in either order)
+        return;
+    }
     float sum[kCols] = {};
     for (int q = 0; q < f.parts; q++) {
-        // a part that starts the tile is its pair's last, any other its first
-        const float *part = f.from + (4 * q + (q == 0)) * kPart + c0 * 128;
+        float x[kCols];
+        if (q != f.here) load_part(f, q, c0, x);
 #pragma unroll
-        for (int j = 0; j < kCols; j++) sum[j] += q == f.here ? v[j] : __ldcg(part + j * 128);
+        for (int j = 0; j < kCols; j++) sum[j] += q == f.here ? v[j] : x[j];
     }
 #pragma unroll
     for (int j = 0; j < kCols; j++) v[j] = sum[j];
@@ -577,7 +621,7 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
     Segment g;
     int d = 0;
     uint32_t phase = 0;
-    pdl_wait();                                          // the counters, and what was written to y before
+    pdl_wait();                                          // (late: the kernel before may use `partial`)
     while (walk.next(g)) {
         const int a_row = g.tile * kTileRows + rank * 128 + quarter * 32;    // the warp's first row of A
         const int64_t first = sh.start[g.e] + g.row0;
@@ -593,7 +637,7 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
         if (!named_all(1, kFinishWarps * 32, ok)) return;
         tmem_fence_after();
         const uint32_t sums = sh.tmem + ((uint32_t)(quarter * 32) << 16) + d * kTileRows;
-        Finish f{sums, p.partial + (int64_t)(4 * from + 2 * rank) * kPart + row, parts, (int)(blockIdx.x / 2) - from};
+        Finish f{sums, p.partial + (int64_t)(4 * from + 2 * rank) * kPart + row * 4, parts, (int)(blockIdx.x / 2) - from};
         bool finish = true;
         if (parts > 1) {
             // the part that is done last adds the others, from memory, to its own
@@ -601,12 +645,11 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
             finish = named_all(1, kFinishWarps * 32, arrived(count) == parts - 1);
             if (!finish) {
                 f.here = -1;
-                float *slot = p.partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * kPart + row;
+                float *slot = p.partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * kPart + row * 4;
                 for (int c0 = half * kCols; c0 < g.rows; c0 += 2 * kCols) {
                     float v[kCols];
                     tmem_load(sums + c0, v);
-#pragma unroll
-                    for (int j = 0; j < kCols; j++) __stcg(slot + (c0 + j) * 128, v[j]);
+                    store_part(slot, c0, v);
                 }
                 __threadfence();
                 named_barrier(1, kFinishWarps * 32);
@@ -617,10 +660,17 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
             }
         }
         if (finish) {
+            // the other part of a tile in two is loaded a block of columns ahead
+            const bool two = f.parts == 2 && f.here >= 0;
+            float other[kCols] = {}, ahead[kCols] = {};
+            if (two) load_part(f, f.here ^ 1, half * kCols, other);
 #pragma unroll 1
             for (int c0 = half * kCols; c0 < g.rows; c0 += 2 * kCols) {
                 float v[kCols];
-                tile_sums(f, c0, v);
+                if (two && c0 + 2 * kCols < g.rows) load_part(f, f.here ^ 1, c0 + 2 * kCols, ahead);
+                tile_sums(f, c0, other, v);
+#pragma unroll
+                for (int j = 0; j < kCols; j++) other[j] = ahead[j];
                 if constexpr (FORM == kWeightGrad) {
                     if (a_row + lane < p.N)
                         finish_weights(p, v, ((int64_t)g.e * p.N + a_row + lane) * p.K + g.row0 + c0, g.rows - c0);
@@ -654,21 +704,18 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
     const Shape shape = shape_of<FORM>(p);
 
-    // The inputs are older than the kernel before, which has passed its own wait when this one
-    // starts; what that one writes is read after pdl_wait.
-    pdl_trigger();
     if (warp == kWarpLoad) {
         if (lane == 0) {
             sh.dead = 0;
             map_prefetch(&maps.a);
             map_prefetch(&maps.b[0]);
         }
-        scan_experts<FORM>(sh, p, shape);
     } else if (warp == kWarpMma) {
         if (lane < kStages) {
-            mbar_init(&sh.full[lane], FORM == kWeightGrad ? 2 : 1);
+            mbar_init(&sh.full[lane], 1);
             mbar_init(&sh.empty[lane], 1);
             mbar_init(&sh.landed[lane], 1);
+            mbar_init(&sh.cleared[lane], 2);
         }
         if (lane < 2) {
             mbar_init(&sh.sums_full[lane], 1);
@@ -679,6 +726,11 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         tmem_alloc_pair(&sh.tmem, kTmemColumns);
         tmem_fence_before();
     }
+    // The kernel after this one starts when all CTAs have passed here, so that it may read what is
+    // older than this one at once.
+    if (!p.late) pdl_wait();
+    pdl_trigger();
+    if (warp == kWarpLoad) scan_experts<FORM>(sh, p, shape);
     __syncthreads();
     cluster_barrier();
     tmem_fence_after();
@@ -703,10 +755,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 }
 
 // Clears the arrival counters of cut tiles.
-__global__ void __launch_bounds__(kMaxCtas) k_product_begin(int32_t *arrivals)
+__global__ void __launch_bounds__(2 * kMaxCtas) k_product_begin(int32_t *arrivals)
 {
-    pdl_wait();
     pdl_trigger();
+    pdl_wait();
     arrivals[threadIdx.x] = 0;
 }
 
@@ -777,25 +829,37 @@ MapSpec gated_map(const void *base, int64_t E, int64_t N, int64_t K)
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 constexpr size_t kPartialBytes = (size_t)2 * kMaxCtas * kPart * 4;
 
+cudaError_t begin(void *ws, cudaStream_t st)
+{
+    cudaError_t err;
+    MOE_TRACED_LAUNCH("k_product_begin", st,
+        err = launch_pdl(k_product_begin, dim3(1), dim3(2 * kMaxCtas), 0, st,
+                         (int32_t *)((uint8_t *)ws + kPartialBytes)));
+    return err;
+}
+
+// `set`: which of the two sets of counters, and whether a product before this one of the same call has
+// waited for the inputs.
 template <int FORM>
-cudaError_t product(const Maps &maps, Args p, void *ws, cudaStream_t st)
+cudaError_t product(const Maps &maps, Args p, void *ws, int set, bool late, cudaStream_t st)
 {
     DeviceInfo di;
     cudaError_t err = device_info(&di);
     if (err != cudaSuccess) return err;
     if ((size_t)di.max_smem_optin < kSmem) return cudaErrorInvalidConfiguration;
     p.partial = (float *)ws;
-    p.arrivals = (int32_t *)((uint8_t *)ws + kPartialBytes);
+    p.arrivals = (int32_t *)((uint8_t *)ws + kPartialBytes) + set * kMaxCtas;
+    p.late = late;
     const int ctas = (di.sm_count < kMaxCtas ? di.sm_count : kMaxCtas) / 2 * 2;
-    MOE_TRACED_LAUNCH("k_product_begin", st,
-        err = launch_pdl(k_product_begin, dim3(1), dim3(kMaxCtas), 0, st, p.arrivals));
-    if (err != cudaSuccess) return err;
     err = cudaFuncSetAttribute(k_expert_product<FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (err != cudaSuccess) return err;
     MOE_TRACED_LAUNCH("k_expert_product", st,
         err = launch_pdl_cluster(k_expert_product<FORM>, dim3(ctas), dim3(kMmThreads), kSmem, 2, st, maps, p));
     return err;
 }
+
+// Whether tiles of a sum of this length may be cut (scan_experts), so that the counters are needed.
+bool may_cut(int sums) { return (sums + kStep - 1) / kStep > kCutSteps; }
 
 // The maps of the rows in boxes of 16, 64 and 128.
 cudaError_t row_boxes(Maps &maps, const void *rows, int64_t a_rows, int64_t width)
@@ -808,7 +872,7 @@ cudaError_t row_boxes(Maps &maps, const void *rows, int64_t a_rows, int64_t widt
 
 }  // namespace
 
-size_t expert_product_ws_bytes() { return kPartialBytes + align256(kMaxCtas * 4); }
+size_t expert_product_ws_bytes() { return kPartialBytes + align256(2 * kMaxCtas * 4); }
 
 cudaError_t launch_expert_product(const uint16_t *a, int a_rows, const int32_t *offsets,
                                   const int32_t *counts, int block_rows, const uint16_t *w, int E,
@@ -821,8 +885,10 @@ cudaError_t launch_expert_product(const uint16_t *a, int a_rows, const int32_t *
     if (err == cudaSuccess) err = row_boxes(maps, a, a_rows, K);
     if (err != cudaSuccess) return err;
     const Args p{offsets, counts, block_rows, a_rows, E, N, K, gated ? 2 * N : N, K, (__nv_bfloat16 *)y,
-                 (__nv_bfloat16 *)pre, nullptr, nullptr, false, nullptr, nullptr, dev_status};
-    return gated ? product<kGated>(maps, p, ws, st) : product<kPlain>(maps, p, ws, st);
+                 (__nv_bfloat16 *)pre, nullptr, nullptr, false, nullptr, nullptr, false, dev_status};
+    if (may_cut(K)) err = begin(ws, st);
+    if (err != cudaSuccess) return err;
+    return gated ? product<kGated>(maps, p, ws, 0, false, st) : product<kPlain>(maps, p, ws, 0, false, st);
 }
 
 cudaError_t launch_expert_product_backward(const uint16_t *d_y, const uint16_t *a, int a_rows,
@@ -838,19 +904,21 @@ cudaError_t launch_expert_product_backward(const uint16_t *d_y, const uint16_t *
     Maps maps;
     cudaError_t err = cudaSuccess;
     Args p{offsets, counts, block_rows, a_rows, E, N, K, K, N, (__nv_bfloat16 *)d_a, nullptr,
-           (const __nv_bfloat16 *)pre, d_w, d_w_type == MOE_TYPE_F32, nullptr, nullptr, dev_status};
+           (const __nv_bfloat16 *)pre, d_w, d_w_type == MOE_TYPE_F32, nullptr, nullptr, false, dev_status};
+    if ((d_a && may_cut(N)) || (d_w && may_cut(a_rows))) err = begin(ws, st);
+    if (err != cudaSuccess) return err;
     if (d_a) {
         err = encode(&maps.a, weights_map(w, E, N, K, 64));
         if (err == cudaSuccess) err = row_boxes(maps, d_y, a_rows, N);
         if (err == cudaSuccess)
-            err = pre ? product<kGateGrad>(maps, p, ws, st) : product<kRowGrad>(maps, p, ws, st);
+            err = pre ? product<kGateGrad>(maps, p, ws, 0, false, st) : product<kRowGrad>(maps, p, ws, 0, false, st);
     }
     if (err != cudaSuccess || !d_w) return err;
     err = encode(&maps.a, rows_map(d_y, a_rows, N, 64));
     if (err == cudaSuccess) err = encode(&maps.b[0], rows_map(a, a_rows, K, 64));
     if (err != cudaSuccess) return err;
     maps.b[1] = maps.b[2] = maps.b[0];
-    return product<kWeightGrad>(maps, p, ws, st);
+    return product<kWeightGrad>(maps, p, ws, 1, d_a != nullptr, st);
 }
 
 }  // namespace moe

@@ -259,11 +259,6 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void mbar_expect_at(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
-}
 // mbar_try and mbar_wait_warp for a barrier that the other CTA arrives at too.
 __device__ __forceinline__ bool mbar_try_cluster(uint64_t *bar, uint32_t parity)
 {
