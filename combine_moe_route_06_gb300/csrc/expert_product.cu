@@ -69,6 +69,7 @@ constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kFinishWarps * k
 
 struct Maps {
     CUtensorMap a, b[3];             // b: boxes of 16, 64 and 128 rows (d_w: the first, of 64)
+    CUtensorMap d;                   // d_w
 };
 struct Args {
     const int32_t *offsets, *counts;
@@ -457,7 +458,8 @@ struct Finish {
     int parts, here;           // how many, and which of them is in tensor memory only (-1: none)
 };
 
-// A part's sums: [column / 4][row][column % 4], so that a thread moves 16 bytes at a time.
+// A part's sums: a block of 16 columns is 4 x 128 threads x 4 values, so that a thread moves
+// 16 bytes at a time.
 __device__ __forceinline__ void store_part(float *part, int c0, const float (&v)[kCols])
 {
 #pragma unroll
@@ -476,12 +478,20 @@ __device__ __forceinline__ void load_part(const Finish &f, int q, int c0, float 
 }
 
 // Columns c0 .. c0 + 15 of the tile, of a cut one over all of its parts in their order;
-// `other` holds part f.here ^ 1 of a tile of two.
+// `other` holds part f.here ^ 1 of a tile of two.  (d_w: 16 columns of the lane's row; else
+// as matrices.)
+template <int FORM>
+__device__ __forceinline__ void load_sums(uint32_t sums, float (&v)[kCols])
+{
+    if constexpr (FORM == kWeightGrad) tmem_load(sums, v);
+    else tmem_load_matrices(sums, v);
+}
+template <int FORM>
 __device__ __forceinline__ void tile_sums(const Finish &f, int c0, const float (&other)[kCols], float (&v)[kCols])
 {
-    if (f.parts == 1 || f.here >= 0) tmem_load(f.sums + c0, v);
+    if (f.parts == 1 || f.here >= 0) load_sums<FORM>(f.sums + c0, v);
     if (f.parts == 1) return;
-    if (f.parts == 2 && f.here >= 0) {
+    if (FORM != kWeightGrad && f.parts == 2 && f.here >= 0) {
 #pragma unroll
         for (int j = 0; j < kCols; j++) v[j] += other[j];       // (the same in either order)
         return;
@@ -497,79 +507,116 @@ __device__ __forceinline__ void tile_sums(const Finish &f, int c0, const float (
     for (int j = 0; j < kCols; j++) v[j] = sum[j];
 }
 
-__device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
-
-// WIDTH outputs of kCols rows from the warp's staging [row][WIDTH] to rows `pitch` values apart,
-// the first `rows` of them and their first `width` outputs.
-template <int WIDTH>
-__device__ __forceinline__ void rows_out(const uint8_t *staging, __nv_bfloat16 *to, int64_t pitch, int rows, int width)
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
 {
-    constexpr int kPieces = WIDTH / 8;           // of 16 bytes
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// The warp's staging: 16 rows of 64 bytes (32: half of them), whose 16-byte pieces are XOR-ed by
+// the row, so that eight rows at one piece, or eight pieces in a row, are on different banks.
+template <int PIECES>
+__device__ __forceinline__ uint8_t *staged(uint8_t *staging, int row, int piece)
+{
+    return staging + row * (16 * PIECES) + ((piece ^ (PIECES == 4 ? row >> 1 & 3 : row >> 2 & 1)) << 4);
+}
+
+// Rows c0 .. c0 + 15 of a tile in staging to rows `pitch` values apart, the first `rows` of them and
+// their first `width` outputs (16 to a row for two pieces, 32 for four).
+template <int PIECES>
+__device__ __forceinline__ void rows_out(uint8_t *staging, __nv_bfloat16 *to, int64_t pitch, int rows, int width)
+{
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < kCols * kPieces / 32; i++) {
-        const int at = i * 32 + lane, row = at / kPieces, piece = at % kPieces;
+    for (int i = 0; i < kCols * PIECES / 32; i++) {
+        const int at = i * 32 + lane, row = at / PIECES, piece = at % PIECES;
         if (row < rows && piece * 8 < width)
-            *(int4 *)(to + row * pitch + piece * 8) = *(const int4 *)(staging + at * 16);
+            *(int4 *)(to + row * pitch + piece * 8) = *(const int4 *)staged<PIECES>(staging, row, piece);
     }
 }
 
-// Rows c0 .. c0 + 15 of a tile, whose sums for this lane's output are v.  `first`: the tile's
-// first row, n0: the warp's first output.
+// Values of two rows and one output each, in 8 x 8 matrices (tmem_load_matrices), into staging:
+// matrix (h, u) of rows 8 g .. 8 g + 7 is its piece PIECE(h, u).
+template <typename Piece>
+__device__ __forceinline__ void stage(uint8_t *staging, const float (&v)[kCols], Piece piece)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int g = 0; g < 2; g++) {
+        uint32_t r[4];
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const int i = 8 * (q >> 1) + 4 * g + 2 * (q & 1);
+            r[q] = bf16_pair(v[i], v[i + 1]);
+        }
+        store_matrices(staged<4>(staging, 8 * g + (lane & 7), piece(lane >> 4, lane >> 3 & 1)), r);
+    }
+}
+
+// Rows c0 .. c0 + 15 of a tile from their sums v.  `first`: the first row, `rows`: how many there
+// are, n0: the warp's first output.
 template <int FORM>
 __device__ __forceinline__ void finish_rows(const Args &p, uint8_t *staging, const float (&v)[kCols], int64_t first,
                                             int rows, int n0, const int4 (&gates)[4])
 {
     const int lane = threadIdx.x & 31;
-    uint16_t *const st = (uint16_t *)staging;
     __syncwarp();
     if constexpr (FORM == kGated) {
-        // lanes l and l ^ 8 have gate and up of output n0 + o; each finishes every other row
-        const bool up_lane = lane & 8;
-        const int o = (lane >> 4) * 8 + (lane & 7);
+        // lanes 16 h + .. of a matrix (h, 0) have the gates of outputs 8 h + .., of (h, 1) their ups
+        uint32_t r[4];
 #pragma unroll
-        for (int j = 0; j < kCols; j += 2) {
-            const float other = __shfl_xor_sync(kFull, up_lane ? v[j] : v[j + 1], 8);
-            const float gate = up_lane ? other : v[j], up = up_lane ? v[j + 1] : other;
-            st[(j + up_lane) * 16 + o] = bf16_bits(gated_output(gate, up));
+        for (int q = 0; q < 4; q++) {
+            const int i = 8 * (q & 1) + 4 * (q >> 1);
+            r[q] = bf16_pair(gated_output(v[i], v[i + 2]), gated_output(v[i + 1], v[i + 3]));
         }
+        store_matrices(staged<2>(staging, 8 * (lane >> 4) + (lane & 7), lane >> 3 & 1), r);
+        if (p.keep) stage(staging + kCols * 32, v, [](int h, int u) { return 2 * u + h; });
         __syncwarp();
-        rows_out<16>(staging, p.out + first * p.N + n0, p.N, rows, p.N - n0);
+        rows_out<2>(staging, p.out + first * p.N + n0, p.N, rows, p.N - n0);
         if (p.keep) {
-            __syncwarp();
+            // pieces 0, 1 of a row are of gate, 2, 3 of up
+            __nv_bfloat16 *const to = p.keep + first * 2 * p.N + n0;
 #pragma unroll
-            for (int j = 0; j < kCols; j++) st[(up_lane * kCols + j) * 16 + o] = bf16_bits(v[j]);
-            __syncwarp();
-            rows_out<16>(staging, p.keep + first * 2 * p.N + n0, 2 * p.N, rows, p.N - n0);
-            rows_out<16>(staging + kCols * 32, p.keep + first * 2 * p.N + p.N + n0, 2 * p.N, rows, p.N - n0);
+            for (int i = 0; i < 2; i++) {
+                const int at = i * 32 + lane, row = at / 4, piece = at % 4;
+                if (row < rows && n0 + (piece & 1) * 8 < p.N)
+                    *(int4 *)(to + (int64_t)row * 2 * p.N + (piece >> 1) * p.N + (piece & 1) * 8) =
+                        *(const int4 *)staged<4>(staging + kCols * 32, row, piece);
+            }
         }
     } else if constexpr (FORM == kGateGrad) {
         const int K = p.K;
 #pragma unroll
-        for (int i = 0; i < 4; i++) *(int4 *)(staging + (i * 32 + lane) * 16) = gates[i];
-        __syncwarp();
-        uint32_t both[kCols];
-#pragma unroll
-        for (int j = 0; j < kCols; j++) {
-            float d_gate, d_up;
-            gated_gradient(__uint_as_float((uint32_t)st[j * 32 + lane] << 16),
-                           __uint_as_float((uint32_t)st[(kCols + j) * 32 + lane] << 16), v[j], d_gate, d_up);
-            both[j] = bf16_bits(d_gate) | (uint32_t)bf16_bits(d_up) << 16;
+        for (int i = 0; i < 4; i++) {
+            const int at = (i & 1) * 32 + lane;
+            *(int4 *)staged<4>(staging + (i >> 1) * kCols * 64, at / 4, at % 4) = gates[i];
         }
         __syncwarp();
+        float d_gate[kCols], d_up[kCols];
 #pragma unroll
-        for (int j = 0; j < kCols; j++) {
-            st[j * 32 + lane] = (uint16_t)both[j];
-            st[(kCols + j) * 32 + lane] = (uint16_t)(both[j] >> 16);
+        for (int g = 0; g < 2; g++) {
+            uint32_t gate[4], up[4];
+            uint8_t *const at = staged<4>(staging, 8 * g + (lane & 7), lane >> 3);
+            load_matrices(at, gate);
+            load_matrices(at + kCols * 64, up);
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const int i = 8 * (q >> 1) + 4 * g + 2 * (q & 1);
+                gated_gradient(__uint_as_float(gate[q] << 16), __uint_as_float(up[q] << 16), v[i], d_gate[i], d_up[i]);
+                gated_gradient(__uint_as_float(gate[q] & 0xffff0000u), __uint_as_float(up[q] & 0xffff0000u), v[i + 1],
+                               d_gate[i + 1], d_up[i + 1]);
+            }
         }
         __syncwarp();
-        rows_out<32>(staging, p.out + first * 2 * K + n0, 2 * K, rows, K - n0);
-        rows_out<32>(staging + kCols * 64, p.out + first * 2 * K + K + n0, 2 * K, rows, K - n0);
+        stage(staging, d_gate, [](int h, int u) { return 2 * h + u; });
+        stage(staging + kCols * 64, d_up, [](int h, int u) { return 2 * h + u; });
+        __syncwarp();
+        rows_out<4>(staging, p.out + first * 2 * K + n0, 2 * K, rows, K - n0);
+        rows_out<4>(staging + kCols * 64, p.out + first * 2 * K + K + n0, 2 * K, rows, K - n0);
     } else {
-#pragma unroll
-        for (int j = 0; j < kCols; j++) st[j * 32 + lane] = bf16_bits(v[j]);
+        stage(staging, v, [](int h, int u) { return 2 * h + u; });
         __syncwarp();
-        rows_out<32>(staging, p.out + first * p.rows_a + n0, p.rows_a, rows, p.rows_a - n0);
+        rows_out<4>(staging, p.out + first * p.rows_a + n0, p.rows_a, rows, p.rows_a - n0);
     }
 }
 
@@ -586,32 +633,37 @@ __device__ __forceinline__ void load_gates(const Args &p, int64_t first, int row
     }
 }
 
-// d_w: 16 columns of this lane's row.
-__device__ __forceinline__ void finish_weights(const Args &p, const float (&v)[kCols], int64_t at, int cols)
+// d_w: COLS columns (64 bytes) of the warp's 32 rows, the first at (e, n0, k0), by one tile store,
+// which writes what is inside the matrix.
+template <int COLS>
+__device__ __forceinline__ void finish_weights(const CUtensorMap *map, uint8_t *staging, const Finish &f, int c0, int e,
+                                               int n0, int k0)
 {
-    if (p.d_w_f32) {
-        float *to = (float *)p.d_w + at;
+    const int lane = threadIdx.x & 31;
+    uint32_t words[16];
+    const float none[kCols] = {};
 #pragma unroll
-        for (int j = 0; j < kCols; j += 4)
-            if (j < cols)
-                st_stream((int4 *)(to + j), make_int4(__float_as_int(v[j]), __float_as_int(v[j + 1]),
-                                                      __float_as_int(v[j + 2]), __float_as_int(v[j + 3])));
-    } else {
-        __nv_bfloat16 *to = (__nv_bfloat16 *)p.d_w + at;
+    for (int i = 0; i < COLS; i += kCols) {
+        float v[kCols];
+        tile_sums<kWeightGrad>(f, c0 + i, none, v);
 #pragma unroll
-        for (int j = 0; j < kCols; j += 8)
-            if (j < cols) {
-                uint32_t r[4];
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    r[i] = bf16_bits(v[j + 2 * i]) | (uint32_t)bf16_bits(v[j + 2 * i + 1]) << 16;
-                st_stream((int4 *)(to + j), make_int4((int)r[0], (int)r[1], (int)r[2], (int)r[3]));
-            }
+        for (int j = 0; j < kCols; j++) {
+            if constexpr (COLS == 16) words[j] = __float_as_uint(v[j]);
+            else if (j % 2 == 0) words[(i + j) / 2] = bf16_pair(v[j], v[j + 1]);
+        }
     }
+    if (lane == 0) tile_stores_read();
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        *(uint4 *)staged<4>(staging, lane, i) = make_uint4(words[4 * i], words[4 * i + 1], words[4 * i + 2], words[4 * i + 3]);
+    async_proxy_fence();
+    __syncwarp();
+    if (lane == 0) tile_store3(map, k0 + c0, n0, e, staging);
 }
 
 template <int FORM>
-__device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const Args &p, const Shape &w)
+__device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const Args &p, const Maps &maps, const Shape &w)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3, half = warp >> 2;
     const uint32_t rank = cluster_rank();
@@ -634,7 +686,7 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
         if constexpr (FORM == kGateGrad)
             load_gates(p, first + half * kCols, g.rows - half * kCols, a_row, gates);
         const bool ok = mbar_wait_cluster(&sh.sums_full[d], phase, &sh.dead);
-        if (!named_all(1, kFinishWarps * 32, ok)) return;
+        if (!named_all(1, kFinishWarps * 32, ok)) break;
         tmem_fence_after();
         const uint32_t sums = sh.tmem + ((uint32_t)(quarter * 32) << 16) + d * kTileRows;
         Finish f{sums, p.partial + (int64_t)(4 * from + 2 * rank) * kPart + row * 4, parts, (int)(blockIdx.x / 2) - from};
@@ -646,9 +698,9 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
             if (!finish) {
                 f.here = -1;
                 float *slot = p.partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * kPart + row * 4;
-                for (int c0 = half * kCols; c0 < g.rows; c0 += 2 * kCols) {
+                for (int c0 = half * kCols; c0 < g.cols; c0 += 2 * kCols) {
                     float v[kCols];
-                    tmem_load(sums + c0, v);
+                    load_sums<FORM>(sums + c0, v);
                     store_part(slot, c0, v);
                 }
                 __threadfence();
@@ -660,21 +712,29 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
             }
         }
         if (finish) {
-            // the other part of a tile in two is loaded a block of columns ahead
-            const bool two = f.parts == 2 && f.here >= 0;
-            float other[kCols] = {}, ahead[kCols] = {};
-            if (two) load_part(f, f.here ^ 1, half * kCols, other);
+            if constexpr (FORM == kWeightGrad) {
+                if (a_row < p.N) {
 #pragma unroll 1
-            for (int c0 = half * kCols; c0 < g.rows; c0 += 2 * kCols) {
-                float v[kCols];
-                if (two && c0 + 2 * kCols < g.rows) load_part(f, f.here ^ 1, c0 + 2 * kCols, ahead);
-                tile_sums(f, c0, other, v);
+                    for (int c0 = half * 32; c0 < g.rows; c0 += 64)
+                        if (p.d_w_f32) {
+                            finish_weights<16>(&maps.d, staging, f, c0, g.e, a_row, g.row0);
+                            if (c0 + 16 < g.rows) finish_weights<16>(&maps.d, staging, f, c0 + 16, g.e, a_row, g.row0);
+                        } else {
+                            finish_weights<32>(&maps.d, staging, f, c0, g.e, a_row, g.row0);
+                        }
+                }
+            } else {
+                // the other part of a tile in two is loaded a block of columns ahead
+                const bool two = f.parts == 2 && f.here >= 0;
+                float other[kCols] = {}, ahead[kCols] = {};
+                if (two) load_part(f, f.here ^ 1, half * kCols, other);
+#pragma unroll 1
+                for (int c0 = half * kCols; c0 < g.rows; c0 += 2 * kCols) {
+                    float v[kCols];
+                    if (two && c0 + 2 * kCols < g.rows) load_part(f, f.here ^ 1, c0 + 2 * kCols, ahead);
+                    tile_sums<FORM>(f, c0, other, v);
 #pragma unroll
-                for (int j = 0; j < kCols; j++) other[j] = ahead[j];
-                if constexpr (FORM == kWeightGrad) {
-                    if (a_row + lane < p.N)
-                        finish_weights(p, v, ((int64_t)g.e * p.N + a_row + lane) * p.K + g.row0 + c0, g.rows - c0);
-                } else {
+                    for (int j = 0; j < kCols; j++) other[j] = ahead[j];
                     int4 next[4];
                     if constexpr (FORM == kGateGrad)
                         load_gates(p, first + c0 + 2 * kCols, g.rows - c0 - 2 * kCols, a_row, next);
@@ -691,6 +751,7 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
         d ^= 1;
         if (d == 0) phase ^= 1;
     }
+    if (FORM == kWeightGrad && lane == 0) tile_stores_done();
 }
 
 template <int FORM>
@@ -742,7 +803,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     } else if (warp == kWarpClear) {
         if constexpr (FORM == kWeightGrad) clear_steps(sh, ring, p, shape);
     } else {
-        finish_steps<FORM>(sh, staging, p, shape);
+        finish_steps<FORM>(sh, staging, p, maps, shape);
     }
     tmem_fence_before();
     __syncthreads();
@@ -764,12 +825,13 @@ __global__ void __launch_bounds__(2 * kMaxCtas) k_product_begin(int32_t *arrival
 
 // ---------------------------------------------------------------- launch
 
-// A tensor map of bf16 values: `dims` sizes, strides in values from the second dimension on.
+// A tensor map of bf16 or fp32 values: `dims` sizes, strides in values from the second dimension on.
 struct MapSpec {
     const void *base;
     int dims;
     uint64_t size[5], stride[4];
     uint32_t box[5];
+    bool f32 = false;
 };
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -797,10 +859,12 @@ cudaError_t encode(CUtensorMap *map, const MapSpec &m)
     if (err != cudaSuccess) return err;
     cuuint64_t strides[4];
     cuuint32_t ones[5] = {1, 1, 1, 1, 1};
-    for (int i = 0; i + 1 < m.dims; i++) strides[i] = m.stride[i] * 2;
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)m.dims, const_cast<void *>(m.base), m.size, strides,
-              m.box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+    for (int i = 0; i + 1 < m.dims; i++) strides[i] = m.stride[i] * (m.f32 ? 4 : 2);
+    const bool bytes64 = m.box[0] * (m.f32 ? 4 : 2) == 64;
+    return fn(map, m.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)m.dims,
+              const_cast<void *>(m.base), m.size, strides, m.box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              bytes64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess
                : cudaErrorInvalidValue;
 }
@@ -880,7 +944,7 @@ cudaError_t launch_expert_product(const uint16_t *a, int a_rows, const int32_t *
                                   uint32_t *dev_status, cudaStream_t st)
 {
     if (a_rows == 0) return cudaSuccess;
-    Maps maps;
+    Maps maps = {};
     cudaError_t err = encode(&maps.a, gated ? gated_map(w, E, N, K) : weights_map(w, E, N, K, 128));
     if (err == cudaSuccess) err = row_boxes(maps, a, a_rows, K);
     if (err != cudaSuccess) return err;
@@ -901,7 +965,7 @@ cudaError_t launch_expert_product_backward(const uint16_t *d_y, const uint16_t *
     if (a_rows == 0)        // no rows: the weights' gradient is zero
         return d_w ? cudaMemsetAsync(d_w, 0, (size_t)E * N * K * (d_w_type == MOE_TYPE_F32 ? 4 : 2), st)
                    : cudaSuccess;
-    Maps maps;
+    Maps maps = {};
     cudaError_t err = cudaSuccess;
     Args p{offsets, counts, block_rows, a_rows, E, N, K, K, N, (__nv_bfloat16 *)d_a, nullptr,
            (const __nv_bfloat16 *)pre, d_w, d_w_type == MOE_TYPE_F32, nullptr, nullptr, false, dev_status};
@@ -918,6 +982,11 @@ cudaError_t launch_expert_product_backward(const uint16_t *d_y, const uint16_t *
     if (err == cudaSuccess) err = encode(&maps.b[0], rows_map(a, a_rows, K, 64));
     if (err != cudaSuccess) return err;
     maps.b[1] = maps.b[2] = maps.b[0];
+    MapSpec d = weights_map(d_w, E, N, K, 32);          // boxes of 64 bytes
+    d.f32 = p.d_w_f32;
+    d.box[0] = p.d_w_f32 ? 16 : 32;
+    err = encode(&maps.d, d);
+    if (err != cudaSuccess) return err;
     return product<kWeightGrad>(maps, p, ws, 1, d_a != nullptr, st);
 }
 

@@ -235,6 +235,39 @@ __device__ __forceinline__ bool named_all(int id, int threads, bool mine)
     return all != 0;
 }
 
+// 16 columns of the warp's 32 lanes, as 8 x 8 matrices: v[8 h + 4 g + 2 u + i] is of lane
+// 16 h + 8 u + l / 4 and column 8 g + 2 (l % 4) + i, for lane l of the warp.
+__device__ __forceinline__ void tmem_load_matrices(uint32_t addr, float (&v)[16])
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr), "r"(addr + (16u << 16))
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
+}
+// Four 8 x 8 matrices of 16-bit values between registers (lane l: row l / 4, columns 2 (l % 4) and
+// the next) and shared memory, where they are transposed: lane l gives the address of column l % 8
+// of matrix l / 8, 16 bytes.
+__device__ __forceinline__ void store_matrices(void *at, const uint32_t (&r)[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem_addr(at)),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+__device__ __forceinline__ void load_matrices(const void *at, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_addr(at))
+                 : "memory");
+}
+
 // ---- pairs of CTAs (a cluster of two): the one of rank 0 leads
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -308,6 +341,17 @@ __device__ __forceinline__ void tile_load5(void *dst, const void *map, int x, in
                  "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v)
                  : "memory");
 }
+// A tile of this CTA's shared memory to a tensor map's place, as one group of this thread; and the
+// wait until its groups have been read.
+__device__ __forceinline__ void tile_store3(const void *map, int x, int y, int z, const void *src)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];\n\t"
+                 "cp.async.bulk.commit_group;" ::"l"(map),
+                 "r"(smem_addr(src)), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void tile_stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tile_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void map_prefetch(const void *map)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
