@@ -4,14 +4,19 @@
 //   h = x + residual,   inv = 1 / sqrt(mean(h^2) + eps),   y = h inv w
 //
 // Forward: a row is held in registers between the sum of squares and the output, so
-// every input is read once and every output written once.  The record is the MXFP8
-// form of the row in bf16 (quant.cuh), the bytes that the quantized pack makes of y.
+// every input is read once and every output written once.  A team of warps has one row, and the
+// next CTA the next ones (16,384 rows of 2,048 with an fp32 residual: 59.5 us, 6.8 TB/s; 69.7 by
+// CTAs that stay and go on to further rows, whose loads then wait for the row before).  The
+// record is the MXFP8 form of the row in bf16 (quant.cuh), the bytes that the quantized pack
+// makes of y (4,096 rows of 5,120 with both outputs: 31 us, 6.1 TB/s).
 //
 // Backward, with q = d_y w:
 //   d_h = d_residual + inv (q - h inv^2 mean(q h)),   d_w = sum over rows of d_y h inv
 // sum(h^2) and sum(q h) come out of one pass over the row in registers.  A CTA adds its
 // rows' parts of d_w in registers, writes them to the workspace, and a second kernel
 // sums the CTAs' parts in their order.
+//
+// (16,384 rows of 5,120 with a residual's gradient: 116 us, 5.8 TB/s.)
 //
 // Both are bound by HBM.
 #include <cuda_bf16.h>
@@ -157,10 +162,9 @@ __global__ void __launch_bounds__(kThreads<WARPS>) k_rms_norm(const __grid_const
     pdl_trigger();
     constexpr int kTeam = 32 * WARPS;
     const int t = threadIdx.x % kTeam;
-    const int64_t step = (int64_t)gridDim.x * kTeams<WARPS>;
     const int record_bytes = 8 * p.V + p.V / 4;
-    int turn = 0;
-    for (int64_t r = (int64_t)blockIdx.x * kTeams<WARPS> + threadIdx.x / kTeam; r < p.rows; r += step) {
+    const int64_t r = (int64_t)blockIdx.x * kTeams<WARPS> + threadIdx.x / kTeam;
+    if (r < p.rows) {
         int4 x[NV];
         Raw8<F32> res[NV];
 #pragma unroll
@@ -185,8 +189,7 @@ __global__ void __launch_bounds__(kThreads<WARPS>) k_rms_norm(const __grid_const
             const int v = t + i * kTeam;
             if (p.residual_out && v < p.V) store8<F32>(p.residual_out, r * p.V + v, h[i]);
         }
-        team_sum<WARPS, 1>(sum, turn);
-        turn ^= 1;
+        team_sum<WARPS, 1>(sum, 0);
         const float inv = 1.f / sqrtf(fmaf(sum[0], p.by_width, p.eps));
 #pragma unroll
         for (int i = 0; i < NV; i++) {
@@ -229,19 +232,69 @@ struct NormBackArgs {
     float *parts;                // [CTAs][8 V], or null: d_w is not wanted
 };
 
-template <int NV, int WARPS, bool F32>
+// The vectors of a row that a thread works on come through shared memory, `AHEAD` rows of
+// them: copies of the next rows are under way while a row is summed and written (a thread reads
+// what it has copied itself, so its own wait is enough).  AHEAD 0: rows too wide for that,
+// straight into registers.
+template <int NV, bool F32>
+constexpr int kRowSlots = NV * (F32 ? 5 : 3);          // 16 bytes of d_y, h and d_residual each
+template <int NV, int WARPS, bool F32, int AHEAD>
+constexpr size_t kRingBytes = (size_t)AHEAD * kRowSlots<NV, F32> * kThreads<WARPS> * 16;
+
+__device__ __forceinline__ void copy_ahead(int4 *to, const int4 *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
+                 : "memory");
+}
+
+template <int NV, int WARPS, bool F32, int AHEAD>
 __global__ void __launch_bounds__(kThreads<WARPS>) k_rms_norm_backward(const __grid_constant__ NormBackArgs p)
 {
+    extern __shared__ int4 ring[];
     pdl_wait();
     pdl_trigger();
-    constexpr int kTeam = 32 * WARPS;
+    constexpr int kTeam = 32 * WARPS, kWords = F32 ? 2 : 1, kSlots = kRowSlots<NV, F32>;
     const int t = threadIdx.x % kTeam;
     const int64_t step = (int64_t)gridDim.x * kTeams<WARPS>;
+    int64_t r = (int64_t)blockIdx.x * kTeams<WARPS> + threadIdx.x / kTeam;
+    auto slot = [&](int stage, int s) { return ring + (stage * kSlots + s) * kThreads<WARPS> + threadIdx.x; };
+    auto fetch = [&](int stage, int64_t row) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int v = t + i * kTeam;
+            if (row < p.rows && v < p.V) {
+                copy_ahead(slot(stage, i), p.d_y + row * p.V + v);
+#pragma unroll
+                for (int q = 0; q < kWords; q++) {
+                    copy_ahead(slot(stage, NV + kWords * i + q), (const int4 *)p.h + (row * p.V + v) * kWords + q);
+                    if (p.d_residual)
+                        copy_ahead(slot(stage, NV + kWords * (NV + i) + q),
+                                   (const int4 *)p.d_residual + (row * p.V + v) * kWords + q);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if constexpr (AHEAD > 0)
+#pragma unroll
+        for (int i = 0; i < AHEAD - 1; i++) fetch(i, r + i * step);
+    constexpr bool kHold = NV <= 2;                    // weights stay in registers
+    float weight[kHold ? NV : 1][8] = {};
+    if constexpr (kHold)
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            if (t + i * kTeam < p.V) load_weight(p.weight, p.weight_f32, t + i * kTeam, weight[i]);
     float acc[NV][8] = {};
-    int turn = 0;
-    for (int64_t r = (int64_t)blockIdx.x * kTeams<WARPS> + threadIdx.x / kTeam; r < p.rows; r += step) {
+    int turn = 0, stage = 0;
+    for (; r < p.rows; r += step) {
+        float h[NV][8], dy[NV][8], sum[2] = {0.f, 0.f};
+        Raw8<F32> res[NV];
+        if constexpr (AHEAD > 0) {
+            fetch(stage == 0 ? AHEAD - 1 : stage - 1, r + (AHEAD - 1) * step);
+            asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD > 0 ? AHEAD - 1 : 0) : "memory");
+        }
         int4 d[NV];
-        Raw8<F32> raw[NV], res[NV];
+        Raw8<F32> raw[NV];
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int v = t + i * kTeam;
@@ -249,23 +302,28 @@ __global__ void __launch_bounds__(kThreads<WARPS>) k_rms_norm_backward(const __g
             raw[i].zero();
             res[i].zero();
             if (v < p.V) {
-                d[i] = ld_stream(p.d_y + r * p.V + v);
-                raw[i].load(p.h, r * p.V + v);
-                if (p.d_residual) res[i].load(p.d_residual, r * p.V + v);
+                if constexpr (AHEAD > 0) {
+                    d[i] = *slot(stage, i);
+#pragma unroll
+                    for (int q = 0; q < kWords; q++) raw[i].w[q] = *slot(stage, NV + kWords * i + q);
+                } else {
+                    d[i] = ld_stream(p.d_y + r * p.V + v);
+                    raw[i].load(p.h, r * p.V + v);
+                    if (p.d_residual) res[i].load(p.d_residual, r * p.V + v);
+                }
             }
         }
-        float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int v = t + i * kTeam;
-            float h[8], dy[8], w[8] = {};
-            raw[i].values(h);
-            unpack8(d[i], dy);
-            if (v < p.V) load_weight(p.weight, p.weight_f32, v, w);
+            float w[8] = {};
+            raw[i].values(h[i]);
+            unpack8(d[i], dy[i]);
+            if (!kHold && v < p.V) load_weight(p.weight, p.weight_f32, v, w);
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                sum[0] = fmaf(h[j], h[j], sum[0]);
-                sum[1] = fmaf(dy[j] * w[j], h[j], sum[1]);
+                sum[0] = fmaf(h[i][j], h[i][j], sum[0]);
+                sum[1] = fmaf(dy[i][j] * (kHold ? weight[i % (kHold ? NV : 1)][j] : w[j]), h[i][j], sum[1]);
             }
         }
         team_sum<WARPS, 2>(sum, turn);
@@ -275,22 +333,25 @@ __global__ void __launch_bounds__(kThreads<WARPS>) k_rms_norm_backward(const __g
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int v = t + i * kTeam;
-            float h[8], dy[8], w[8] = {}, add[8], out[8];
-            raw[i].values(h);
-            unpack8(d[i], dy);
+            float w[8] = {}, add[8], out[8];
+            if (AHEAD > 0 && v < p.V && p.d_residual)
+#pragma unroll
+                for (int q = 0; q < kWords; q++) res[i].w[q] = *slot(stage, NV + kWords * (NV + i) + q);
             res[i].values(add);
-            if (v < p.V) load_weight(p.weight, p.weight_f32, v, w);
+            if (!kHold && v < p.V) load_weight(p.weight, p.weight_f32, v, w);
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                out[j] = inv * (dy[j] * w[j] - h[j] * inv * along);
+                const float unit = h[i][j] * inv;
+                out[j] = inv * (dy[i][j] * (kHold ? weight[i % (kHold ? NV : 1)][j] : w[j]) - unit * along);
                 if (p.d_residual) out[j] += add[j];
-                acc[i][j] = fmaf(dy[j], h[j] * inv, acc[i][j]);
+                acc[i][j] = fmaf(dy[i][j], unit, acc[i][j]);
             }
             if (v < p.V) {
                 store8<F32>(p.d_h, r * p.V + v, out);
                 if (p.d_x) st_stream(p.d_x + r * p.V + v, pack8(out));
             }
         }
+        if (AHEAD > 0) stage = stage == AHEAD - 1 ? 0 : stage + 1;
     }
     if (!p.parts) return;
     // the CTA's part of d_w: the teams' sums in their order
@@ -349,9 +410,7 @@ __global__ void __launch_bounds__(kSumThreads) k_sum_parts(const float *__restri
 template <int NV, int WARPS, bool F32>
 cudaError_t norm(const NormArgs &p, cudaStream_t st)
 {
-    const int64_t want = (p.rows + kTeams<WARPS> - 1) / kTeams<WARPS>;
-    const int64_t fit = resident_grid((const void *)k_rms_norm<NV, WARPS, F32>, kThreads<WARPS>, 0);
-    const int64_t grid = fit > 0 && want > fit ? fit : want;
+    const int64_t grid = (p.rows + kTeams<WARPS> - 1) / kTeams<WARPS>;
     cudaError_t err;
     MOE_TRACED_LAUNCH("k_rms_norm", st,
         err = launch_pdl(k_rms_norm<NV, WARPS, F32>, dim3((unsigned)grid), dim3(kThreads<WARPS>), 0, st, p));
@@ -361,15 +420,20 @@ cudaError_t norm(const NormArgs &p, cudaStream_t st)
 template <int NV, int WARPS, bool F32>
 cudaError_t norm_backward(const NormBackArgs &p, float *d_w, cudaStream_t st)
 {
+    // three rows in the ring where two CTAs of them fit an SM, else two (116 us; 130 with two rows,
+    // 182 straight into registers)
+    constexpr int kAhead = kRingBytes<NV, WARPS, F32, 3> <= 110 * 1024 ? 3 : kRingBytes<NV, WARPS, F32, 2> <= 110 * 1024 ? 2 : 0;
+    constexpr size_t kSmem = kRingBytes<NV, WARPS, F32, kAhead>;
+    const auto kernel = k_rms_norm_backward<NV, WARPS, F32, kAhead>;
     const int64_t want = (p.rows + kTeams<WARPS> - 1) / kTeams<WARPS>;
-    int64_t fit = resident_grid((const void *)k_rms_norm_backward<NV, WARPS, F32>, kThreads<WARPS>, 0);
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (err != cudaSuccess) return err;
+    int64_t fit = resident_grid((const void *)kernel, kThreads<WARPS>, kSmem);
     if (fit <= 0 || fit > kMaxParts) fit = kMaxParts;
     const int64_t grid = want > fit ? fit : want;
-    cudaError_t err = cudaSuccess;
     if (grid > 0) {
         MOE_TRACED_LAUNCH("k_rms_norm_backward", st,
-            err = launch_pdl(k_rms_norm_backward<NV, WARPS, F32>, dim3((unsigned)grid),
-                             dim3(kThreads<WARPS>), 0, st, p));
+            err = launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads<WARPS>), kSmem, st, p));
         if (err != cudaSuccess) return err;
     }
     if (!d_w) return err;
@@ -380,7 +444,7 @@ cudaError_t norm_backward(const NormBackArgs &p, float *d_w, cudaStream_t st)
     return err;
 }
 
-// The smallest team that holds a row of V vectors: CALL(NV, WARPS).
+// The team for a row of V vectors: CALL(NV, WARPS).
 #define BY_WIDTH(V, CALL)              \
     if ((V) <= 32) return CALL(1, 1);  \
     if ((V) <= 64) return CALL(2, 1);  \
@@ -389,6 +453,18 @@ cudaError_t norm_backward(const NormBackArgs &p, float *d_w, cudaStream_t st)
     if ((V) <= 512) return CALL(4, 4); \
     if ((V) <= 640) return CALL(5, 4); \
     if ((V) <= 1024) return CALL(4, 8); \
+    if ((V) <= 2048) return CALL(4, 16); \
+    return CALL(4, 32)
+// Backward: two vectors a thread where that holds the row, which leaves registers for twenty or
+// more warps an SM (16,384 rows of 5,120: 116 us with ten warps and two vectors, 187 with four and five).
+#define BY_WIDTH_BACK(V, CALL)          \
+    if ((V) <= 32) return CALL(1, 1);   \
+    if ((V) <= 64) return CALL(2, 1);   \
+    if ((V) <= 128) return CALL(1, 4);  \
+    if ((V) <= 256) return CALL(2, 4);  \
+    if ((V) <= 512) return CALL(2, 8);  \
+    if ((V) <= 640) return CALL(2, 10); \
+    if ((V) <= 1024) return CALL(2, 16); \
     if ((V) <= 2048) return CALL(4, 16); \
     return CALL(4, 32)
 
@@ -427,11 +503,11 @@ cudaError_t launch_rms_norm_backward(const uint16_t *d_y, const void *h, int h_t
                          d_weight ? (float *)ws : nullptr};
 #define CALL(NV, WARPS) norm_backward<NV, WARPS, true>(p, d_weight, st)
     if (h_type == MOE_TYPE_F32) {
-        BY_WIDTH(p.V, CALL);
+        BY_WIDTH_BACK(p.V, CALL);
     }
 #undef CALL
 #define CALL(NV, WARPS) norm_backward<NV, WARPS, false>(p, d_weight, st)
-    BY_WIDTH(p.V, CALL);
+    BY_WIDTH_BACK(p.V, CALL);
 #undef CALL
 }
 
