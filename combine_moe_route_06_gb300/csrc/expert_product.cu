@@ -50,6 +50,7 @@ constexpr int kCutSteps = 40;                    // steps that the parts of cut 
 constexpr int64_t kPart = (int64_t)kTileRows * 128;   // sums of one part of a tile, in one CTA
 constexpr int kMaxCtas = 160;
 constexpr int kCols = 16;                        // columns of D that a warp finishes at once
+constexpr int kGroups = kFinishWarps / 4;        // warps that share the columns of 32 rows of D
 constexpr int kStaging = 4 * kCols * 32;         // bytes of shared memory a warp has for that
 
 struct Shared {
@@ -82,6 +83,7 @@ struct Args {
     float *partial;
     int32_t *arrivals;
     bool late;                       // the kernel before has waited for the inputs, and is not waited for
+    int first_pair, pairs;           // the pairs that share the work
     uint32_t *dev_status;
 };
 
@@ -128,7 +130,7 @@ struct Walk {
     int wave, at, to;
     __device__ Walk(const Shared &s, const Args &a, const Shape &shape) : sh(s), p(a), w(shape)
     {
-        const int b = blockIdx.x / 2;
+        const int b = blockIdx.x / 2 - p.first_pair;
         wave = 0;
         at = sh.shared + (b < sh.parts ? b * sh.base + min(b, sh.more) : 0);
         to = at + (b < sh.parts ? sh.base + (b < sh.more) : 0);
@@ -149,7 +151,7 @@ struct Walk {
     {
         int task, count;
         if (wave < sh.waves) {
-            task = wave * (int)(gridDim.x / 2) + blockIdx.x / 2;
+            task = wave * p.pairs + blockIdx.x / 2 - p.first_pair;
             wave++;
             if (task >= sh.tasks) return false;
             if constexpr (FORM == kWeightGrad) {
@@ -249,7 +251,7 @@ __device__ __forceinline__ void scan_experts(Shared &sh, const Args &p, const Sh
         // operands come from L2.  Cutting the last ones evenly takes kCutSteps, and there is nothing
         // to gain where the pairs' last tiles wait for less; nor are all tiles taken in turn
         // where a few experts have most of the steps.
-        const int pairs = gridDim.x / 2, turns = (tasks + pairs - 1) / pairs;
+        const int pairs = p.pairs, turns = (tasks + pairs - 1) / pairs;
         const bool whole = ((int64_t)turns * pairs - tasks) * longest <= (int64_t)kCutSteps * pairs;
         const bool even = (int64_t)longest * tasks <= 2 * (int64_t)before;
         const int waves = longest <= kCutSteps ? turns : !even ? 0 : whole ? turns : max(0, tasks / pairs - 1);
@@ -269,7 +271,7 @@ __device__ __forceinline__ void scan_experts(Shared &sh, const Args &p, const Sh
         sh.base = parts ? rest / parts : 0;
         sh.more = parts ? rest - sh.base * parts : 0;
     }
-    if (bad && blockIdx.x == 0) flag_status(p.dev_status, MOE_ERR_INVALID_ARG);
+    if (bad && blockIdx.x == 2 * p.first_pair) flag_status(p.dev_status, MOE_ERR_INVALID_ARG);
     __syncwarp();
 }
 
@@ -665,7 +667,7 @@ __device__ __forceinline__ void finish_weights(const CUtensorMap *map, uint8_t *
 template <int FORM>
 __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const Args &p, const Maps &maps, const Shape &w)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3, half = warp >> 2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3, group = warp >> 2;
     const uint32_t rank = cluster_rank();
     const int row = quarter * 32 + lane;                 // of this CTA's 128 rows of D
     staging += warp * kStaging;
@@ -684,7 +686,7 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
         }
         int4 gates[4];
         if constexpr (FORM == kGateGrad)
-            load_gates(p, first + half * kCols, g.rows - half * kCols, a_row, gates);
+            load_gates(p, first + group * kCols, g.rows - group * kCols, a_row, gates);
         const bool ok = mbar_wait_cluster(&sh.sums_full[d], phase, &sh.dead);
         if (!named_all(1, kFinishWarps * 32, ok)) break;
         tmem_fence_after();
@@ -698,7 +700,7 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
             if (!finish) {
                 f.here = -1;
                 float *slot = p.partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * kPart + row * 4;
-                for (int c0 = half * kCols; c0 < g.cols; c0 += 2 * kCols) {
+                for (int c0 = group * kCols; c0 < g.cols; c0 += kGroups * kCols) {
                     float v[kCols];
                     load_sums<FORM>(sums + c0, v);
                     store_part(slot, c0, v);
@@ -715,7 +717,7 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
             if constexpr (FORM == kWeightGrad) {
                 if (a_row < p.N) {
 #pragma unroll 1
-                    for (int c0 = half * 32; c0 < g.rows; c0 += 64)
+                    for (int c0 = group * 32; c0 < g.rows; c0 += kGroups * 32)
                         if (p.d_w_f32) {
                             finish_weights<16>(&maps.d, staging, f, c0, g.e, a_row, g.row0);
                             if (c0 + 16 < g.rows) finish_weights<16>(&maps.d, staging, f, c0 + 16, g.e, a_row, g.row0);
@@ -727,17 +729,17 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
                 // the other part of a tile in two is loaded a block of columns ahead
                 const bool two = f.parts == 2 && f.here >= 0;
                 float other[kCols] = {}, ahead[kCols] = {};
-                if (two) load_part(f, f.here ^ 1, half * kCols, other);
+                if (two) load_part(f, f.here ^ 1, group * kCols, other);
 #pragma unroll 1
-                for (int c0 = half * kCols; c0 < g.rows; c0 += 2 * kCols) {
+                for (int c0 = group * kCols; c0 < g.rows; c0 += kGroups * kCols) {
                     float v[kCols];
-                    if (two && c0 + 2 * kCols < g.rows) load_part(f, f.here ^ 1, c0 + 2 * kCols, ahead);
+                    if (two && c0 + kGroups * kCols < g.rows) load_part(f, f.here ^ 1, c0 + kGroups * kCols, ahead);
                     tile_sums<FORM>(f, c0, other, v);
 #pragma unroll
                     for (int j = 0; j < kCols; j++) other[j] = ahead[j];
                     int4 next[4];
                     if constexpr (FORM == kGateGrad)
-                        load_gates(p, first + c0 + 2 * kCols, g.rows - c0 - 2 * kCols, a_row, next);
+                        load_gates(p, first + c0 + kGroups * kCols, g.rows - c0 - kGroups * kCols, a_row, next);
                     finish_rows<FORM>(p, staging, v, first + c0, g.rows - c0, FORM == kGated ? a_row / 2 : a_row, gates);
                     if constexpr (FORM == kGateGrad)
 #pragma unroll
@@ -755,10 +757,8 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
 }
 
 template <int FORM>
-__global__ void __launch_bounds__(kMmThreads, 1)
-    k_expert_product(const __grid_constant__ Maps maps, const __grid_constant__ Args p)
+__device__ __forceinline__ void run_product(uint8_t *raw, const Maps &maps, const Args &p)
 {
-    extern __shared__ uint8_t raw[];
     uint8_t *ring = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
     uint8_t *staging = ring + kStages * kStageBytes;
     Shared &sh = *(Shared *)(staging + kFinishWarps * kStaging);
@@ -813,6 +813,26 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         tmem_fence_after();
         tmem_free_pair(sh.tmem, kTmemColumns);
     }
+}
+
+template <int FORM>
+__global__ void __launch_bounds__(kMmThreads, 1)
+    k_expert_product(const __grid_constant__ Maps maps, const __grid_constant__ Args p)
+{
+    extern __shared__ uint8_t raw[];
+    run_product<FORM>(raw, maps, p);
+}
+
+// Both gradients in one launch, where together they have no more tiles than there are pairs: pairs
+// with tiles of their own each (five experts' 300 rows of 328 x 648: 18 us in two launches).
+template <int FORM>
+__global__ void __launch_bounds__(kMmThreads, 1)
+    k_expert_gradients(const __grid_constant__ Maps maps, const __grid_constant__ Args p,
+                       const __grid_constant__ Maps maps_w, const __grid_constant__ Args p_w)
+{
+    extern __shared__ uint8_t raw[];
+    if ((int)blockIdx.x / 2 < p.pairs) run_product<FORM>(raw, maps, p);
+    else run_product<kWeightGrad>(raw, maps_w, p_w);
 }
 
 // Clears the arrival counters of cut tiles.
@@ -902,23 +922,47 @@ cudaError_t begin(void *ws, cudaStream_t st)
     return err;
 }
 
+// CTAs of a launch: one per SM, in pairs.
+cudaError_t grid_of(int *ctas)
+{
+    DeviceInfo di;
+    const cudaError_t err = device_info(&di);
+    if (err != cudaSuccess) return err;
+    if ((size_t)di.max_smem_optin < kSmem) return cudaErrorInvalidConfiguration;
+    *ctas = (di.sm_count < kMaxCtas ? di.sm_count : kMaxCtas) / 2 * 2;
+    return cudaSuccess;
+}
+
 // `set`: which of the two sets of counters, and whether a product before this one of the same call has
 // waited for the inputs.
 template <int FORM>
 cudaError_t product(const Maps &maps, Args p, void *ws, int set, bool late, cudaStream_t st)
 {
-    DeviceInfo di;
-    cudaError_t err = device_info(&di);
+    int ctas;
+    cudaError_t err = grid_of(&ctas);
     if (err != cudaSuccess) return err;
-    if ((size_t)di.max_smem_optin < kSmem) return cudaErrorInvalidConfiguration;
     p.partial = (float *)ws;
     p.arrivals = (int32_t *)((uint8_t *)ws + kPartialBytes) + set * kMaxCtas;
     p.late = late;
-    const int ctas = (di.sm_count < kMaxCtas ? di.sm_count : kMaxCtas) / 2 * 2;
+    p.pairs = ctas / 2;
     err = cudaFuncSetAttribute(k_expert_product<FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (err != cudaSuccess) return err;
     MOE_TRACED_LAUNCH("k_expert_product", st,
         err = launch_pdl_cluster(k_expert_product<FORM>, dim3(ctas), dim3(kMmThreads), kSmem, 2, st, maps, p));
+    return err;
+}
+
+// The rows' gradient on the first `pairs` pairs, the weights' on the others; no tile is cut.
+template <int FORM>
+cudaError_t gradients(const Maps &maps, Args p, const Maps &maps_w, Args p_w, int pairs, int ctas, cudaStream_t st)
+{
+    p.pairs = p_w.first_pair = pairs;
+    p_w.pairs = ctas / 2 - pairs;
+    cudaError_t err =
+        cudaFuncSetAttribute(k_expert_gradients<FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (err != cudaSuccess) return err;
+    MOE_TRACED_LAUNCH("k_expert_gradients", st,
+        err = launch_pdl_cluster(k_expert_gradients<FORM>, dim3(ctas), dim3(kMmThreads), kSmem, 2, st, maps, p, maps_w, p_w));
     return err;
 }
 
@@ -949,7 +993,7 @@ cudaError_t launch_expert_product(const uint16_t *a, int a_rows, const int32_t *
     if (err == cudaSuccess) err = row_boxes(maps, a, a_rows, K);
     if (err != cudaSuccess) return err;
     const Args p{offsets, counts, block_rows, a_rows, E, N, K, gated ? 2 * N : N, K, (__nv_bfloat16 *)y,
-                 (__nv_bfloat16 *)pre, nullptr, nullptr, false, nullptr, nullptr, false, dev_status};
+                 (__nv_bfloat16 *)pre, nullptr, nullptr, false, nullptr, nullptr, false, 0, 0, dev_status};
     if (may_cut(K)) err = begin(ws, st);
     if (err != cudaSuccess) return err;
     return gated ? product<kGated>(maps, p, ws, 0, false, st) : product<kPlain>(maps, p, ws, 0, false, st);
@@ -965,29 +1009,40 @@ cudaError_t launch_expert_product_backward(const uint16_t *d_y, const uint16_t *
     if (a_rows == 0)        // no rows: the weights' gradient is zero
         return d_w ? cudaMemsetAsync(d_w, 0, (size_t)E * N * K * (d_w_type == MOE_TYPE_F32 ? 4 : 2), st)
                    : cudaSuccess;
-    Maps maps = {};
+    const Args p{offsets, counts, block_rows, a_rows, E, N, K, K, N, (__nv_bfloat16 *)d_a, nullptr,
+                 (const __nv_bfloat16 *)pre, d_w, d_w_type == MOE_TYPE_F32, nullptr, nullptr, false, 0, 0,
+                 dev_status};
+    Maps maps = {}, maps_w = {};
     cudaError_t err = cudaSuccess;
-    Args p{offsets, counts, block_rows, a_rows, E, N, K, K, N, (__nv_bfloat16 *)d_a, nullptr,
-           (const __nv_bfloat16 *)pre, d_w, d_w_type == MOE_TYPE_F32, nullptr, nullptr, false, dev_status};
-    if ((d_a && may_cut(N)) || (d_w && may_cut(a_rows))) err = begin(ws, st);
-    if (err != cudaSuccess) return err;
     if (d_a) {
         err = encode(&maps.a, weights_map(w, E, N, K, 64));
         if (err == cudaSuccess) err = row_boxes(maps, d_y, a_rows, N);
-        if (err == cudaSuccess)
-            err = pre ? product<kGateGrad>(maps, p, ws, 0, false, st) : product<kRowGrad>(maps, p, ws, 0, false, st);
     }
-    if (err != cudaSuccess || !d_w) return err;
-    err = encode(&maps.a, rows_map(d_y, a_rows, N, 64));
-    if (err == cudaSuccess) err = encode(&maps.b[0], rows_map(a, a_rows, K, 64));
+    if (err == cudaSuccess && d_w) {
+        err = encode(&maps_w.a, rows_map(d_y, a_rows, N, 64));
+        if (err == cudaSuccess) err = encode(&maps_w.b[0], rows_map(a, a_rows, K, 64));
+        MapSpec d = weights_map(d_w, E, N, K, 32);          // boxes of 64 bytes
+        d.f32 = p.d_w_f32;
+        d.box[0] = p.d_w_f32 ? 16 : 32;
+        if (err == cudaSuccess) err = encode(&maps_w.d, d);
+    }
     if (err != cudaSuccess) return err;
-    maps.b[1] = maps.b[2] = maps.b[0];
-    MapSpec d = weights_map(d_w, E, N, K, 32);          // boxes of 64 bytes
-    d.f32 = p.d_w_f32;
-    d.box[0] = p.d_w_f32 ? 16 : 32;
-    err = encode(&maps.d, d);
-    if (err != cudaSuccess) return err;
-    return product<kWeightGrad>(maps, p, ws, 1, d_a != nullptr, st);
+    const bool cut_a = d_a && may_cut(N), cut_w = d_w && may_cut(a_rows);
+    if (d_a && d_w && !cut_a && !cut_w) {
+        int ctas;
+        err = grid_of(&ctas);
+        if (err != cudaSuccess) return err;
+        const int64_t tiles_n = (N + kTileRows - 1) / kTileRows, tiles_k = (K + kTileRows - 1) / kTileRows;
+        const int64_t most_a = tiles_k * (a_rows / kTileRows + (a_rows < E ? a_rows : E));
+        if (most_a + E * tiles_n * tiles_k <= ctas / 2)
+            return pre ? gradients<kGateGrad>(maps, p, maps_w, p, (int)most_a, ctas, st)
+                       : gradients<kRowGrad>(maps, p, maps_w, p, (int)most_a, ctas, st);
+    }
+    if (cut_a || cut_w) err = begin(ws, st);
+    if (err == cudaSuccess && d_a)
+        err = pre ? product<kGateGrad>(maps, p, ws, 0, false, st) : product<kRowGrad>(maps, p, ws, 0, false, st);
+    if (err == cudaSuccess && d_w) err = product<kWeightGrad>(maps_w, p, ws, 1, d_a != nullptr, st);
+    return err;
 }
 
 }  // namespace moe
