@@ -45,6 +45,7 @@ constexpr int kFinishWarps = 8;
 constexpr int kWarpLoad = kFinishWarps, kWarpMma = kFinishWarps + 1, kWarpClear = kFinishWarps + 2;
 constexpr int kMmThreads = 32 * (kFinishWarps + 3);
 constexpr int kTmemColumns = 512;                // two tiles of 256 columns of sums
+constexpr int kSumSteps = 12;                    // d_w: steps summed by the tensor core alone
 constexpr int kMinPart = 8;                      // steps worth a part of their own
 constexpr int kCutSteps = 40;                    // steps that the parts of cut tiles take to be joined
 constexpr int64_t kPart = (int64_t)kTileRows * 128;   // sums of one part of a tile, in one CTA
@@ -418,10 +419,17 @@ __device__ __forceinline__ void issue_steps(Shared &sh, uint8_t *ring, const Arg
     bool ok = true;
     while (ok && walk.next(g)) {
         const uint32_t word = mma_pair_word(g.cols, kAByK, kBByK);
-        if (!(ok = mbar_wait_cluster(&sh.sums_empty[d], sums_phase ^ 1, &sh.dead))) break;
-        tmem_fence_after();
-        const uint32_t sums = sh.tmem + d * kTileRows;
+        const int most = FORM == kWeightGrad ? kSumSteps : g.steps;     // steps of a sum in tensor memory
+        int left = 0;
         for (int c = g.c0; c < g.c1; c++) {
+            const bool fresh = left == 0;
+            if (fresh) {
+                left = min(most, g.c1 - c);
+                if (!(ok = mbar_wait_cluster(&sh.sums_empty[d], sums_phase ^ 1, &sh.dead))) break;
+                tmem_fence_after();
+            }
+            left--;
+            const uint32_t sums = sh.tmem + d * kTileRows;
             if (!(ok = mbar_wait_cluster(&sh.full[s], phase, &sh.dead))) break;
             if (FORM == kWeightGrad && ragged_step(g, sh.count[g.e], c)) {
                 if (!(ok = mbar_wait_cluster(&sh.cleared[s], cleared >> s & 1, &sh.dead))) break;
@@ -437,27 +445,28 @@ __device__ __forceinline__ void issue_steps(Shared &sh, uint8_t *ring, const Arg
                 for (int i = 0; i < 4; i++)     // 16 of the sum: 32 bytes along it, 2 KiB across
                     if (FORM != kWeightGrad || i < n)
                         mma_bf16_pair(sums, a + (uint64_t)(i * (kAByK ? 2 : 128)),
-                                      b + (uint64_t)(i * (kBByK ? 2 : 128)), word, c > g.c0 || i > 0);
+                                      b + (uint64_t)(i * (kBByK ? 2 : 128)), word, !fresh || i > 0);
                 mma_commit_pair(&sh.empty[s]);
-                if (c == g.c1 - 1) mma_commit_pair(&sh.sums_full[d]);
+                if (left == 0) mma_commit_pair(&sh.sums_full[d]);
             }
             __syncwarp();
             if (++s == kStages) {
                 s = 0;
                 phase ^= 1;
             }
+            if (left == 0) {
+                d ^= 1;
+                if (d == 0) sums_phase ^= 1;
+            }
         }
-        d ^= 1;
-        if (d == 0) sums_phase ^= 1;
     }
 }
 
 // ---------------------------------------------------------------- the end of a tile
 
 struct Finish {
-    uint32_t sums;             // the tile's sums in tensor memory, at this warp's lanes
-    const float *from;         // parts of a cut tile: at this thread's row of the first one
-    int parts, here;           // how many, and which of them is in tensor memory only (-1: none)
+    const float *from;         // parts of a cut tile: at this thread's place in the first one
+    int parts, here;           // how many, and which of them this CTA holds and has not stored (-1: none)
 };
 
 // A part's sums: a block of 16 columns is 4 x 128 threads x 4 values, so that a thread moves
@@ -479,25 +488,10 @@ __device__ __forceinline__ void load_part(const Finish &f, int q, int c0, float 
     }
 }
 
-// Columns c0 .. c0 + 15 of the tile, of a cut one over all of its parts in their order;
-// `other` holds part f.here ^ 1 of a tile of two.  (d_w: 16 columns of the lane's row; else
-// as matrices.)
-template <int FORM>
-__device__ __forceinline__ void load_sums(uint32_t sums, float (&v)[kCols])
+// The sums of a cut tile in columns c0 .. c0 + 15 over all of its parts in their order; v holds this
+// CTA's part.
+__device__ __forceinline__ void add_parts(const Finish &f, int c0, float (&v)[kCols])
 {
-    if constexpr (FORM == kWeightGrad) tmem_load(sums, v);
-    else tmem_load_matrices(sums, v);
-}
-template <int FORM>
-__device__ __forceinline__ void tile_sums(const Finish &f, int c0, const float (&other)[kCols], float (&v)[kCols])
-{
-    if (f.parts == 1 || f.here >= 0) load_sums<FORM>(f.sums + c0, v);
-    if (f.parts == 1) return;
-    if (FORM != kWeightGrad && f.parts == 2 && f.here >= 0) {
-#pragma unroll
-        for (int j = 0; j < kCols; j++) v[j] += other[j];       // (the same in either order)
-        return;
-    }
     float sum[kCols] = {};
     for (int q = 0; q < f.parts; q++) {
         float x[kCols];
@@ -507,6 +501,33 @@ __device__ __forceinline__ void tile_sums(const Finish &f, int c0, const float (
     }
 #pragma unroll
     for (int j = 0; j < kCols; j++) v[j] = sum[j];
+}
+
+// By all of the CTA's finishing warps: where this segment is part of a cut tile, whether they are to
+// finish it, which falls to the part that is done last.  Any other goes to memory by
+// `store(slot)`.
+template <typename Store>
+__device__ __forceinline__ bool join_parts(Shared &sh, const Args &p, const Segment &g, Finish &f, Store store)
+{
+    const int row = threadIdx.x & 127;      // of D; the same for the warps that share its columns
+    const uint32_t rank = cluster_rank();
+    f.parts = 1;
+    if (g.c1 - g.c0 == g.steps) return true;
+    const int from = owner_of(sh, g.unit);
+    f.parts = owner_of(sh, g.unit + g.steps - 1) - from + 1;
+    f.here = (int)(blockIdx.x / 2) - from;
+    f.from = p.partial + (int64_t)(4 * from + 2 * rank) * kPart + row * 4;
+    int32_t *const count = p.arrivals + 2 * from + rank;
+    if (named_all(1, kFinishWarps * 32, arrived(count) == f.parts - 1)) return true;
+    f.here = -1;
+    store(p.partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * kPart + row * 4);
+    __threadfence();
+    named_barrier(1, kFinishWarps * 32);
+    if (threadIdx.x == 0) sh.last = atomicAdd(count, 1) == f.parts - 1;
+    named_barrier(1, kFinishWarps * 32);
+    const bool last = sh.last;
+    __threadfence();
+    return last;
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
@@ -635,25 +656,12 @@ __device__ __forceinline__ void load_gates(const Args &p, int64_t first, int row
     }
 }
 
-// d_w: COLS columns (64 bytes) of the warp's 32 rows, the first at (e, n0, k0), by one tile store,
-// which writes what is inside the matrix.
-template <int COLS>
-__device__ __forceinline__ void finish_weights(const CUtensorMap *map, uint8_t *staging, const Finish &f, int c0, int e,
-                                               int n0, int k0)
+// d_w: 64 bytes of each of the warp's 32 rows, the first at (e, n0, k), by one tile store, which writes
+// what is inside the matrix.
+__device__ __forceinline__ void weights_out(const CUtensorMap *map, uint8_t *staging, const uint32_t (&words)[16], int e,
+                                            int n0, int k)
 {
     const int lane = threadIdx.x & 31;
-    uint32_t words[16];
-    const float none[kCols] = {};
-#pragma unroll
-    for (int i = 0; i < COLS; i += kCols) {
-        float v[kCols];
-        tile_sums<kWeightGrad>(f, c0 + i, none, v);
-#pragma unroll
-        for (int j = 0; j < kCols; j++) {
-            if constexpr (COLS == 16) words[j] = __float_as_uint(v[j]);
-            else if (j % 2 == 0) words[(i + j) / 2] = bf16_pair(v[j], v[j + 1]);
-        }
-    }
     if (lane == 0) tile_stores_read();
     __syncwarp();
 #pragma unroll
@@ -661,15 +669,15 @@ __device__ __forceinline__ void finish_weights(const CUtensorMap *map, uint8_t *
         *(uint4 *)staged<4>(staging, lane, i) = make_uint4(words[4 * i], words[4 * i + 1], words[4 * i + 2], words[4 * i + 3]);
     async_proxy_fence();
     __syncwarp();
-    if (lane == 0) tile_store3(map, k0 + c0, n0, e, staging);
+    if (lane == 0) tile_store3(map, k, n0, e, staging);
 }
 
 template <int FORM>
-__device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const Args &p, const Maps &maps, const Shape &w)
+__device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const Args &p, const Shape &w)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3, group = warp >> 2;
+    constexpr int kTurn = kGroups * kCols;
     const uint32_t rank = cluster_rank();
-    const int row = quarter * 32 + lane;                 // of this CTA's 128 rows of D
     staging += warp * kStaging;
     Walk<FORM> walk(sh, p, w);
     Segment g;
@@ -679,72 +687,44 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
     while (walk.next(g)) {
         const int a_row = g.tile * kTileRows + rank * 128 + quarter * 32;    // the warp's first row of A
         const int64_t first = sh.start[g.e] + g.row0;
-        int from = 0, parts = 1;
-        if (g.c1 - g.c0 < g.steps) {
-            from = owner_of(sh, g.unit);
-            parts = owner_of(sh, g.unit + g.steps - 1) - from + 1;
-        }
         int4 gates[4];
-        if constexpr (FORM == kGateGrad)
-            load_gates(p, first + group * kCols, g.rows - group * kCols, a_row, gates);
+        if constexpr (FORM == kGateGrad) load_gates(p, first + group * kCols, g.rows - group * kCols, a_row, gates);
         const bool ok = mbar_wait_cluster(&sh.sums_full[d], phase, &sh.dead);
         if (!named_all(1, kFinishWarps * 32, ok)) break;
         tmem_fence_after();
         const uint32_t sums = sh.tmem + ((uint32_t)(quarter * 32) << 16) + d * kTileRows;
-        Finish f{sums, p.partial + (int64_t)(4 * from + 2 * rank) * kPart + row * 4, parts, (int)(blockIdx.x / 2) - from};
-        bool finish = true;
-        if (parts > 1) {
-            // the part that is done last adds the others, from memory, to its own
-            int32_t *const count = p.arrivals + 2 * from + rank;
-            finish = named_all(1, kFinishWarps * 32, arrived(count) == parts - 1);
-            if (!finish) {
-                f.here = -1;
-                float *slot = p.partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * kPart + row * 4;
-                for (int c0 = group * kCols; c0 < g.cols; c0 += kGroups * kCols) {
-                    float v[kCols];
-                    load_sums<FORM>(sums + c0, v);
-                    store_part(slot, c0, v);
-                }
-                __threadfence();
-                named_barrier(1, kFinishWarps * 32);
-                if (threadIdx.x == 0) sh.last = atomicAdd(count, 1) == parts - 1;
-                named_barrier(1, kFinishWarps * 32);
-                finish = sh.last;
-                __threadfence();
+        Finish f;
+        const bool finish = join_parts(sh, p, g, f, [&](float *slot) {
+            for (int c0 = group * kCols; c0 < g.rows; c0 += kTurn) {
+                float v[kCols];
+                tmem_load_matrices(sums + c0, v);
+                store_part(slot, c0, v);
             }
-        }
+        });
         if (finish) {
-            if constexpr (FORM == kWeightGrad) {
-                if (a_row < p.N) {
+            // the other part of a tile in two is loaded a block of columns ahead
+            const bool two = f.parts == 2 && f.here >= 0;
+            float other[kCols] = {}, ahead[kCols] = {};
+            if (two) load_part(f, f.here ^ 1, group * kCols, other);
 #pragma unroll 1
-                    for (int c0 = group * 32; c0 < g.rows; c0 += kGroups * 32)
-                        if (p.d_w_f32) {
-                            finish_weights<16>(&maps.d, staging, f, c0, g.e, a_row, g.row0);
-                            if (c0 + 16 < g.rows) finish_weights<16>(&maps.d, staging, f, c0 + 16, g.e, a_row, g.row0);
-                        } else {
-                            finish_weights<32>(&maps.d, staging, f, c0, g.e, a_row, g.row0);
-                        }
-                }
-            } else {
-                // the other part of a tile in two is loaded a block of columns ahead
-                const bool two = f.parts == 2 && f.here >= 0;
-                float other[kCols] = {}, ahead[kCols] = {};
-                if (two) load_part(f, f.here ^ 1, group * kCols, other);
-#pragma unroll 1
-                for (int c0 = group * kCols; c0 < g.rows; c0 += kGroups * kCols) {
-                    float v[kCols];
-                    if (two && c0 + kGroups * kCols < g.rows) load_part(f, f.here ^ 1, c0 + kGroups * kCols, ahead);
-                    tile_sums<FORM>(f, c0, other, v);
+            for (int c0 = group * kCols; c0 < g.rows; c0 += kTurn) {
+                float v[kCols];
+                if (two && c0 + kTurn < g.rows) load_part(f, f.here ^ 1, c0 + kTurn, ahead);
+                if (f.parts == 1 || f.here >= 0) tmem_load_matrices(sums + c0, v);
+                if (two) {
 #pragma unroll
-                    for (int j = 0; j < kCols; j++) other[j] = ahead[j];
-                    int4 next[4];
-                    if constexpr (FORM == kGateGrad)
-                        load_gates(p, first + c0 + kGroups * kCols, g.rows - c0 - kGroups * kCols, a_row, next);
-                    finish_rows<FORM>(p, staging, v, first + c0, g.rows - c0, FORM == kGated ? a_row / 2 : a_row, gates);
-                    if constexpr (FORM == kGateGrad)
-#pragma unroll
-                        for (int i = 0; i < 4; i++) gates[i] = next[i];
+                    for (int j = 0; j < kCols; j++) v[j] += other[j];       // (the same in either order)
+                } else if (f.parts > 1) {
+                    add_parts(f, c0, v);
                 }
+#pragma unroll
+                for (int j = 0; j < kCols; j++) other[j] = ahead[j];
+                int4 next[4];
+                if constexpr (FORM == kGateGrad) load_gates(p, first + c0 + kTurn, g.rows - c0 - kTurn, a_row, next);
+                finish_rows<FORM>(p, staging, v, first + c0, g.rows - c0, FORM == kGated ? a_row / 2 : a_row, gates);
+                if constexpr (FORM == kGateGrad)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) gates[i] = next[i];
             }
         }
         tmem_fence_before();
@@ -753,7 +733,80 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
         d ^= 1;
         if (d == 0) phase ^= 1;
     }
-    if (FORM == kWeightGrad && lane == 0) tile_stores_done();
+}
+
+// d_w.  The tensor core cuts its sums off where they leave fp32, which grows with their length (2,048
+// rows: 2.1e-6 of the result, towards zero).  So it sums kSumSteps steps at a time, and these
+// warps add them up, rounding to nearest, in registers: a thread has half of the columns of a row
+// of D.  (8 experts' 16,384 rows of 2,048 x 1,408 in fp32: 8.4e-7 and 75 us with 12 steps, 5.8e-7 and 84 us
+// with 8, 1.1e-6 and 71 us with 16.)  That also hands tensor memory back before the tile is written.
+constexpr int kBlocks = kTileRows / kCols / kGroups;
+
+__device__ __forceinline__ void finish_weights(Shared &sh, uint8_t *staging, const Args &p, const Maps &maps, const Shape &w)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3, group = warp >> 2;
+    const uint32_t rank = cluster_rank();
+    staging += warp * kStaging;
+    Walk<kWeightGrad> walk(sh, p, w);
+    Segment g;
+    int d = 0;
+    uint32_t phase = 0;
+    // block b of this warp: 32 columns by the groups in turn
+    auto column = [&](int b) { return ((b >> 1) * kGroups + group) * 32 + (b & 1) * kCols; };
+    pdl_wait();                                          // (late: the kernel before may use `partial`)
+    while (walk.next(g)) {
+        const int a_row = g.tile * kTileRows + rank * 128 + quarter * 32;    // the warp's first row of A
+        float sum[kBlocks][kCols] = {};
+        bool ok = true;
+        for (int c = g.c0; ok && c < g.c1; c += kSumSteps) {
+            if (!(ok = mbar_wait_cluster(&sh.sums_full[d], phase, &sh.dead))) break;
+            tmem_fence_after();
+            const uint32_t sums = sh.tmem + ((uint32_t)(quarter * 32) << 16) + d * kTileRows;
+#pragma unroll
+            for (int b = 0; b < kBlocks; b++)
+                if (column(b) < g.cols) {
+                    float v[kCols];
+                    tmem_load(sums + column(b), v);
+#pragma unroll
+                    for (int j = 0; j < kCols; j++) sum[b][j] += v[j];
+                }
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(cluster_addr(&sh.sums_empty[d], 0));
+            d ^= 1;
+            if (d == 0) phase ^= 1;
+        }
+        if (!named_all(1, kFinishWarps * 32, ok)) break;
+        Finish f;
+        const bool finish = join_parts(sh, p, g, f, [&](float *slot) {
+#pragma unroll
+            for (int b = 0; b < kBlocks; b++)
+                if (column(b) < g.cols) store_part(slot, column(b), sum[b]);
+        });
+        if (!finish || a_row >= p.N) continue;
+#pragma unroll
+        for (int b = 0; b < kBlocks; b += 2) {
+            if (column(b) >= g.rows) break;
+            if (f.parts > 1)
+#pragma unroll
+                for (int i = 0; i < 2; i++) add_parts(f, column(b + i), sum[b + i]);
+            uint32_t words[16];
+            if (p.d_w_f32) {
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+                    if (column(b + i) < g.rows) {
+#pragma unroll
+                        for (int j = 0; j < kCols; j++) words[j] = __float_as_uint(sum[b + i][j]);
+                        weights_out(&maps.d, staging, words, g.e, a_row, g.row0 + column(b + i));
+                    }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; j++) words[j] = bf16_pair(sum[b + j / 8][j % 8 * 2], sum[b + j / 8][j % 8 * 2 + 1]);
+                weights_out(&maps.d, staging, words, g.e, a_row, g.row0 + column(b));
+            }
+        }
+    }
+    if (lane == 0) tile_stores_done();
 }
 
 template <int FORM>
@@ -803,7 +856,8 @@ __device__ __forceinline__ void run_product(uint8_t *raw, const Maps &maps, cons
     } else if (warp == kWarpClear) {
         if constexpr (FORM == kWeightGrad) clear_steps(sh, ring, p, shape);
     } else {
-        finish_steps<FORM>(sh, staging, p, maps, shape);
+        if constexpr (FORM == kWeightGrad) finish_weights(sh, staging, p, maps, shape);
+        else finish_steps<FORM>(sh, staging, p, shape);
     }
     tmem_fence_before();
     __syncthreads();
