@@ -46,7 +46,9 @@ constexpr int kWarpLoad = kFinishWarps, kWarpMma = kFinishWarps + 1, kWarpClear 
 constexpr int kMmThreads = 32 * (kFinishWarps + 3);
 constexpr int kTmemColumns = 512;                // two tiles of 256 columns of sums
 constexpr int kSumSteps = 12;                    // d_w: steps summed by the tensor core alone
-constexpr int kMinPart = 8;                      // steps worth a part of their own
+// Steps worth a part of their own, for tiles of up to 64 rows and of more: the last one reads the sums
+// of all (375 rows over 4 experts of 48 x 4,040: 20.8 us with 8 steps, 16.4 with 16).
+constexpr int kMinPart = 8, kMinPartWide = 16;
 constexpr int kCutSteps = 40;                    // steps that the parts of cut tiles take to be joined
 constexpr int64_t kPart = (int64_t)kTileRows * 128;   // sums of one part of a tile, in one CTA
 constexpr int kMaxCtas = 160;
@@ -60,15 +62,16 @@ struct Shared {
     int before[kMaxE + 1];           // steps of the experts before e
     int start[kMaxE], count[kMaxE];
     uint32_t tmem;
+    int first_pair, pairs;           // the pairs that share the work
     int tasks, waves;                // tiles, and how many of them a pair takes whole, in turn
     int shared;                      // first step of the rest, which is cut evenly
     int parts;                       // pairs that share it
     int base, more;                  // the first `more` pairs have base + 1 steps, the rest base
     int last;
+    bool weights;                    // of two products at once this CTA has d_w
     volatile int dead;               // a wait gave up
 };
 constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kFinishWarps * kStaging + sizeof(Shared);
-
 struct Maps {
     CUtensorMap a, b[3];             // b: boxes of 16, 64 and 128 rows (d_w: the first, of 64)
     CUtensorMap d;                   // d_w
@@ -83,8 +86,6 @@ struct Args {
     bool d_w_f32;
     float *partial;
     int32_t *arrivals;
-    bool late;                       // the kernel before has waited for the inputs, and is not waited for
-    int first_pair, pairs;           // the pairs that share the work
     uint32_t *dev_status;
 };
 
@@ -108,7 +109,7 @@ __device__ __forceinline__ Shape shape_of(const Args &p)
         return {p.E, (p.N + kTileRows - 1) / kTileRows, 0, (p.K + kTileRows - 1) / kTileRows};
     return {p.E, (p.rows_a + kTileRows - 1) / kTileRows, (p.sums + kStep - 1) / kStep, 0};
 }
-// (an expert without rows has one step of zeros, which writes the zeros of its gradient)
+// (an expert without rows has one step, of nothing but the zeros of its gradient)
 __device__ __forceinline__ int steps_of(const Shape &w, int count)
 {
     return w.steps ? w.steps : max(1, (int)(((unsigned)count + kStep - 1) / kStep));
@@ -131,7 +132,7 @@ struct Walk {
     int wave, at, to;
     __device__ Walk(const Shared &s, const Args &a, const Shape &shape) : sh(s), p(a), w(shape)
     {
-        const int b = blockIdx.x / 2 - p.first_pair;
+        const int b = blockIdx.x / 2 - sh.first_pair;
         wave = 0;
         at = sh.shared + (b < sh.parts ? b * sh.base + min(b, sh.more) : 0);
         to = at + (b < sh.parts ? sh.base + (b < sh.more) : 0);
@@ -152,7 +153,7 @@ struct Walk {
     {
         int task, count;
         if (wave < sh.waves) {
-            task = wave * p.pairs + blockIdx.x / 2 - p.first_pair;
+            task = wave * sh.pairs + blockIdx.x / 2 - sh.first_pair;
             wave++;
             if (task >= sh.tasks) return false;
             if constexpr (FORM == kWeightGrad) {
@@ -208,7 +209,7 @@ __device__ __forceinline__ void scan_experts(Shared &sh, const Args &p, const Sh
 {
     constexpr int kAhead = 4;            // loads in flight
     const int lane = threadIdx.x & 31;
-    int before = 0, tasks = 0, longest = 0;
+    int before = 0, tasks = 0, longest = 0, widest = 0;
     bool fell = false, bad = false;
     for (int e0 = 0; e0 < p.E; e0 += 32 * kAhead) {
         int start[kAhead], count[kAhead];
@@ -233,6 +234,7 @@ __device__ __forceinline__ void scan_experts(Shared &sh, const Args &p, const Sh
             const int n = e >= p.E ? 0 : FORM == kWeightGrad ? w.tiles * w.tiles_b : w.tiles * row_tiles(count[i]);
             const int units = n * steps_of(w, count[i]);
             longest = max(longest, e < p.E ? steps_of(w, count[i]) : 0);
+            widest = max(widest, count[i]);
             const int inc = warp_inclusive_scan(units);
             if (e < p.E) {
                 sh.start[e] = start[i];
@@ -245,6 +247,7 @@ __device__ __forceinline__ void scan_experts(Shared &sh, const Args &p, const Sh
     }
     tasks = __reduce_add_sync(kFull, tasks);
     longest = __reduce_max_sync(kFull, longest);
+    widest = FORM == kWeightGrad ? kTileRows : __reduce_max_sync(kFull, widest);
     __syncwarp();
     if (lane == 0) {
         sh.before[p.E] = before;
@@ -252,7 +255,7 @@ __device__ __forceinline__ void scan_experts(Shared &sh, const Args &p, const Sh
         // operands come from L2.  Cutting the last ones evenly takes kCutSteps, and there is nothing
         // to gain where the pairs' last tiles wait for less; nor are all tiles taken in turn
         // where a few experts have most of the steps.
-        const int pairs = p.pairs, turns = (tasks + pairs - 1) / pairs;
+        const int pairs = sh.pairs, turns = (tasks + pairs - 1) / pairs;
         const bool whole = ((int64_t)turns * pairs - tasks) * longest <= (int64_t)kCutSteps * pairs;
         const bool even = (int64_t)longest * tasks <= 2 * (int64_t)before;
         const int waves = longest <= kCutSteps ? turns : !even ? 0 : whole ? turns : max(0, tasks / pairs - 1);
@@ -264,7 +267,7 @@ __device__ __forceinline__ void scan_experts(Shared &sh, const Args &p, const Sh
         }
         const int rest = before - shared;
         // every pair takes part where that leaves it kMinPart steps or a tile
-        const int parts = min(pairs, max(tasks - task, rest / kMinPart));
+        const int parts = min(pairs, max(tasks - task, rest / (widest <= 64 ? kMinPart : kMinPartWide)));
         sh.tasks = tasks;
         sh.waves = waves;
         sh.shared = shared;
@@ -272,7 +275,7 @@ __device__ __forceinline__ void scan_experts(Shared &sh, const Args &p, const Sh
         sh.base = parts ? rest / parts : 0;
         sh.more = parts ? rest - sh.base * parts : 0;
     }
-    if (bad && blockIdx.x == 2 * p.first_pair) flag_status(p.dev_status, MOE_ERR_INVALID_ARG);
+    if (bad && (int)blockIdx.x == 2 * sh.first_pair) flag_status(p.dev_status, MOE_ERR_INVALID_ARG);
     __syncwarp();
 }
 
@@ -288,10 +291,10 @@ __device__ __forceinline__ int arrived(const int32_t *p)
 // d_w: rows of the expert in step c, steps of the MMA that they take, and whether rows of
 // others are in the last one.
 __device__ __forceinline__ int valid_rows(int count, int c) { return min(kStep, count - c * kStep); }
-__device__ __forceinline__ int mma_steps(int valid) { return max(1, (valid + 15) / 16); }
+__device__ __forceinline__ int mma_steps(int valid) { return (valid + 15) / 16; }
 __device__ __forceinline__ bool ragged_step(const Segment &g, int count, int c)
 {
-    return c == g.steps - 1 && (count % kStep != 0 || count == 0);
+    return c == g.steps - 1 && count % kStep != 0;
 }
 
 // Rows of B that a CTA loads for `half` rows: by 16 up to 32, else 64 or 128.
@@ -307,6 +310,7 @@ __device__ __forceinline__ void load_steps(Shared &sh, uint8_t *ring, const Args
     uint32_t phase = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
+        if (FORM == kWeightGrad && sh.count[g.e] == 0) continue;
         const int half = g.cols / 2;
         const int a0 = g.tile * kTileRows + rank * 128;      // first row of A
         const int start = sh.start[g.e], count = sh.count[g.e];
@@ -386,6 +390,7 @@ __device__ __forceinline__ void clear_steps(Shared &sh, uint8_t *ring, const Arg
     bool ok = true;
     while (ok && walk.next(g)) {
         const int count = sh.count[g.e];
+        if (count == 0) continue;
         const int ahead = g.c1 - g.c0;
         if (ragged_step(g, count, g.c1 - 1)) {
             const int last = (s + ahead - 1) % kStages;
@@ -418,6 +423,7 @@ __device__ __forceinline__ void issue_steps(Shared &sh, uint8_t *ring, const Arg
     uint32_t phase = 0, sums_phase = 0, cleared = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
+        if (FORM == kWeightGrad && sh.count[g.e] == 0) continue;
         const uint32_t word = mma_pair_word(g.cols, kAByK, kBByK);
         const int most = FORM == kWeightGrad ? kSumSteps : g.steps;     // steps of a sum in tensor memory
         int left = 0;
@@ -490,14 +496,20 @@ __device__ __forceinline__ void load_part(const Finish &f, int q, int c0, float 
 
 // The sums of a cut tile in columns c0 .. c0 + 15 over all of its parts in their order; v holds this
 // CTA's part.
+template <int AHEAD>      // parts whose loads are in flight
 __device__ __forceinline__ void add_parts(const Finish &f, int c0, float (&v)[kCols])
 {
     float sum[kCols] = {};
-    for (int q = 0; q < f.parts; q++) {
-        float x[kCols];
-        if (q != f.here) load_part(f, q, c0, x);
+    for (int q0 = 0; q0 < f.parts; q0 += AHEAD) {
+        float x[AHEAD][kCols];
 #pragma unroll
-        for (int j = 0; j < kCols; j++) sum[j] += q == f.here ? v[j] : x[j];
+        for (int i = 0; i < AHEAD; i++)
+            if (q0 + i < f.parts && q0 + i != f.here) load_part(f, q0 + i, c0, x[i]);
+#pragma unroll
+        for (int i = 0; i < AHEAD; i++)
+            if (q0 + i < f.parts)
+#pragma unroll
+                for (int j = 0; j < kCols; j++) sum[j] += q0 + i == f.here ? v[j] : x[i][j];
     }
 #pragma unroll
     for (int j = 0; j < kCols; j++) v[j] = sum[j];
@@ -505,8 +517,8 @@ __device__ __forceinline__ void add_parts(const Finish &f, int c0, float (&v)[kC
 
 // By all of the CTA's finishing warps: where this segment is part of a cut tile, whether they are to
 // finish it, which falls to the part that is done last.  Any other goes to memory by
-// `store(slot)`.
-template <typename Store>
+// `store(slot)`; EARLY: the last one does not, where that is known before.
+template <bool EARLY, typename Store>
 __device__ __forceinline__ bool join_parts(Shared &sh, const Args &p, const Segment &g, Finish &f, Store store)
 {
     const int row = threadIdx.x & 127;      // of D; the same for the warps that share its columns
@@ -515,10 +527,10 @@ __device__ __forceinline__ bool join_parts(Shared &sh, const Args &p, const Segm
     if (g.c1 - g.c0 == g.steps) return true;
     const int from = owner_of(sh, g.unit);
     f.parts = owner_of(sh, g.unit + g.steps - 1) - from + 1;
-    f.here = (int)(blockIdx.x / 2) - from;
-    f.from = p.partial + (int64_t)(4 * from + 2 * rank) * kPart + row * 4;
+    f.here = (int)(blockIdx.x / 2) - sh.first_pair - from;
+    f.from = p.partial + (int64_t)(4 * (sh.first_pair + from) + 2 * rank) * kPart + row * 4;
     int32_t *const count = p.arrivals + 2 * from + rank;
-    if (named_all(1, kFinishWarps * 32, arrived(count) == f.parts - 1)) return true;
+    if (EARLY && named_all(1, kFinishWarps * 32, arrived(count) == f.parts - 1)) return true;
     f.here = -1;
     store(p.partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * kPart + row * 4);
     __threadfence();
@@ -683,7 +695,6 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
     Segment g;
     int d = 0;
     uint32_t phase = 0;
-    pdl_wait();                                          // (late: the kernel before may use `partial`)
     while (walk.next(g)) {
         const int a_row = g.tile * kTileRows + rank * 128 + quarter * 32;    // the warp's first row of A
         const int64_t first = sh.start[g.e] + g.row0;
@@ -694,7 +705,7 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
         tmem_fence_after();
         const uint32_t sums = sh.tmem + ((uint32_t)(quarter * 32) << 16) + d * kTileRows;
         Finish f;
-        const bool finish = join_parts(sh, p, g, f, [&](float *slot) {
+        const bool finish = join_parts<true>(sh, p, g, f, [&](float *slot) {
             for (int c0 = group * kCols; c0 < g.rows; c0 += kTurn) {
                 float v[kCols];
                 tmem_load_matrices(sums + c0, v);
@@ -715,7 +726,7 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
 #pragma unroll
                     for (int j = 0; j < kCols; j++) v[j] += other[j];       // (the same in either order)
                 } else if (f.parts > 1) {
-                    add_parts(f, c0, v);
+                    add_parts<2>(f, c0, v);
                 }
 #pragma unroll
                 for (int j = 0; j < kCols; j++) other[j] = ahead[j];
@@ -753,12 +764,11 @@ __device__ __forceinline__ void finish_weights(Shared &sh, uint8_t *staging, con
     uint32_t phase = 0;
     // block b of this warp: 32 columns by the groups in turn
     auto column = [&](int b) { return ((b >> 1) * kGroups + group) * 32 + (b & 1) * kCols; };
-    pdl_wait();                                          // (late: the kernel before may use `partial`)
     while (walk.next(g)) {
         const int a_row = g.tile * kTileRows + rank * 128 + quarter * 32;    // the warp's first row of A
         float sum[kBlocks][kCols] = {};
         bool ok = true;
-        for (int c = g.c0; ok && c < g.c1; c += kSumSteps) {
+        for (int c = sh.count[g.e] ? g.c0 : g.c1; ok && c < g.c1; c += kSumSteps) {
             if (!(ok = mbar_wait_cluster(&sh.sums_full[d], phase, &sh.dead))) break;
             tmem_fence_after();
             const uint32_t sums = sh.tmem + ((uint32_t)(quarter * 32) << 16) + d * kTileRows;
@@ -778,7 +788,7 @@ __device__ __forceinline__ void finish_weights(Shared &sh, uint8_t *staging, con
         }
         if (!named_all(1, kFinishWarps * 32, ok)) break;
         Finish f;
-        const bool finish = join_parts(sh, p, g, f, [&](float *slot) {
+        const bool finish = join_parts<false>(sh, p, g, f, [&](float *slot) {
 #pragma unroll
             for (int b = 0; b < kBlocks; b++)
                 if (column(b) < g.cols) store_part(slot, column(b), sum[b]);
@@ -789,7 +799,7 @@ __device__ __forceinline__ void finish_weights(Shared &sh, uint8_t *staging, con
             if (column(b) >= g.rows) break;
             if (f.parts > 1)
 #pragma unroll
-                for (int i = 0; i < 2; i++) add_parts(f, column(b + i), sum[b + i]);
+                for (int i = 0; i < 2; i++) add_parts<1>(f, column(b + i), sum[b + i]);    // (all from memory)
             uint32_t words[16];
             if (p.d_w_f32) {
 #pragma unroll
@@ -809,20 +819,26 @@ __device__ __forceinline__ void finish_weights(Shared &sh, uint8_t *staging, con
     if (lane == 0) tile_stores_done();
 }
 
-template <int FORM>
-__device__ __forceinline__ void run_product(uint8_t *raw, const Maps &maps, const Args &p)
-{
-    uint8_t *ring = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
-    uint8_t *staging = ring + kStages * kStageBytes;
-    Shared &sh = *(Shared *)(staging + kFinishWarps * kStaging);
-    const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
-    const Shape shape = shape_of<FORM>(p);
+// The places in shared memory that do not depend on the product.
+struct Memory {
+    uint8_t *ring;
+    Shared &sh;
+    __device__ Memory(uint8_t *raw)
+        : ring(raw + (1024 - (smem_addr(raw) & 1023)) % 1024),
+          sh(*(Shared *)(ring + kStages * kStageBytes + kFinishWarps * kStaging))
+    {
+    }
+};
 
+// Before the work is known: barriers, tensor memory, and the wait for the kernel before.
+__device__ __forceinline__ void start(Shared &sh, int warp)
+{
+    const int lane = threadIdx.x & 31;
     if (warp == kWarpLoad) {
         if (lane == 0) {
             sh.dead = 0;
-            map_prefetch(&maps.a);
-            map_prefetch(&maps.b[0]);
+            sh.first_pair = 0;
+            sh.pairs = gridDim.x / 2;
         }
     } else if (warp == kWarpMma) {
         if (lane < kStages) {
@@ -840,15 +856,26 @@ __device__ __forceinline__ void run_product(uint8_t *raw, const Maps &maps, cons
         tmem_alloc_pair(&sh.tmem, kTmemColumns);
         tmem_fence_before();
     }
-    // The kernel after this one starts when all CTAs have passed here, so that it may read what is
-    // older than this one at once.
-    if (!p.late) pdl_wait();
+    pdl_wait();
     pdl_trigger();
-    if (warp == kWarpLoad) scan_experts<FORM>(sh, p, shape);
-    __syncthreads();
-    cluster_barrier();
-    tmem_fence_after();
+}
 
+template <int FORM>
+__device__ __forceinline__ void scan_product(Shared &sh, const Maps &maps, const Args &p)
+{
+    if ((threadIdx.x & 31) == 0) {
+        map_prefetch(&maps.a);
+        map_prefetch(&maps.b[0]);
+    }
+    scan_experts<FORM>(sh, p, shape_of<FORM>(p));
+}
+
+// By all threads, after the load warp's scan.
+template <int FORM>
+__device__ __forceinline__ void run_product(uint8_t *ring, Shared &sh, int warp, const Maps &maps, const Args &p)
+{
+    const Shape shape = shape_of<FORM>(p);
+    uint8_t *staging = ring + kStages * kStageBytes;
     if (warp == kWarpLoad) {
         load_steps<FORM>(sh, ring, p, maps, shape);
     } else if (warp == kWarpMma) {
@@ -859,11 +886,15 @@ __device__ __forceinline__ void run_product(uint8_t *raw, const Maps &maps, cons
         if constexpr (FORM == kWeightGrad) finish_weights(sh, staging, p, maps, shape);
         else finish_steps<FORM>(sh, staging, p, shape);
     }
+}
+
+__device__ __forceinline__ void end(Shared &sh, int warp, uint32_t *dev_status)
+{
     tmem_fence_before();
     __syncthreads();
     cluster_barrier();
     if (warp == kWarpClear) {
-        if (sh.dead && lane == 0) flag_status(p.dev_status, MOE_ERR_TIMEOUT);
+        if (sh.dead && (threadIdx.x & 31) == 0) flag_status(dev_status, MOE_ERR_TIMEOUT);
         tmem_fence_after();
         tmem_free_pair(sh.tmem, kTmemColumns);
     }
@@ -874,19 +905,68 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     k_expert_product(const __grid_constant__ Maps maps, const __grid_constant__ Args p)
 {
     extern __shared__ uint8_t raw[];
-    run_product<FORM>(raw, maps, p);
+    const Memory m(raw);
+    const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
+    start(m.sh, warp);
+    if (warp == kWarpLoad) scan_product<FORM>(m.sh, maps, p);
+    __syncthreads();
+    cluster_barrier();
+    tmem_fence_after();
+    run_product<FORM>(m.ring, m.sh, warp, maps, p);
+    end(m.sh, warp, p.dev_status);
 }
 
-// Both gradients in one launch, where together they have no more tiles than there are pairs: pairs
-// with tiles of their own each (five experts' 300 rows of 328 x 648: 18 us in two launches).
+// Pairs for the rows' gradient where both gradients are taken at once, by what they take: their steps,
+// and those that the end of a tile is worth by what it reads and writes.  By one warp, the same in
+// every CTA.  (Counting the turns of each side for every split took longer than it won.)
+__device__ __forceinline__ int split_pairs(const Args &p)
+{
+    const int rows_end = p.pre ? 8 : 6, weights_end = p.d_w_f32 ? 8 : 6;
+    const Shape a = shape_of<kRowGrad>(p), w = shape_of<kWeightGrad>(p);
+    int tiles = 0, steps = 0;
+    bool bad = false;
+    for (int e = threadIdx.x & 31; e < p.E; e += 32) {
+        int start, count;
+        expert_rows(p.offsets, p.counts, p.block_rows, p.a_rows, e, start, count, bad);
+        tiles += row_tiles(count);
+        steps += steps_of(w, count) + weights_end;
+    }
+    const float rows = (float)__reduce_add_sync(kFull, tiles) * (float)(a.tiles * (a.steps + rows_end));
+    const float weights = (float)__reduce_add_sync(kFull, steps) * (float)(w.tiles * w.tiles_b);
+    const int pairs = gridDim.x / 2;
+    return rows == 0.f ? 0 : min(pairs - 1, max(1, (int)((float)pairs * rows / (rows + weights) + 0.5f)));
+}
+
+// Both gradients in one launch, each on pairs of its own: one start and one end, and one's stores beside
+// the other's MMAs (8 experts' 4,096 rows of 2,048 x 1,408: 63 us, 71 in two launches; 300 rows of 328 x 648
+// in five experts: 13 us, 19).
 template <int FORM>
 __global__ void __launch_bounds__(kMmThreads, 1)
     k_expert_gradients(const __grid_constant__ Maps maps, const __grid_constant__ Args p,
                        const __grid_constant__ Maps maps_w, const __grid_constant__ Args p_w)
 {
     extern __shared__ uint8_t raw[];
-    if ((int)blockIdx.x / 2 < p.pairs) run_product<FORM>(raw, maps, p);
-    else run_product<kWeightGrad>(raw, maps_w, p_w);
+    const Memory m(raw);
+    const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
+    start(m.sh, warp);
+    if (warp == kWarpLoad) {
+        const int split = split_pairs(p);
+        const bool weights = (int)blockIdx.x / 2 >= split;
+        if ((threadIdx.x & 31) == 0) {
+            m.sh.first_pair = weights ? split : 0;
+            m.sh.pairs = weights ? gridDim.x / 2 - split : split;
+            m.sh.weights = weights;
+        }
+        __syncwarp();
+        if (weights) scan_product<kWeightGrad>(m.sh, maps_w, p_w);
+        else scan_product<FORM>(m.sh, maps, p);
+    }
+    __syncthreads();
+    cluster_barrier();
+    tmem_fence_after();
+    if (m.sh.weights) run_product<kWeightGrad>(m.ring, m.sh, warp, maps_w, p_w);
+    else run_product<FORM>(m.ring, m.sh, warp, maps, p);
+    end(m.sh, warp, p.dev_status);
 }
 
 // Clears the arrival counters of cut tiles.
@@ -987,18 +1067,14 @@ cudaError_t grid_of(int *ctas)
     return cudaSuccess;
 }
 
-// `set`: which of the two sets of counters, and whether a product before this one of the same call has
-// waited for the inputs.
 template <int FORM>
-cudaError_t product(const Maps &maps, Args p, void *ws, int set, bool late, cudaStream_t st)
+cudaError_t product(const Maps &maps, Args p, void *ws, cudaStream_t st)
 {
     int ctas;
     cudaError_t err = grid_of(&ctas);
     if (err != cudaSuccess) return err;
     p.partial = (float *)ws;
-    p.arrivals = (int32_t *)((uint8_t *)ws + kPartialBytes) + set * kMaxCtas;
-    p.late = late;
-    p.pairs = ctas / 2;
+    p.arrivals = (int32_t *)((uint8_t *)ws + kPartialBytes);
     err = cudaFuncSetAttribute(k_expert_product<FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (err != cudaSuccess) return err;
     MOE_TRACED_LAUNCH("k_expert_product", st,
@@ -1006,14 +1082,17 @@ cudaError_t product(const Maps &maps, Args p, void *ws, int set, bool late, cuda
     return err;
 }
 
-// The rows' gradient on the first `pairs` pairs, the weights' on the others; no tile is cut.
 template <int FORM>
-cudaError_t gradients(const Maps &maps, Args p, const Maps &maps_w, Args p_w, int pairs, int ctas, cudaStream_t st)
+cudaError_t gradients(const Maps &maps, Args p, const Maps &maps_w, void *ws, cudaStream_t st)
 {
-    p.pairs = p_w.first_pair = pairs;
-    p_w.pairs = ctas / 2 - pairs;
-    cudaError_t err =
-        cudaFuncSetAttribute(k_expert_gradients<FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    int ctas;
+    cudaError_t err = grid_of(&ctas);
+    if (err != cudaSuccess) return err;
+    p.partial = (float *)ws;
+    p.arrivals = (int32_t *)((uint8_t *)ws + kPartialBytes);
+    Args p_w = p;
+    p_w.arrivals += kMaxCtas;
+    err = cudaFuncSetAttribute(k_expert_gradients<FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (err != cudaSuccess) return err;
     MOE_TRACED_LAUNCH("k_expert_gradients", st,
         err = launch_pdl_cluster(k_expert_gradients<FORM>, dim3(ctas), dim3(kMmThreads), kSmem, 2, st, maps, p, maps_w, p_w));
@@ -1047,10 +1126,10 @@ cudaError_t launch_expert_product(const uint16_t *a, int a_rows, const int32_t *
     if (err == cudaSuccess) err = row_boxes(maps, a, a_rows, K);
     if (err != cudaSuccess) return err;
     const Args p{offsets, counts, block_rows, a_rows, E, N, K, gated ? 2 * N : N, K, (__nv_bfloat16 *)y,
-                 (__nv_bfloat16 *)pre, nullptr, nullptr, false, nullptr, nullptr, false, 0, 0, dev_status};
+                 (__nv_bfloat16 *)pre, nullptr, nullptr, false, nullptr, nullptr, dev_status};
     if (may_cut(K)) err = begin(ws, st);
     if (err != cudaSuccess) return err;
-    return gated ? product<kGated>(maps, p, ws, 0, false, st) : product<kPlain>(maps, p, ws, 0, false, st);
+    return gated ? product<kGated>(maps, p, ws, st) : product<kPlain>(maps, p, ws, st);
 }
 
 cudaError_t launch_expert_product_backward(const uint16_t *d_y, const uint16_t *a, int a_rows,
@@ -1064,8 +1143,7 @@ cudaError_t launch_expert_product_backward(const uint16_t *d_y, const uint16_t *
         return d_w ? cudaMemsetAsync(d_w, 0, (size_t)E * N * K * (d_w_type == MOE_TYPE_F32 ? 4 : 2), st)
                    : cudaSuccess;
     const Args p{offsets, counts, block_rows, a_rows, E, N, K, K, N, (__nv_bfloat16 *)d_a, nullptr,
-                 (const __nv_bfloat16 *)pre, d_w, d_w_type == MOE_TYPE_F32, nullptr, nullptr, false, 0, 0,
-                 dev_status};
+                 (const __nv_bfloat16 *)pre, d_w, d_w_type == MOE_TYPE_F32, nullptr, nullptr, dev_status};
     Maps maps = {}, maps_w = {};
     cudaError_t err = cudaSuccess;
     if (d_a) {
@@ -1081,22 +1159,13 @@ cudaError_t launch_expert_product_backward(const uint16_t *d_y, const uint16_t *
         if (err == cudaSuccess) err = encode(&maps_w.d, d);
     }
     if (err != cudaSuccess) return err;
-    const bool cut_a = d_a && may_cut(N), cut_w = d_w && may_cut(a_rows);
-    if (d_a && d_w && !cut_a && !cut_w) {
-        int ctas;
-        err = grid_of(&ctas);
-        if (err != cudaSuccess) return err;
-        const int64_t tiles_n = (N + kTileRows - 1) / kTileRows, tiles_k = (K + kTileRows - 1) / kTileRows;
-        const int64_t most_a = tiles_k * (a_rows / kTileRows + (a_rows < E ? a_rows : E));
-        if (most_a + E * tiles_n * tiles_k <= ctas / 2)
-            return pre ? gradients<kGateGrad>(maps, p, maps_w, p, (int)most_a, ctas, st)
-                       : gradients<kRowGrad>(maps, p, maps_w, p, (int)most_a, ctas, st);
-    }
-    if (cut_a || cut_w) err = begin(ws, st);
-    if (err == cudaSuccess && d_a)
-        err = pre ? product<kGateGrad>(maps, p, ws, 0, false, st) : product<kRowGrad>(maps, p, ws, 0, false, st);
-    if (err == cudaSuccess && d_w) err = product<kWeightGrad>(maps_w, p, ws, 1, d_a != nullptr, st);
-    return err;
+    if ((d_a && may_cut(N)) || (d_w && may_cut(a_rows))) err = begin(ws, st);
+    if (err != cudaSuccess) return err;
+    if (d_a && d_w)
+        return pre ? gradients<kGateGrad>(maps, p, maps_w, ws, st) : gradients<kRowGrad>(maps, p, maps_w, ws, st);
+    if (d_w) return product<kWeightGrad>(maps_w, p, ws, st);
+    if (!d_a) return cudaSuccess;
+    return pre ? product<kGateGrad>(maps, p, ws, st) : product<kRowGrad>(maps, p, ws, st);
 }
 
 }  // namespace moe

@@ -30,16 +30,15 @@ namespace moe {
 
 namespace {
 
-constexpr int kRowsThreads = 256;       // CTA of one-warp teams
+constexpr int kRowsWarps = 8;           // warps of a CTA that several teams share
 constexpr int kMaxParts = 640;          // CTAs of the backward pass, and parts of d_w
 
 // A row is shared by a team of WARPS warps, each thread with NV vectors of 8 values:
-// vector i of thread t is columns 8 (t + i * 32 WARPS) on.  Teams of one warp share a
-// CTA of kRowsThreads, larger ones have their own.
+// vector i of thread t is columns 8 (t + i * 32 WARPS) on.  Small teams share a CTA.
 template <int WARPS>
-constexpr int kTeams = WARPS == 1 ? kRowsThreads / 32 : 1;
+constexpr int kTeams = WARPS < kRowsWarps ? kRowsWarps / WARPS : 1;
 template <int WARPS>
-constexpr int kThreads = WARPS == 1 ? kRowsThreads : 32 * WARPS;
+constexpr int kThreads = 32 * WARPS * kTeams<WARPS>;
 
 __device__ __forceinline__ void unpack8(int4 v, float (&f)[8])
 {
@@ -132,14 +131,22 @@ __device__ __forceinline__ void team_sum(float (&v)[COUNT], int turn)
 #pragma unroll
     for (int c = 0; c < COUNT; c++) v[c] = warp_sum(v[c]);
     if constexpr (WARPS > 1) {
-        __shared__ float part[2][COUNT][WARPS];
-        const int lane = threadIdx.x & 31;
+        __shared__ float part[2][COUNT][kTeams<WARPS>][WARPS];
+        const int lane = threadIdx.x & 31, team = threadIdx.x / (32 * WARPS), warp = threadIdx.x / 32 % WARPS;
 #pragma unroll
         for (int c = 0; c < COUNT; c++)
-            if (lane == 0) part[turn][c][threadIdx.x >> 5] = v[c];
-        __syncthreads();
+            if (lane == 0) part[turn][c][team][warp] = v[c];
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * WARPS) : "memory");
 #pragma unroll
-        for (int c = 0; c < COUNT; c++) v[c] = warp_sum(lane < WARPS ? part[turn][c][lane] : 0.f);
+        for (int c = 0; c < COUNT; c++) {
+            if constexpr (WARPS <= 4) {
+                v[c] = part[turn][c][team][0];
+#pragma unroll
+                for (int w = 1; w < WARPS; w++) v[c] += part[turn][c][team][w];
+            } else {
+                v[c] = warp_sum(lane < WARPS ? part[turn][c][team][lane] : 0.f);
+            }
+        }
     }
 }
 
@@ -240,6 +247,9 @@ template <int NV, bool F32>
 constexpr int kRowSlots = NV * (F32 ? 5 : 3);          // 16 bytes of d_y, h and d_residual each
 template <int NV, int WARPS, bool F32, int AHEAD>
 constexpr size_t kRingBytes = (size_t)AHEAD * kRowSlots<NV, F32> * kThreads<WARPS> * 16;
+// After the last row the teams of a CTA add up their parts of d_w in the same memory.
+template <int NV, int WARPS>
+constexpr size_t kMergeBytes = kTeams<WARPS> > 1 ? (size_t)NV * 8 * kThreads<WARPS> * 4 : 0;
 
 __device__ __forceinline__ void copy_ahead(int4 *to, const int4 *from)
 {
@@ -356,19 +366,19 @@ __global__ void __launch_bounds__(kThreads<WARPS>) k_rms_norm_backward(const __g
     if (!p.parts) return;
     // the CTA's part of d_w: the teams' sums in their order
     if constexpr (kTeams<WARPS> > 1) {
-        __shared__ float own[kTeams<WARPS>][NV * 32 * 8];
-        const int team = threadIdx.x / kTeam;
+        float *const own = (float *)ring;
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < NV; i++)
 #pragma unroll
-            for (int j = 0; j < 8; j++) own[team][(i * 8 + j) * 32 + t] = acc[i][j];
+            for (int j = 0; j < 8; j++) own[(i * 8 + j) * kThreads<WARPS> + threadIdx.x] = acc[i][j];
         __syncthreads();
-        for (int at = threadIdx.x; at < NV * 32 * 8; at += kThreads<WARPS>) {
+        for (int at = threadIdx.x; at < NV * 8 * kTeam; at += kThreads<WARPS>) {
+            const int column = at / kTeam, u = at % kTeam, v = u + column / 8 * kTeam;
             float s = 0.f;
 #pragma unroll
-            for (int m = 0; m < kTeams<WARPS>; m++) s += own[m][at];
-            const int v = at % 32 + at / 256 * 32, j = at / 32 % 8;
-            if (v < p.V) p.parts[(int64_t)blockIdx.x * 8 * p.V + 8 * v + j] = s;
+            for (int m = 0; m < kTeams<WARPS>; m++) s += own[column * kThreads<WARPS> + m * kTeam + u];
+            if (v < p.V) p.parts[(int64_t)blockIdx.x * 8 * p.V + 8 * v + column % 8] = s;
         }
     } else {
 #pragma unroll
@@ -383,9 +393,9 @@ __global__ void __launch_bounds__(kThreads<WARPS>) k_rms_norm_backward(const __g
     }
 }
 
-// d_w[c] = the sum of column c over the parts: 32 columns a CTA, its 8 warps take the
+// d_w[c] = the sum of column c over the parts: 32 columns a CTA, its 32 warps take the
 // parts in turn, and their sums are added in order.
-constexpr int kSumThreads = 256;
+constexpr int kSumThreads = 1024;
 __global__ void __launch_bounds__(kSumThreads) k_sum_parts(const float *__restrict__ parts, int count, int H,
                                                            float *__restrict__ d_w)
 {
@@ -423,7 +433,8 @@ cudaError_t norm_backward(const NormBackArgs &p, float *d_w, cudaStream_t st)
     // three rows in the ring where two CTAs of them fit an SM, else two (116 us; 130 with two rows,
     // 182 straight into registers)
     constexpr int kAhead = kRingBytes<NV, WARPS, F32, 3> <= 110 * 1024 ? 3 : kRingBytes<NV, WARPS, F32, 2> <= 110 * 1024 ? 2 : 0;
-    constexpr size_t kSmem = kRingBytes<NV, WARPS, F32, kAhead>;
+    constexpr size_t kRing = kRingBytes<NV, WARPS, F32, kAhead>, kMerge = kMergeBytes<NV, WARPS>;
+    constexpr size_t kSmem = kRing > kMerge ? kRing : kMerge;
     const auto kernel = k_rms_norm_backward<NV, WARPS, F32, kAhead>;
     const int64_t want = (p.rows + kTeams<WARPS> - 1) / kTeams<WARPS>;
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
@@ -448,19 +459,22 @@ cudaError_t norm_backward(const NormBackArgs &p, float *d_w, cudaStream_t st)
 #define BY_WIDTH(V, CALL)              \
     if ((V) <= 32) return CALL(1, 1);  \
     if ((V) <= 64) return CALL(2, 1);  \
-    if ((V) <= 128) return CALL(4, 1); \
+    if ((V) <= 128) return CALL(2, 2); \
+    if ((V) <= 192) return CALL(3, 2); \
     if ((V) <= 256) return CALL(2, 4); \
     if ((V) <= 512) return CALL(4, 4); \
     if ((V) <= 640) return CALL(5, 4); \
     if ((V) <= 1024) return CALL(4, 8); \
     if ((V) <= 2048) return CALL(4, 16); \
     return CALL(4, 32)
+// Several small teams share a CTA: CTAs of 128 threads start too slowly for short rows (10,525 rows of
+// 1,320: 11.7 us, 14.4 with a CTA a row).
 // Backward: two vectors a thread where that holds the row, which leaves registers for twenty or
 // more warps an SM (16,384 rows of 5,120: 116 us with ten warps and two vectors, 187 with four and five).
 #define BY_WIDTH_BACK(V, CALL)          \
     if ((V) <= 32) return CALL(1, 1);   \
     if ((V) <= 64) return CALL(2, 1);   \
-    if ((V) <= 128) return CALL(1, 4);  \
+    if ((V) <= 128) return CALL(2, 2);  \
     if ((V) <= 256) return CALL(2, 4);  \
     if ((V) <= 512) return CALL(2, 8);  \
     if ((V) <= 640) return CALL(2, 10); \
