@@ -24,6 +24,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "gate.cuh"
 #include "launch.h"
@@ -56,6 +58,15 @@ constexpr int kCols = 16;                        // columns of D that a warp fin
 constexpr int kGroups = kFinishWarps / 4;        // warps that share the columns of 32 rows of D
 constexpr int kStaging = 4 * kCols * 32;         // bytes of shared memory a warp has for that
 
+// A tile, or a part of one, that a pair has.
+struct Segment {
+    int e, tile;                     // expert, tile of the A side
+    int row0, rows, cols;            // d_w: first column, columns in the matrix, columns of the MMA;
+                                     // else first row of the tile, its rows, and those rounded up
+    int c0, c1, steps;               // steps of the segment, of the whole tile
+    int unit;                        // first step of the tile
+};
+
 struct Shared {
     uint64_t full[kStages], empty[kStages], landed[kStages], cleared[kStages];
     uint64_t sums_full[2], sums_empty[2];
@@ -80,6 +91,7 @@ struct Args {
     const int32_t *offsets, *counts;
     int block_rows, a_rows, E, N, K;
     int rows_a, sums;                // rows of the A side (outputs of a row), length of the sum
+    int most;                        // rows of a tile of the B side: 256, 128 or 64
     __nv_bfloat16 *out, *keep;
     const __nv_bfloat16 *pre;
     void *d_w;
@@ -89,8 +101,9 @@ struct Args {
     uint32_t *dev_status;
 };
 
-// Rows of an expert in units of 32, their tiles of at most 8 units, and where tile i starts.
-__device__ __forceinline__ int row_tiles(int count) { return (int)(((unsigned)count + kTileRows - 1) / kTileRows); }
+// Rows of an expert in tiles of at most `most` (a multiple of 32), and where tile i starts: their units of
+// 32 in equal parts.
+__device__ __forceinline__ int row_tiles(int count, int most) { return (int)(((unsigned)count + most - 1) / most); }
 __device__ __forceinline__ int tile_start(int count, int tiles, int i)
 {
     return (int)((int64_t)i * (((unsigned)count + 31) / 32) / tiles) * 32;
@@ -106,7 +119,7 @@ template <int FORM>
 __device__ __forceinline__ Shape shape_of(const Args &p)
 {
     if (FORM == kWeightGrad)
-        return {p.E, (p.N + kTileRows - 1) / kTileRows, 0, (p.K + kTileRows - 1) / kTileRows};
+        return {p.E, (p.N + kTileRows - 1) / kTileRows, 0, (p.K + p.most - 1) / p.most};
     return {p.E, (p.rows_a + kTileRows - 1) / kTileRows, (p.sums + kStep - 1) / kStep, 0};
 }
 // (an expert without rows has one step, of nothing but the zeros of its gradient)
@@ -116,14 +129,6 @@ __device__ __forceinline__ int steps_of(const Shape &w, int count)
 }
 
 // The steps of this pair, one tile after the other; for whole warps.
-struct Segment {
-    int e, tile;                     // expert, tile of the A side
-    int row0, rows, cols;            // d_w: first column, columns in the matrix, columns of the MMA;
-                                     // else first row of the tile, its rows, and those rounded up
-    int c0, c1, steps;               // steps of the segment, of the whole tile
-    int unit;                        // first step of the tile
-};
-
 template <int FORM>
 struct Walk {
     const Shared &sh;
@@ -182,10 +187,10 @@ struct Walk {
         }
         if constexpr (FORM == kWeightGrad) {
             g.tile = task / w.tiles_b;
-            g.row0 = (task - g.tile * w.tiles_b) * kTileRows;
-            g.rows = min(kTileRows, p.K - g.row0);
+            g.row0 = (task - g.tile * w.tiles_b) * p.most;
+            g.rows = min(p.most, p.K - g.row0);
         } else {
-            const int nt = row_tiles(count);
+            const int nt = row_tiles(count, p.most);
             g.tile = task / nt;
             const int i = task - g.tile * nt;
             g.row0 = tile_start(count, nt, i);
@@ -231,7 +236,7 @@ __device__ __forceinline__ void scan_experts(Shared &sh, const Args &p, const Sh
             const unsigned fall = __ballot_sync(kFull, falls[i]);
             if (fell || (fall & (lanemask_lt() | 1u << lane))) count[i] = 0;
             fell = fell || fall;
-            const int n = e >= p.E ? 0 : FORM == kWeightGrad ? w.tiles * w.tiles_b : w.tiles * row_tiles(count[i]);
+            const int n = e >= p.E ? 0 : FORM == kWeightGrad ? w.tiles * w.tiles_b : w.tiles * row_tiles(count[i], p.most);
             const int units = n * steps_of(w, count[i]);
             longest = max(longest, e < p.E ? steps_of(w, count[i]) : 0);
             widest = max(widest, count[i]);
@@ -247,7 +252,7 @@ __device__ __forceinline__ void scan_experts(Shared &sh, const Args &p, const Sh
     }
     tasks = __reduce_add_sync(kFull, tasks);
     longest = __reduce_max_sync(kFull, longest);
-    widest = FORM == kWeightGrad ? kTileRows : __reduce_max_sync(kFull, widest);
+    widest = FORM == kWeightGrad ? p.most : min(p.most, __reduce_max_sync(kFull, widest));
     __syncwarp();
     if (lane == 0) {
         sh.before[p.E] = before;
@@ -471,8 +476,9 @@ __device__ __forceinline__ void issue_steps(Shared &sh, uint8_t *ring, const Arg
 // ---------------------------------------------------------------- the end of a tile
 
 struct Finish {
-    const float *from;         // parts of a cut tile: at this thread's place in the first one
-    int parts, here;           // how many, and which of them this CTA holds and has not stored (-1: none)
+    int first, parts;          // parts of a cut tile: the pair that has the first one, how many
+    int here;                  // which of them this CTA holds and has not stored (-1: none)
+    const float *from;         // this thread's place in the first one
 };
 
 // A part's sums: a block of 16 columns is 4 x 128 threads x 4 values, so that a thread moves
@@ -482,6 +488,10 @@ __device__ __forceinline__ void store_part(float *part, int c0, const float (&v)
 #pragma unroll
     for (int j = 0; j < kCols; j += 4)
         __stcg((float4 *)(part + (c0 + j) * 128), make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
+}
+__device__ __forceinline__ const float *parts_from(const Shared &sh, const Args &p, const Finish &f)
+{
+    return p.partial + (int64_t)(4 * (sh.first_pair + f.first) + 2 * cluster_rank()) * kPart + (threadIdx.x & 127) * 4;
 }
 __device__ __forceinline__ void load_part(const Finish &f, int q, int c0, float (&v)[kCols])
 {
@@ -515,27 +525,42 @@ __device__ __forceinline__ void add_parts(const Finish &f, int c0, float (&v)[kC
     for (int j = 0; j < kCols; j++) v[j] = sum[j];
 }
 
-// By all of the CTA's finishing warps: where this segment is part of a cut tile, whether they are to
-// finish it, which falls to the part that is done last.  Any other goes to memory by
-// `store(slot)`; EARLY: the last one does not, where that is known before.
-template <bool EARLY, typename Store>
-__device__ __forceinline__ bool join_parts(Shared &sh, const Args &p, const Segment &g, Finish &f, Store store)
+// The same with all parts in memory.
+__device__ __forceinline__ void read_parts(const Finish &f, int c0, float (&v)[kCols])
 {
-    const int row = threadIdx.x & 127;      // of D; the same for the warps that share its columns
-    const uint32_t rank = cluster_rank();
+#pragma unroll
+    for (int j = 0; j < kCols; j++) v[j] = 0.f;
+#pragma unroll 1
+    for (int q = 0; q < f.parts; q++) {
+        float x[kCols];
+        load_part(f, q, c0, x);
+#pragma unroll
+        for (int j = 0; j < kCols; j++) v[j] += x[j];
+    }
+}
+
+// Where this segment is part of a cut tile: its parts.
+__device__ __forceinline__ void find_parts(const Shared &sh, const Segment &g, Finish &f)
+{
     f.parts = 1;
-    if (g.c1 - g.c0 == g.steps) return true;
-    const int from = owner_of(sh, g.unit);
-    f.parts = owner_of(sh, g.unit + g.steps - 1) - from + 1;
-    f.here = (int)(blockIdx.x / 2) - sh.first_pair - from;
-    f.from = p.partial + (int64_t)(4 * (sh.first_pair + from) + 2 * rank) * kPart + row * 4;
-    int32_t *const count = p.arrivals + 2 * from + rank;
-    if (EARLY && named_all(1, kFinishWarps * 32, arrived(count) == f.parts - 1)) return true;
+    if (g.c1 - g.c0 == g.steps) return;
+    f.first = owner_of(sh, g.unit);
+    f.parts = owner_of(sh, g.unit + g.steps - 1) - f.first + 1;
+    f.here = (int)(blockIdx.x / 2) - sh.first_pair - f.first;
+}
+
+// By all of the CTA's finishing warps: whether they are to finish the tile, which falls to the part that
+// is done last (`early`: all others had arrived before).  Any other goes to memory by `store(slot)`.
+template <typename Store>
+__device__ __forceinline__ bool join_parts(Shared &sh, const Args &p, const Segment &g, Finish &f, bool early, Store store)
+{
+    if (f.parts == 1 || early) return true;
     f.here = -1;
-    store(p.partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * kPart + row * 4);
+    // (the thread's place among the 128 of a row block is the same for the warps that share its columns)
+    store(p.partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * kPart + (threadIdx.x & 127) * 4);
     __threadfence();
     named_barrier(1, kFinishWarps * 32);
-    if (threadIdx.x == 0) sh.last = atomicAdd(count, 1) == f.parts - 1;
+    if (threadIdx.x == 0) sh.last = atomicAdd(p.arrivals + 2 * f.first + cluster_rank(), 1) == f.parts - 1;
     named_barrier(1, kFinishWarps * 32);
     const bool last = sh.last;
     __threadfence();
@@ -700,12 +725,15 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
         const int64_t first = sh.start[g.e] + g.row0;
         int4 gates[4];
         if constexpr (FORM == kGateGrad) load_gates(p, first + group * kCols, g.rows - group * kCols, a_row, gates);
+        Finish f;
+        find_parts(sh, g, f);
+        const bool others = f.parts > 1 && arrived(p.arrivals + 2 * f.first + rank) == f.parts - 1;
         const bool ok = mbar_wait_cluster(&sh.sums_full[d], phase, &sh.dead);
         if (!named_all(1, kFinishWarps * 32, ok)) break;
+        const bool early = f.parts > 1 && named_all(1, kFinishWarps * 32, others);
         tmem_fence_after();
         const uint32_t sums = sh.tmem + ((uint32_t)(quarter * 32) << 16) + d * kTileRows;
-        Finish f;
-        const bool finish = join_parts<true>(sh, p, g, f, [&](float *slot) {
+        const bool finish = join_parts(sh, p, g, f, early, [&](float *slot) {
             for (int c0 = group * kCols; c0 < g.rows; c0 += kTurn) {
                 float v[kCols];
                 tmem_load_matrices(sums + c0, v);
@@ -713,6 +741,7 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
             }
         });
         if (finish) {
+            f.from = parts_from(sh, p, f);
             // the other part of a tile in two is loaded a block of columns ahead
             const bool two = f.parts == 2 && f.here >= 0;
             float other[kCols] = {}, ahead[kCols] = {};
@@ -726,7 +755,7 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
 #pragma unroll
                     for (int j = 0; j < kCols; j++) v[j] += other[j];       // (the same in either order)
                 } else if (f.parts > 1) {
-                    add_parts<2>(f, c0, v);
+                    add_parts<FORM == kGateGrad ? 1 : 4>(f, c0, v);
                 }
 #pragma unroll
                 for (int j = 0; j < kCols; j++) other[j] = ahead[j];
@@ -765,16 +794,16 @@ __device__ __forceinline__ void finish_weights(Shared &sh, uint8_t *staging, con
     // block b of this warp: 32 columns by the groups in turn
     auto column = [&](int b) { return ((b >> 1) * kGroups + group) * 32 + (b & 1) * kCols; };
     while (walk.next(g)) {
-        const int a_row = g.tile * kTileRows + rank * 128 + quarter * 32;    // the warp's first row of A
         float sum[kBlocks][kCols] = {};
         bool ok = true;
-        for (int c = sh.count[g.e] ? g.c0 : g.c1; ok && c < g.c1; c += kSumSteps) {
+        const int to = g.c1, cols = g.cols;
+        for (int c = sh.count[g.e] ? g.c0 : to; ok && c < to; c += kSumSteps) {
             if (!(ok = mbar_wait_cluster(&sh.sums_full[d], phase, &sh.dead))) break;
             tmem_fence_after();
             const uint32_t sums = sh.tmem + ((uint32_t)(quarter * 32) << 16) + d * kTileRows;
 #pragma unroll
             for (int b = 0; b < kBlocks; b++)
-                if (column(b) < g.cols) {
+                if (column(b) < cols) {
                     float v[kCols];
                     tmem_load(sums + column(b), v);
 #pragma unroll
@@ -787,19 +816,22 @@ __device__ __forceinline__ void finish_weights(Shared &sh, uint8_t *staging, con
             if (d == 0) phase ^= 1;
         }
         if (!named_all(1, kFinishWarps * 32, ok)) break;
+        const int a_row = g.tile * kTileRows + rank * 128 + quarter * 32;    // the warp's first row of A
         Finish f;
-        const bool finish = join_parts<false>(sh, p, g, f, [&](float *slot) {
+        find_parts(sh, g, f);
+        const bool finish = join_parts(sh, p, g, f, false, [&](float *slot) {
 #pragma unroll
             for (int b = 0; b < kBlocks; b++)
                 if (column(b) < g.cols) store_part(slot, column(b), sum[b]);
         });
         if (!finish || a_row >= p.N) continue;
+        if (f.parts > 1) f.from = parts_from(sh, p, f);
 #pragma unroll
         for (int b = 0; b < kBlocks; b += 2) {
             if (column(b) >= g.rows) break;
             if (f.parts > 1)
 #pragma unroll
-                for (int i = 0; i < 2; i++) add_parts<1>(f, column(b + i), sum[b + i]);    // (all from memory)
+                for (int i = 0; i < 2; i++) read_parts(f, column(b + i), sum[b + i]);
             uint32_t words[16];
             if (p.d_w_f32) {
 #pragma unroll
@@ -919,16 +951,16 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 // Pairs for the rows' gradient where both gradients are taken at once, by what they take: their steps,
 // and those that the end of a tile is worth by what it reads and writes.  By one warp, the same in
 // every CTA.  (Counting the turns of each side for every split took longer than it won.)
-__device__ __forceinline__ int split_pairs(const Args &p)
+__device__ __forceinline__ int split_pairs(const Args &p, const Args &p_w)
 {
     const int rows_end = p.pre ? 8 : 6, weights_end = p.d_w_f32 ? 8 : 6;
-    const Shape a = shape_of<kRowGrad>(p), w = shape_of<kWeightGrad>(p);
+    const Shape a = shape_of<kRowGrad>(p), w = shape_of<kWeightGrad>(p_w);
     int tiles = 0, steps = 0;
     bool bad = false;
     for (int e = threadIdx.x & 31; e < p.E; e += 32) {
         int start, count;
         expert_rows(p.offsets, p.counts, p.block_rows, p.a_rows, e, start, count, bad);
-        tiles += row_tiles(count);
+        tiles += row_tiles(count, p.most);
         steps += steps_of(w, count) + weights_end;
     }
     const float rows = (float)__reduce_add_sync(kFull, tiles) * (float)(a.tiles * (a.steps + rows_end));
@@ -950,7 +982,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
     start(m.sh, warp);
     if (warp == kWarpLoad) {
-        const int split = split_pairs(p);
+        const int split = split_pairs(p, p_w);
         const bool weights = (int)blockIdx.x / 2 >= split;
         if ((threadIdx.x & 31) == 0) {
             m.sh.first_pair = weights ? split : 0;
@@ -1067,15 +1099,36 @@ cudaError_t grid_of(int *ctas)
     return cudaSuccess;
 }
 
-template <int FORM>
-cudaError_t product(const Maps &maps, Args p, void *ws, cudaStream_t st)
+// Rows of a tile of the B side: half, or a quarter, of 256 where the tiles are few for the pairs all the
+// same (2,571 rows of 376 x 1,856: 16.5 us with 256, 13.2 with 128).
+int tile_rows(int pairs, int64_t tiles_a, int64_t rows, int64_t experts)
 {
-    int ctas;
-    cudaError_t err = grid_of(&ctas);
+    int most = kTileRows;
+    while (most > 64 && tiles_a * (2 * rows / most + experts) <= pairs) most /= 2;
+    return most;
+}
+
+// The shared memory of a kernel, allowed once per device (a bit of `done` each).
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
+    const uint64_t bit = (uint64_t)1 << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (err == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return err;
+}
+
+template <int FORM>
+cudaError_t product(const Maps &maps, Args p, int ctas, void *ws, cudaStream_t st)
+{
     p.partial = (float *)ws;
     p.arrivals = (int32_t *)((uint8_t *)ws + kPartialBytes);
-    err = cudaFuncSetAttribute(k_expert_product<FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t err = allow_smem(k_expert_product<FORM>, allowed);
     if (err != cudaSuccess) return err;
     MOE_TRACED_LAUNCH("k_expert_product", st,
         err = launch_pdl_cluster(k_expert_product<FORM>, dim3(ctas), dim3(kMmThreads), kSmem, 2, st, maps, p));
@@ -1083,16 +1136,13 @@ cudaError_t product(const Maps &maps, Args p, void *ws, cudaStream_t st)
 }
 
 template <int FORM>
-cudaError_t gradients(const Maps &maps, Args p, const Maps &maps_w, void *ws, cudaStream_t st)
+cudaError_t gradients(const Maps &maps, Args p, const Maps &maps_w, Args p_w, int ctas, void *ws, cudaStream_t st)
 {
-    int ctas;
-    cudaError_t err = grid_of(&ctas);
-    if (err != cudaSuccess) return err;
-    p.partial = (float *)ws;
+    p.partial = p_w.partial = (float *)ws;
     p.arrivals = (int32_t *)((uint8_t *)ws + kPartialBytes);
-    Args p_w = p;
-    p_w.arrivals += kMaxCtas;
-    err = cudaFuncSetAttribute(k_expert_gradients<FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    p_w.arrivals = p.arrivals + kMaxCtas;
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t err = allow_smem(k_expert_gradients<FORM>, allowed);
     if (err != cudaSuccess) return err;
     MOE_TRACED_LAUNCH("k_expert_gradients", st,
         err = launch_pdl_cluster(k_expert_gradients<FORM>, dim3(ctas), dim3(kMmThreads), kSmem, 2, st, maps, p, maps_w, p_w));
@@ -1102,12 +1152,14 @@ cudaError_t gradients(const Maps &maps, Args p, const Maps &maps_w, void *ws, cu
 // Whether tiles of a sum of this length may be cut (scan_experts), so that the counters are needed.
 bool may_cut(int sums) { return (sums + kStep - 1) / kStep > kCutSteps; }
 
-// The maps of the rows in boxes of 16, 64 and 128.
-cudaError_t row_boxes(Maps &maps, const void *rows, int64_t a_rows, int64_t width)
+// The maps of the rows in boxes of 16, 64 and 128, those that tiles of at most `most` rows use.
+cudaError_t row_boxes(Maps &maps, const void *rows, int64_t a_rows, int64_t width, int most)
 {
     const uint32_t box[3] = {16, 64, 128};
-    cudaError_t err = cudaSuccess;
-    for (int i = 0; i < 3 && err == cudaSuccess; i++) err = encode(&maps.b[i], rows_map(rows, a_rows, width, box[i]));
+    const int64_t half = (a_rows < most ? (a_rows + 31) / 32 * 32 : most) / 2;
+    cudaError_t err = encode(&maps.b[0], rows_map(rows, a_rows, width, box[0]));
+    for (int i = 1; i < 3 && err == cudaSuccess && half > box[i] / 2; i++)
+        err = encode(&maps.b[i], rows_map(rows, a_rows, width, box[i]));
     return err;
 }
 
@@ -1121,15 +1173,20 @@ cudaError_t launch_expert_product(const uint16_t *a, int a_rows, const int32_t *
                                   uint32_t *dev_status, cudaStream_t st)
 {
     if (a_rows == 0) return cudaSuccess;
-    Maps maps = {};
-    cudaError_t err = encode(&maps.a, gated ? gated_map(w, E, N, K) : weights_map(w, E, N, K, 128));
-    if (err == cudaSuccess) err = row_boxes(maps, a, a_rows, K);
+    int ctas;
+    cudaError_t err = grid_of(&ctas);
     if (err != cudaSuccess) return err;
-    const Args p{offsets, counts, block_rows, a_rows, E, N, K, gated ? 2 * N : N, K, (__nv_bfloat16 *)y,
+    const int rows_w = gated ? 2 * N : N;
+    const int most = tile_rows(ctas / 2, (rows_w + kTileRows - 1) / kTileRows, a_rows, a_rows < E ? a_rows : E);
+    Maps maps = {};
+    err = encode(&maps.a, gated ? gated_map(w, E, N, K) : weights_map(w, E, N, K, 128));
+    if (err == cudaSuccess) err = row_boxes(maps, a, a_rows, K, most);
+    if (err != cudaSuccess) return err;
+    const Args p{offsets, counts, block_rows, a_rows, E, N, K, rows_w, K, most, (__nv_bfloat16 *)y,
                  (__nv_bfloat16 *)pre, nullptr, nullptr, false, nullptr, nullptr, dev_status};
     if (may_cut(K)) err = begin(ws, st);
     if (err != cudaSuccess) return err;
-    return gated ? product<kGated>(maps, p, ws, st) : product<kPlain>(maps, p, ws, st);
+    return gated ? product<kGated>(maps, p, ctas, ws, st) : product<kPlain>(maps, p, ctas, ws, st);
 }
 
 cudaError_t launch_expert_product_backward(const uint16_t *d_y, const uint16_t *a, int a_rows,
@@ -1142,13 +1199,20 @@ cudaError_t launch_expert_product_backward(const uint16_t *d_y, const uint16_t *
     if (a_rows == 0)        // no rows: the weights' gradient is zero
         return d_w ? cudaMemsetAsync(d_w, 0, (size_t)E * N * K * (d_w_type == MOE_TYPE_F32 ? 4 : 2), st)
                    : cudaSuccess;
-    const Args p{offsets, counts, block_rows, a_rows, E, N, K, K, N, (__nv_bfloat16 *)d_a, nullptr,
-                 (const __nv_bfloat16 *)pre, d_w, d_w_type == MOE_TYPE_F32, nullptr, nullptr, dev_status};
+    int ctas;
+    cudaError_t err = grid_of(&ctas);
+    if (err != cudaSuccess) return err;
+    const int pairs = d_a && d_w ? ctas / 4 : ctas / 2;
+    const int64_t tiles_n = (N + kTileRows - 1) / kTileRows, tiles_k = (K + kTileRows - 1) / kTileRows;
+    Args p{offsets, counts, block_rows, a_rows, E, N, K, K, N, tile_rows(pairs, tiles_k, a_rows, a_rows < E ? a_rows : E),
+           (__nv_bfloat16 *)d_a, nullptr, (const __nv_bfloat16 *)pre, d_w, d_w_type == MOE_TYPE_F32, nullptr, nullptr,
+           dev_status};
+    Args p_w = p;
+    p_w.most = tile_rows(pairs, E * tiles_n, K, 1);
     Maps maps = {}, maps_w = {};
-    cudaError_t err = cudaSuccess;
     if (d_a) {
         err = encode(&maps.a, weights_map(w, E, N, K, 64));
-        if (err == cudaSuccess) err = row_boxes(maps, d_y, a_rows, N);
+        if (err == cudaSuccess) err = row_boxes(maps, d_y, a_rows, N, p.most);
     }
     if (err == cudaSuccess && d_w) {
         err = encode(&maps_w.a, rows_map(d_y, a_rows, N, 64));
@@ -1162,10 +1226,11 @@ cudaError_t launch_expert_product_backward(const uint16_t *d_y, const uint16_t *
     if ((d_a && may_cut(N)) || (d_w && may_cut(a_rows))) err = begin(ws, st);
     if (err != cudaSuccess) return err;
     if (d_a && d_w)
-        return pre ? gradients<kGateGrad>(maps, p, maps_w, ws, st) : gradients<kRowGrad>(maps, p, maps_w, ws, st);
-    if (d_w) return product<kWeightGrad>(maps_w, p, ws, st);
+        return pre ? gradients<kGateGrad>(maps, p, maps_w, p_w, ctas, ws, st)
+                   : gradients<kRowGrad>(maps, p, maps_w, p_w, ctas, ws, st);
+    if (d_w) return product<kWeightGrad>(maps_w, p_w, ctas, ws, st);
     if (!d_a) return cudaSuccess;
-    return pre ? product<kGateGrad>(maps, p, ws, st) : product<kRowGrad>(maps, p, ws, st);
+    return pre ? product<kGateGrad>(maps, p, ctas, ws, st) : product<kRowGrad>(maps, p, ctas, ws, st);
 }
 
 }  // namespace moe
