@@ -1286,6 +1286,22 @@ class MoePath:
         moe_combine_stage2(self.ret, self.token_slot, self.out, self.dev_status, stream,
                                recv_part=self.recv_part)
 
+    def dispatch_records(self, logits, record, stream=None):
+        """dispatch_fused for rows that are MXFP8 records already, record uint8 [S,T,H+H/32] as
+        moe_rms_norm writes them: quantized once per token, then moved.  For quant="mxfp8" paths;
+        recv holds what dispatch_fused makes of the rows in bf16."""
+        if self.quant != "mxfp8" or self.placement is not None:
+            raise ValueError("dispatch_records needs quant='mxfp8' and no placement")
+        if tuple(record.shape) != (self.S, self.T, self.row_bytes):
+            raise ValueError(f"record must be [{self.S}, {self.T}, {self.row_bytes}] uint8")
+        _dev(record, "record", (torch.uint8,), 3)
+        rows = torch.bfloat16
+        moe_dispatch(logits, record.view(rows), self.E, self.P, self.recv_part, self.align,
+                     self.topk_ids, self.topk_w, self.expert_counts, self.expert_rank,
+                     self.part_counts, self.part_offsets, self.token_slot, self.send.view(rows),
+                     self.send_src, self.recv.view(rows), self.expert_offsets, self.pair_row,
+                     self.recv_pair, self.ws, self.dev_status, stream)
+
     def dispatch_fused(self, logits, x, stream=None):
         """route + layout + pack + permute through one moe_dispatch (with quantized
         rows moe_dispatch_quantized, with the masked layout moe_dispatch_masked) call."""

@@ -5,7 +5,9 @@
 `ServedLayer` routes and dispatches a batch, multiplies every expert's rows by its 4-bit weights
 (gate and up with silu, then down) and combines: four calls, all of which a CUDA graph can hold.
 `TrainedLayer` computes the layer with per-expert scales in the experts' place, the router's
-balance and z loss, and the gradients of rows, experts and router logits.
+balance and z loss, and the gradients of rows, experts and router logits.  `TrainedBlock` is a whole
+block of a model that trains: residual addition and RMS norm, router, experts with bf16 weights,
+combine, and the gradients of its inputs and of all its weights.
 """
 import math
 import os
@@ -118,6 +120,62 @@ class TrainedLayer:
         return self.d_x, self.d_logits
 
 
+class TrainedBlock:
+    """h = x + residual, out = experts(norm(h)) by the router's picks; the block's outputs are out and h.
+
+    norm [H], router [E, H], gate_up [E, 2F, H] and down [E, H, F] are its weights, the last three bf16.
+    """
+
+    def __init__(self, T, H, F, E, k, P, norm, router, gate_up, down):
+        f32, bf16, u8 = (dict(dtype=d, device="cuda") for d in (torch.float32, torch.bfloat16, torch.uint8))
+        self.norm, self.router, self.gate_up, self.down = norm, router, gate_up, down
+        self.path = moe.MoePath(1, T, H, E, k, P)
+        rows = self.path.cap_recv
+        self.h, self.normed, self.d_x, self.d_normed = (torch.empty((1, T, H), **bf16) for _ in range(4))
+        self.pre, self.d_pre = (torch.empty((rows, 2 * F), **bf16) for _ in range(2))
+        self.act = torch.empty((rows, F), **bf16)
+        self.y, self.d_y, self.d_recv = (torch.empty((rows, H), **bf16) for _ in range(3))
+        self.d_w, self.ones = torch.empty((1, T, k), **f32), torch.ones((1, T, k), **f32)
+        self.d_logits = torch.empty((1, T, E), **f32)
+        self.d_gate_up, self.d_down = torch.empty(gate_up.shape, **f32), torch.empty(down.shape, **f32)
+        self.d_norm = torch.empty(norm.shape, **f32)
+        self.ws = torch.empty(max(moe.moe_expert_product_workspace_bytes(rows, E, F, H, True),
+                                  moe.moe_expert_product_workspace_bytes(rows, E, H, F),
+                                  moe.moe_expert_product_backward_workspace_bytes(rows, E, 2 * F, H),
+                                  moe.moe_expert_product_backward_workspace_bytes(rows, E, H, F),
+                                  moe.moe_rms_norm_backward_workspace_bytes(T, H)), **u8)
+
+    def forward(self, x, residual):
+        p = self.path
+        moe.moe_rms_norm(x, self.norm, y=self.normed, residual=residual, residual_out=self.h)
+        p.dispatch_fused((self.normed @ self.router.t()).float(), self.normed)
+        by = dict(expert_offsets=p.expert_offsets, dev_status=p.dev_status)
+        moe.moe_expert_product(p.recv, self.gate_up, self.act, self.ws, gated=True, pre=self.pre, **by)
+        moe.moe_expert_product(self.act, self.down, self.y, self.ws, **by)
+        p.combine(self.y)
+        return p.out, self.h
+
+    def backward(self, d_out, d_h):
+        """Gradients of x and residual (the same) and of norm, router, gate_up and down."""
+        p = self.path
+        by = dict(expert_offsets=p.expert_offsets, dev_status=p.dev_status)
+        moe.moe_combine_backward(d_out, self.y, p.pair_row, p.topk_w, self.d_y, self.d_w,
+                                 recv_pair=p.recv_pair, dev_status=p.dev_status)
+        moe.moe_expert_product_backward(self.d_y, self.act, self.down, self.ws, d_a=self.d_pre,
+                                        d_w=self.d_down, pre=self.pre, **by)
+        moe.moe_expert_product_backward(self.d_pre, p.recv, self.gate_up, self.ws, d_a=self.d_recv,
+                                        d_w=self.d_gate_up, **by)
+        moe.moe_combine(self.d_recv, p.pair_row, self.ones, self.d_normed, p.dev_status)
+        moe.moe_route_backward(None, p.topk_ids, p.topk_w, self.d_w, None, None, None, None,
+                               self.d_logits, dev_status=p.dev_status)
+        d_logits = self.d_logits[0].bfloat16()
+        d_router = d_logits.t() @ self.normed[0]
+        d_normed = self.d_normed + (d_logits @ self.router).unsqueeze(0)
+        moe.moe_rms_norm_backward(d_normed, self.h, self.norm, self.d_x, self.ws, d_weight=self.d_norm,
+                                  d_residual=d_h)
+        return self.d_x, self.d_norm, d_router, self.d_gate_up, self.d_down
+
+
 def relative(got, want):
     return float((got.double() - want.double()).norm() / want.double().norm())
 
@@ -165,7 +223,38 @@ def check_trained(S=2, T=96, H=256, E=16, k=3, P=4):
             "d_x": relative(d_x, x64.grad), "d_logits": relative(d_logits, l64.grad)}
 
 
+def check_block(T=200, H=512, F=264, E=16, k=3, P=4):
+    g = torch.Generator(device="cuda").manual_seed(3)
+    randn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, residual, d_out, d_h = (randn(1, T, H).bfloat16() for _ in range(4))
+    weights = [1 + 0.2 * randn(H)] + [(randn(*s) / math.sqrt(s[-1])).bfloat16()
+                                      for s in ((E, H), (E, 2 * F, H), (E, H, F))]
+    block = TrainedBlock(T, H, F, E, k, P, *weights)
+    out, h = block.forward(x, residual)
+    grads = block.backward(d_out, d_h)
+    # the same by automatic differentiation in 64 bits, for the picks that were made
+    ids = block.path.topk_ids[0].long()
+    x64, r64, *w64 = (t.double().requires_grad_() for t in (x[0], residual[0], *weights))
+    norm, router, gate_up, down = w64
+    h64 = x64 + r64
+    y64 = h64 / (h64.square().mean(-1, keepdim=True) + 1e-6).sqrt() * norm
+    w = torch.softmax((y64 @ router.t()).gather(1, ids), -1)
+    want = torch.zeros_like(y64)
+    for e in range(E):
+        t, j = torch.nonzero(ids == e, as_tuple=True)
+        gate, up = (y64[t] @ gate_up[e].t()).chunk(2, -1)
+        want = want.index_add(0, t, w[t, j, None] * ((torch.nn.functional.silu(gate) * up) @ down[e].t()))
+    ((want * d_out[0].double()).sum() + (h64 * d_h[0].double()).sum()).backward()
+    assert int(block.path.dev_status.item()) == 0
+    errors = {"out": relative(out[0], want.detach()), "h": relative(h[0], h64.detach()),
+              "d_x": relative(grads[0][0], x64.grad)}
+    errors.update({f"d_{name}": relative(got, leaf.grad) for name, got, leaf in
+                   zip(("norm", "router", "gate_up", "down"), grads[1:], w64)})
+    return errors
+
+
 if __name__ == "__main__":
     moe.build()
     print(f"served: relative error of the output {check_served():.1e}")
     print("trained: relative errors " + ", ".join(f"{k} {v:.1e}" for k, v in check_trained().items()))
+    print("block: relative errors " + ", ".join(f"{k} {v:.1e}" for k, v in check_block().items()))
