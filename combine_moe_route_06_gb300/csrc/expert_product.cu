@@ -21,6 +21,15 @@
 // A tensor map fills what lies outside the matrix with zeros, so N and K need no padding;
 // rows of B behind an expert's give columns of D that nobody reads.  Only for d_w are rows summed
 // over, and those behind the expert's are cleared in shared memory (they may hold anything).
+//
+// What bounds it: with up to some 290 rows an expert the bytes of the weights in use, above that the
+// tensor core.  48 rows over 36 experts of 5,120 x 2,048 take 115 us, 6.6 TB/s; 16,384 rows over 8
+// experts of 2,816 x 2,048, gated, 113 us at 1.57 GHz, 1.67 PFLOP/s, the tensor pipe active for 86% of
+// it, and 132 us where calls back to back keep the chip at its power limit.  A step's 64 KiB come from L2
+// (80% hits: pairs on neighbouring tiles); taken in contiguous ranges of tiles instead, 1.3 GB came from
+// HBM and the same call took 236 us.  Shared memory is the other limit: MMA operands and their loads
+// take about all of its bandwidth, so what the end of a tile does there counts (stores of single
+// values for 8 x 8 matrices: 119 us for 113).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -49,9 +58,12 @@ constexpr int kMmThreads = 32 * (kFinishWarps + 3);
 constexpr int kTmemColumns = 512;                // two tiles of 256 columns of sums
 constexpr int kSumSteps = 12;                    // d_w: steps summed by the tensor core alone
 // Steps worth a part of their own, for tiles of up to 64 rows and of more: the last one reads the sums
-// of all (375 rows over 4 experts of 48 x 4,040: 20.8 us with 8 steps, 16.4 with 16).
+// of all (375 rows over 4 experts of 48 x 4,040: 20.8 us with 8 steps, 18.0 with 16).
 constexpr int kMinPart = 8, kMinPartWide = 16;
-constexpr int kCutSteps = 40;                    // steps that the parts of cut tiles take to be joined
+// Steps that the parts of cut tiles take to be joined: where whole tiles leave the pairs waiting for less,
+// none is cut (16,384 rows over 8 experts: gated 2,816 x 2,048 125 us with 0, 118 with 24 or more; gradient
+// of 1,408 x 2,048 103 us with 0 or 12, 94 with 24, 93 with 40; shorter sums than this are never cut).
+constexpr int kCutSteps = 40;
 constexpr int64_t kPart = (int64_t)kTileRows * 128;   // sums of one part of a tile, in one CTA
 constexpr int kMaxCtas = 160;
 constexpr int kCols = 16;                        // columns of D that a warp finishes at once
@@ -83,6 +95,7 @@ struct Shared {
     volatile int dead;               // a wait gave up
 };
 constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kFinishWarps * kStaging + sizeof(Shared);
+
 struct Maps {
     CUtensorMap a, b[3];             // b: boxes of 16, 64 and 128 rows (d_w: the first, of 64)
     CUtensorMap d;                   // d_w
@@ -971,7 +984,7 @@ __device__ __forceinline__ int split_pairs(const Args &p, const Args &p_w)
 
 // Both gradients in one launch, each on pairs of its own: one start and one end, and one's stores beside
 // the other's MMAs (8 experts' 4,096 rows of 2,048 x 1,408: 63 us, 71 in two launches; 300 rows of 328 x 648
-// in five experts: 13 us, 19).
+// in five experts: 13 us, 19, before smaller tiles made it 11).
 template <int FORM>
 __global__ void __launch_bounds__(kMmThreads, 1)
     k_expert_gradients(const __grid_constant__ Maps maps, const __grid_constant__ Args p,
@@ -1100,7 +1113,7 @@ cudaError_t grid_of(int *ctas)
 }
 
 // Rows of a tile of the B side: half, or a quarter, of 256 where the tiles are few for the pairs all the
-// same (2,571 rows of 376 x 1,856: 16.5 us with 256, 13.2 with 128).
+// same (2,571 rows of 376 x 1,856: 16.5 us with 256, 12.4 with 128).
 int tile_rows(int pairs, int64_t tiles_a, int64_t rows, int64_t experts)
 {
     int most = kTileRows;
