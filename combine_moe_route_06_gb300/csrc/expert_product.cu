@@ -10,7 +10,7 @@
 // the weights, which then are the bound, always fill their side.  Each CTA of a pair
 // loads half of A and of B by TMA, holds 128 rows of D in tensor memory and finishes them.
 // Gated: A has 8 gate rows and the 8 up rows of the same outputs in turn, so that the two
-// factors of an output are eight lanes apart.
+// factors of an output meet in one thread (tmem_load_matrices).
 //
 // The work is a list of steps (expert, tile, 64 of the summed index).  Where there are many
 // tiles the pairs, one per two SMs, take them in turn; the last one or two per pair, or all of
