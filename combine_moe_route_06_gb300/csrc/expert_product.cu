@@ -766,7 +766,7 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
                 if (f.parts == 1 || f.here >= 0) tmem_load_matrices(sums + c0, v);
                 if (two) {
 #pragma unroll
-                    for (int j = 0; j < kCols; j++) v[j] += other[j];       // (the same in either order)
+                    for (int j = 0; j < kCols; j++) v[j] = 0.f + v[j] + other[j];   // (as add_parts, -0 too)
                 } else if (f.parts > 1) {
                     add_parts<FORM == kGateGrad ? 1 : 4>(f, c0, v);
                 }

@@ -85,6 +85,20 @@ def test_the_same_bytes_with_cut_tiles():
         assert torch.equal(d_a[used], d_a2[used]) and torch.equal(d_w, d_w2)
 
 
+def test_zeros_have_the_same_sign_every_time():
+    """Rows of zeros times negative weights, in tiles that are cut in two: whichever part is done last, the
+    sign bits of the results are the same."""
+    N, K, rows = 2560, 4160, Rows([700, 500], spare=0)
+    a, w = torch.zeros(rows.total, K, dtype=BF, device=DEV), -randn(20, 2, N, K).abs()
+    want = None
+    for _ in range(10):
+        y, _ = forward(rows, a, w, False, False)
+        assert bool((y == 0).all())
+        bits = y.view(torch.int16)
+        assert want is None or torch.equal(bits, want)
+        want = bits
+
+
 def test_calls_on_two_streams_at_once():
     """Two calls with workspaces of their own, enqueued on two streams without a wait between."""
     N, K, counts = 512, 4096, [300, 40]

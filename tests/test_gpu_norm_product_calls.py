@@ -124,7 +124,7 @@ def test_offsets_that_change_between_replays():
 
 def test_traced():
     """The calls' launches are among the traced kernels."""
-    args = inputs()
+    args = inputs(rows=1000)
     m.trace_enable(None, 64)
     try:
         step(*args)
