@@ -875,12 +875,19 @@ struct Memory {
     }
 };
 
-// Before the work is known: barriers, tensor memory, and the wait for the kernel before.
-__device__ __forceinline__ void start(Shared &sh, int warp)
+// Before the work is known: barriers, tensor memory, tensor maps, the pair's other CTA, and then the wait
+// for the kernel before, whose end all that runs beside.
+__device__ __forceinline__ void start(Shared &sh, int warp, const Maps &maps, const Maps &maps_w)
 {
     const int lane = threadIdx.x & 31;
     if (warp == kWarpLoad) {
         if (lane == 0) {
+            map_prefetch(&maps.a);
+            map_prefetch(&maps.b[0]);
+            if (&maps != &maps_w) {
+                map_prefetch(&maps_w.a);
+                map_prefetch(&maps_w.b[0]);
+            }
             sh.dead = 0;
             sh.first_pair = 0;
             sh.pairs = gridDim.x / 2;
@@ -901,18 +908,10 @@ __device__ __forceinline__ void start(Shared &sh, int warp)
         tmem_alloc_pair(&sh.tmem, kTmemColumns);
         tmem_fence_before();
     }
+    cluster_barrier();
+    tmem_fence_after();
     pdl_wait();
     pdl_trigger();
-}
-
-template <int FORM>
-__device__ __forceinline__ void scan_product(Shared &sh, const Maps &maps, const Args &p)
-{
-    if ((threadIdx.x & 31) == 0) {
-        map_prefetch(&maps.a);
-        map_prefetch(&maps.b[0]);
-    }
-    scan_experts<FORM>(sh, p, shape_of<FORM>(p));
 }
 
 // By all threads, after the load warp's scan.
@@ -952,11 +951,9 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     extern __shared__ uint8_t raw[];
     const Memory m(raw);
     const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
-    start(m.sh, warp);
-    if (warp == kWarpLoad) scan_product<FORM>(m.sh, maps, p);
+    start(m.sh, warp, maps, maps);
+    if (warp == kWarpLoad) scan_experts<FORM>(m.sh, p, shape_of<FORM>(p));
     __syncthreads();
-    cluster_barrier();
-    tmem_fence_after();
     run_product<FORM>(m.ring, m.sh, warp, maps, p);
     end(m.sh, warp, p.dev_status);
 }
@@ -993,7 +990,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     extern __shared__ uint8_t raw[];
     const Memory m(raw);
     const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
-    start(m.sh, warp);
+    start(m.sh, warp, maps, maps_w);
     if (warp == kWarpLoad) {
         const int split = split_pairs(p, p_w);
         const bool weights = (int)blockIdx.x / 2 >= split;
@@ -1003,12 +1000,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             m.sh.weights = weights;
         }
         __syncwarp();
-        if (weights) scan_product<kWeightGrad>(m.sh, maps_w, p_w);
-        else scan_product<FORM>(m.sh, maps, p);
+        if (weights) scan_experts<kWeightGrad>(m.sh, p_w, shape_of<kWeightGrad>(p_w));
+        else scan_experts<FORM>(m.sh, p, shape_of<FORM>(p));
     }
     __syncthreads();
-    cluster_barrier();
-    tmem_fence_after();
     if (m.sh.weights) run_product<kWeightGrad>(m.ring, m.sh, warp, maps_w, p_w);
     else run_product<FORM>(m.ring, m.sh, warp, maps, p);
     end(m.sh, warp, p.dev_status);
