@@ -50,7 +50,7 @@ enum Form { kPlain, kGated, kRowGrad, kGateGrad, kWeightGrad };
 
 constexpr int kStep = 64;                        // of the summed index, 128 bytes
 constexpr int kTileRows = 256;                   // rows of A and D, most rows of B
-constexpr int kStages = 6;
+constexpr int kStages = 6, kMaxStages = 10;      // of whole tiles, of tiles with few rows on the B side
 constexpr int kABytes = 128 * kStep * 2, kBBytes = 128 * kStep * 2, kStageBytes = kABytes + kBBytes;
 constexpr int kFinishWarps = 8;
 constexpr int kWarpLoad = kFinishWarps, kWarpMma = kFinishWarps + 1, kWarpClear = kFinishWarps + 2;
@@ -80,11 +80,12 @@ struct Segment {
 };
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages], landed[kStages], cleared[kStages];
+    uint64_t full[kMaxStages], empty[kMaxStages], landed[kStages], cleared[kStages];
     uint64_t sums_full[2], sums_empty[2];
     int before[kMaxE + 1];           // steps of the experts before e
     int start[kMaxE], count[kMaxE];
     uint32_t tmem;
+    int stages, stage_bytes;         // the ring of operands
     int first_pair, pairs;           // the pairs that share the work
     int tasks, waves;                // tiles, and how many of them a pair takes whole, in turn
     int shared;                      // first step of the rest, which is cut evenly
@@ -220,6 +221,9 @@ __device__ __forceinline__ int owner_of(const Shared &sh, int unit)
     return unit < longer ? unit / (sh.base + 1) : sh.more + (unit - longer) / sh.base;
 }
 
+// Rows of B that a CTA loads for `half` rows: by 16 up to 32, else 64 or 128.
+__device__ __forceinline__ int loaded_rows(int half) { return half <= 32 ? half : half <= 64 ? 64 : 128; }
+
 // By one warp: the experts' rows, and before[e], the steps of those before e.  Runs could only
 // overlap where the offsets fall: from there on no expert has rows.
 template <int FORM>
@@ -286,6 +290,10 @@ __device__ __forceinline__ void scan_experts(Shared &sh, const Args &p, const Sh
         const int rest = before - shared;
         // every pair takes part where that leaves it kMinPart steps or a tile
         const int parts = min(pairs, max(tasks - task, rest / (widest <= 64 ? kMinPart : kMinPartWide)));
+        // with few rows more stages fit the ring: more of the weights are under way
+        const int half = FORM == kWeightGrad ? 128 : (widest + 31) / 32 * 16;
+        sh.stage_bytes = kABytes + loaded_rows(half) * 128;
+        sh.stages = FORM == kWeightGrad ? kStages : min(kMaxStages, kStages * kStageBytes / sh.stage_bytes);
         sh.tasks = tasks;
         sh.waves = waves;
         sh.shared = shared;
@@ -315,15 +323,14 @@ __device__ __forceinline__ bool ragged_step(const Segment &g, int count, int c)
     return c == g.steps - 1 && count % kStep != 0;
 }
 
-// Rows of B that a CTA loads for `half` rows: by 16 up to 32, else 64 or 128.
-__device__ __forceinline__ int loaded_rows(int half) { return half <= 32 ? half : half <= 64 ? 64 : 128; }
-
 template <int FORM>
 __device__ __forceinline__ void load_steps(Shared &sh, uint8_t *ring, const Args &p, const Maps &maps, const Shape &w)
 {
     const uint32_t rank = cluster_rank();
     Walk<FORM> walk(sh, p, w);
     Segment g;
+    const int stages = FORM == kWeightGrad ? kStages : sh.stages;
+    const int stage_bytes = FORM == kWeightGrad ? kStageBytes : sh.stage_bytes;
     int s = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -336,7 +343,7 @@ __device__ __forceinline__ void load_steps(Shared &sh, uint8_t *ring, const Args
         for (int c = g.c0; c < g.c1; c++) {
             if (!(ok = mbar_wait_cluster(&sh.empty[s], phase ^ 1, &sh.dead))) break;
             if (elect_lane()) {
-                uint8_t *at = ring + s * kStageBytes, *bt = at + kABytes;
+                uint8_t *at = ring + s * stage_bytes, *bt = at + kABytes;
                 uint32_t bar = cluster_addr(&sh.full[s], 0);
                 if constexpr (FORM == kWeightGrad) {
                     // the last rows of an expert go by this CTA's warp that clears what is behind
@@ -376,16 +383,16 @@ __device__ __forceinline__ void load_steps(Shared &sh, uint8_t *ring, const Args
                 }
             }
             __syncwarp();
-            if (++s == kStages) {
+            if (++s == stages) {
                 s = 0;
                 phase ^= 1;
             }
         }
     }
     // the stages in use come free before the CTA ends: then no copy, MMA or arrival is under way
-    for (int i = 0; ok && i < kStages; i++) {
+    for (int i = 0; ok && i < stages; i++) {
         ok = mbar_wait_cluster(&sh.empty[s], phase ^ 1, &sh.dead);
-        if (++s == kStages) {
+        if (++s == stages) {
             s = 0;
             phase ^= 1;
         }
@@ -437,6 +444,8 @@ __device__ __forceinline__ void issue_steps(Shared &sh, uint8_t *ring, const Arg
     constexpr bool kAByK = FORM == kPlain || FORM == kGated, kBByK = FORM != kWeightGrad;
     Walk<FORM> walk(sh, p, w);
     Segment g;
+    const int stages = FORM == kWeightGrad ? kStages : sh.stages;
+    const int stage_bytes = FORM == kWeightGrad ? kStageBytes : sh.stage_bytes;
     int s = 0, d = 0;
     uint32_t phase = 0, sums_phase = 0, cleared = 0;
     bool ok = true;
@@ -460,7 +469,7 @@ __device__ __forceinline__ void issue_steps(Shared &sh, uint8_t *ring, const Arg
                 cleared ^= 1u << s;
             }
             tmem_fence_after();
-            const uint32_t at = smem_addr(ring) + s * kStageBytes, bt = at + kABytes;
+            const uint32_t at = smem_addr(ring) + s * stage_bytes, bt = at + kABytes;
             const uint64_t a = kAByK ? mma_smem_word(at, 1024) : mma_across_word(at, 8192);
             const uint64_t b = kBByK ? mma_smem_word(bt, 1024) : mma_across_word(bt, 8192);
             const int n = FORM == kWeightGrad ? mma_steps(valid_rows(sh.count[g.e], c)) : 4;
@@ -474,7 +483,7 @@ __device__ __forceinline__ void issue_steps(Shared &sh, uint8_t *ring, const Arg
                 if (left == 0) mma_commit_pair(&sh.sums_full[d]);
             }
             __syncwarp();
-            if (++s == kStages) {
+            if (++s == stages) {
                 s = 0;
                 phase ^= 1;
             }
@@ -893,9 +902,11 @@ __device__ __forceinline__ void start(Shared &sh, int warp, const Maps &maps, co
             sh.pairs = gridDim.x / 2;
         }
     } else if (warp == kWarpMma) {
-        if (lane < kStages) {
+        if (lane < kMaxStages) {
             mbar_init(&sh.full[lane], 1);
             mbar_init(&sh.empty[lane], 1);
+        }
+        if (lane < kStages) {
             mbar_init(&sh.landed[lane], 1);
             mbar_init(&sh.cleared[lane], 2);
         }
