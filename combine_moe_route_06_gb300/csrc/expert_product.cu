@@ -168,6 +168,7 @@ struct Walk {
             __ballot_sync(kFull, lane < step && base + lane < w.E && sh.before[base + lane] <= at);
         return base + 31 - __clz((int)below2);
     }
+    __device__ bool over() const { return (wave >= sh.waves || wave * sh.pairs + (int)(blockIdx.x / 2) - sh.first_pair >= sh.tasks) && at >= to; }
     __device__ bool next(Segment &g)
     {
         int task, count;
@@ -499,7 +500,7 @@ __device__ __forceinline__ void issue_steps(Shared &sh, uint8_t *ring, const Arg
 
 struct Finish {
     int first, parts;          // parts of a cut tile: the pair that has the first one, how many
-    int here;                  // which of them this CTA holds and has not stored (-1: none)
+    int here;                  // which of them this CTA holds
     const float *from;         // this thread's place in the first one
 };
 
@@ -577,7 +578,6 @@ template <typename Store>
 __device__ __forceinline__ bool join_parts(Shared &sh, const Args &p, const Segment &g, Finish &f, bool early, Store store)
 {
     if (f.parts == 1 || early) return true;
-    f.here = -1;
     // (the thread's place among the 128 of a row block is the same for the warps that share its columns)
     store(p.partial + (int64_t)(2 * blockIdx.x + (g.c0 == 0)) * kPart + (threadIdx.x & 127) * 4);
     __threadfence();
@@ -731,8 +731,52 @@ __device__ __forceinline__ void weights_out(const CUtensorMap *map, uint8_t *sta
     if (lane == 0) tile_store3(map, k, n0, e, staging);
 }
 
+// The other parts of a cut tile into the ring, when it is no longer in use: all of their loads at once, where
+// they fit (82 rows over 2 experts of 2,496 x 3,808: 17.8 us, 19 a block of columns at a time).  A thread
+// reads what it has copied itself.
+constexpr int kRingBlocks = kStages * kStageBytes / (kFinishWarps * 32 * kCols * 4);
+__device__ __forceinline__ int4 *ring_block(uint8_t *ring, int i, int j)
+{
+    return (int4 *)ring + (i * (kCols / 4) + j) * (kFinishWarps * 32) + threadIdx.x;
+}
+__device__ __forceinline__ void copy_parts(uint8_t *ring, const Finish &f, int c0, int turn, int rows)
+{
+    int i = 0;
+    for (int q = 0; q < f.parts; q++) {
+        if (q == f.here) continue;
+        const float *part = f.from + (4 * q + (q == 0)) * kPart;
+        for (int c = c0; c < rows; c += turn, i++)
+#pragma unroll
+            for (int j = 0; j < kCols / 4; j++)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(ring_block(ring, i, j))),
+                             "l"(part + (c + 4 * j) * 128)
+                             : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+// Block b (of `blocks`) of the tile out of them, over all parts in their order.
+__device__ __forceinline__ void add_copies(uint8_t *ring, const Finish &f, int b, int blocks, float (&v)[kCols])
+{
+    float sum[kCols] = {};
+    for (int q = 0, i = b; q < f.parts; q++) {
+        if (q == f.here) {
+#pragma unroll
+            for (int j = 0; j < kCols; j++) sum[j] += v[j];
+            continue;
+        }
+#pragma unroll
+        for (int j = 0; j < kCols / 4; j++) {
+            const float4 x = *(const float4 *)ring_block(ring, i, j);
+            sum[4 * j] += x.x, sum[4 * j + 1] += x.y, sum[4 * j + 2] += x.z, sum[4 * j + 3] += x.w;
+        }
+        i += blocks;
+    }
+#pragma unroll
+    for (int j = 0; j < kCols; j++) v[j] = sum[j];
+}
+
 template <int FORM>
-__device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const Args &p, const Shape &w)
+__device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *ring, uint8_t *staging, const Args &p, const Shape &w)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3, group = warp >> 2;
     constexpr int kTurn = kGroups * kCols;
@@ -745,7 +789,7 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
     while (walk.next(g)) {
         const int a_row = g.tile * kTileRows + rank * 128 + quarter * 32;    // the warp's first row of A
         const int64_t first = sh.start[g.e] + g.row0;
-        int4 gates[4];
+        int4 gates[4];                                   // loaded a block of rows ahead
         if constexpr (FORM == kGateGrad) load_gates(p, first + group * kCols, g.rows - group * kCols, a_row, gates);
         Finish f;
         find_parts(sh, g, f);
@@ -764,25 +808,19 @@ __device__ __forceinline__ void finish_steps(Shared &sh, uint8_t *staging, const
         });
         if (finish) {
             f.from = parts_from(sh, p, f);
-            // the other part of a tile in two is loaded a block of columns ahead
-            const bool two = f.parts == 2 && f.here >= 0;
-            float other[kCols] = {}, ahead[kCols] = {};
-            if (two) load_part(f, f.here ^ 1, group * kCols, other);
+            const int blocks = max(0, (g.rows - group * kCols + kTurn - 1) / kTurn);
+            // (gate and up in their registers' place: 16,384 rows' gradients take 144 us without, 148 with)
+            const bool copied = FORM != kGateGrad && f.parts > 1 && walk.over() && (f.parts - 1) * blocks <= kRingBlocks;
+            if (copied) copy_parts(ring, f, group * kCols, kTurn, g.rows);
+            int b = 0;
 #pragma unroll 1
-            for (int c0 = group * kCols; c0 < g.rows; c0 += kTurn) {
+            for (int c0 = group * kCols; c0 < g.rows; c0 += kTurn, b++) {
                 float v[kCols];
-                if (two && c0 + kTurn < g.rows) load_part(f, f.here ^ 1, c0 + kTurn, ahead);
-                if (f.parts == 1 || f.here >= 0) tmem_load_matrices(sums + c0, v);
-                if (two) {
-#pragma unroll
-                    for (int j = 0; j < kCols; j++) v[j] = 0.f + v[j] + other[j];   // (as add_parts, -0 too)
-                } else if (f.parts > 1) {
-                    add_parts<FORM == kGateGrad ? 1 : 4>(f, c0, v);
-                }
-#pragma unroll
-                for (int j = 0; j < kCols; j++) other[j] = ahead[j];
                 int4 next[4];
                 if constexpr (FORM == kGateGrad) load_gates(p, first + c0 + kTurn, g.rows - c0 - kTurn, a_row, next);
+                tmem_load_matrices(sums + c0, v);
+                if (copied) add_copies(ring, f, b, blocks, v);
+                else if (f.parts > 1) add_parts<FORM == kGateGrad ? 1 : 4>(f, c0, v);
                 finish_rows<FORM>(p, staging, v, first + c0, g.rows - c0, FORM == kGated ? a_row / 2 : a_row, gates);
                 if constexpr (FORM == kGateGrad)
 #pragma unroll
@@ -841,6 +879,7 @@ __device__ __forceinline__ void finish_weights(Shared &sh, uint8_t *staging, con
         const int a_row = g.tile * kTileRows + rank * 128 + quarter * 32;    // the warp's first row of A
         Finish f;
         find_parts(sh, g, f);
+        // (the last one reads all parts from memory: what it holds has no registers beside them)
         const bool finish = join_parts(sh, p, g, f, false, [&](float *slot) {
 #pragma unroll
             for (int b = 0; b < kBlocks; b++)
@@ -939,7 +978,7 @@ __device__ __forceinline__ void run_product(uint8_t *ring, Shared &sh, int warp,
         if constexpr (FORM == kWeightGrad) clear_steps(sh, ring, p, shape);
     } else {
         if constexpr (FORM == kWeightGrad) finish_weights(sh, staging, p, maps, shape);
-        else finish_steps<FORM>(sh, staging, p, shape);
+        else finish_steps<FORM>(sh, ring, staging, p, shape);
     }
 }
 
