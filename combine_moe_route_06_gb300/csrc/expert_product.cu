@@ -23,9 +23,9 @@
 // over, and those behind the expert's are cleared in shared memory (they may hold anything).
 //
 // What bounds it: with up to some 290 rows an expert the bytes of the weights in use, above that the
-// tensor core.  48 rows over 36 experts of 5,120 x 2,048 take 115 us, 6.6 TB/s; 16,384 rows over 8
-// experts of 2,816 x 2,048, gated, 113 us at 1.57 GHz, 1.67 PFLOP/s, the tensor pipe active for 86% of
-// it, and 132 us where calls back to back keep the chip at its power limit.  A step's 64 KiB come from L2
+// tensor core.  48 rows over 36 experts of 5,120 x 2,048 take 114 us, 6.6 TB/s; 16,384 rows over 8
+// experts of 2,816 x 2,048, gated, 113 us at 1.57 GHz, 1.67 PFLOP/s, the tensor pipe active for 87% of
+// it, and 131 us where calls back to back keep the chip at its power limit.  A step's 64 KiB come from L2
 // (80% hits: pairs on neighbouring tiles); taken in contiguous ranges of tiles instead, 1.3 GB came from
 // HBM and the same call took 236 us.  Shared memory is the other limit: MMA operands and their loads
 // take about all of its bandwidth, so what the end of a tile does there counts (stores of single

@@ -16,7 +16,7 @@
 // rows' parts of d_w in registers, writes them to the workspace, and a second kernel
 // sums the CTAs' parts in their order.
 //
-// (16,384 rows of 5,120 with a residual's gradient: 113 us, 5.9 TB/s.)
+// (16,384 rows of 5,120 with a residual's gradient: 104 us, 6.45 TB/s.)
 //
 // Both are bound by HBM.
 #include <cuda_bf16.h>
@@ -252,7 +252,7 @@ template <int NV, int WARPS>
 constexpr size_t kMergeBytes = kTeams<WARPS> > 1 ? (size_t)NV * 8 * kThreads<WARPS> * 4 : 0;
 
 // (By way of L1: the two halves of a thread's 32 bytes of fp32 are copies of their own, and past L1 each
-// fetches the whole sector.  16,384 rows of 5,120: 198 us, 265 without.)
+// fetches the whole sector.  16,384 rows of 5,120 in fp32: 198 us, 265 without; in bf16 104 and 113.)
 __device__ __forceinline__ void copy_ahead(int4 *to, const int4 *from)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
@@ -432,10 +432,11 @@ cudaError_t norm(const NormArgs &p, cudaStream_t st)
 template <int NV, int WARPS, bool F32>
 cudaError_t norm_backward(const NormBackArgs &p, float *d_w, cudaStream_t st)
 {
-    // three rows in the ring where two CTAs of them fit an SM, else two (113 us; 130 with two rows, 182
-    // straight into registers).  Teams of sixteen warps have an SM's registers to themselves, and take four
-    // rows or what its shared memory holds (9,000 rows of 6,000 in fp32: 134 us, 201 straight into
-    // registers); with four vectors a thread too that is slower (4,000 rows of 16,000: 148 us for 129).
+    // Three rows in the ring where two CTAs of them fit an SM, else two (16,384 rows of 5,120: 104 us; past
+    // L1, 116 with three rows, 130 with two and 182 straight into registers).  Teams of sixteen warps have
+    // an SM's registers to themselves, and take four rows or what its shared memory holds (9,000 rows of
+    // 6,000 in fp32: 134 us, 201 straight into registers); with four vectors a thread too that is slower
+    // (4,000 rows of 16,000: 148 us for 129).
     constexpr bool kAlone = WARPS >= 16 && NV <= 2;
     constexpr size_t kRoom = kAlone ? 220 * 1024 : 110 * 1024;
     constexpr int kAhead = kAlone && kRingBytes<NV, WARPS, F32, 4> <= kRoom ? 4
@@ -479,7 +480,7 @@ cudaError_t norm_backward(const NormBackArgs &p, float *d_w, cudaStream_t st)
 // Several small teams share a CTA: CTAs of 128 threads start too slowly for short rows (10,525 rows of
 // 1,320: 11.7 us, 14.4 with a CTA a row).
 // Backward: two vectors a thread where that holds the row, which leaves registers for twenty or
-// more warps an SM (16,384 rows of 5,120: 113 us with ten warps and two vectors, 187 with four and five).
+// more warps an SM (16,384 rows of 5,120: 116 us with ten warps and two vectors, 187 with four and five, past L1).
 #define BY_WIDTH_BACK(V, CALL)          \
     if ((V) <= 32) return CALL(1, 1);   \
     if ((V) <= 64) return CALL(2, 1);   \
