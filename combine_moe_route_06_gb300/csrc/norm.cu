@@ -259,8 +259,14 @@ __device__ __forceinline__ void copy_ahead(int4 *to, const int4 *from)
                  : "memory");
 }
 
+// CTAs that an SM has registers for.  Two of bf16 rows where teams are small (16,384 rows of 5,120: 104 us,
+// 111 with one).  One of fp32 rows: the rings of two leave L1 too little for the second halves of
+// sectors (266 us, 198 with one).
+template <int WARPS, bool F32>
+constexpr int kCtas = WARPS >= 16 || F32 ? 1 : 2;
+
 template <int NV, int WARPS, bool F32, int AHEAD>
-__global__ void __launch_bounds__(kThreads<WARPS>) k_rms_norm_backward(const __grid_constant__ NormBackArgs p)
+__global__ void __launch_bounds__(kThreads<WARPS>, kCtas<WARPS, F32>) k_rms_norm_backward(const __grid_constant__ NormBackArgs p)
 {
     extern __shared__ int4 ring[];
     pdl_wait();
