@@ -168,7 +168,12 @@ struct Walk {
             __ballot_sync(kFull, lane < step && base + lane < w.E && sh.before[base + lane] <= at);
         return base + 31 - __clz((int)below2);
     }
-    __device__ bool over() const { return (wave >= sh.waves || wave * sh.pairs + (int)(blockIdx.x / 2) - sh.first_pair >= sh.tasks) && at >= to; }
+    // no segment is left
+    __device__ bool over() const
+    {
+        const int task = wave * sh.pairs + (int)(blockIdx.x / 2) - sh.first_pair;
+        return (wave >= sh.waves || task >= sh.tasks) && at >= to;
+    }
     __device__ bool next(Segment &g)
     {
         int task, count;
