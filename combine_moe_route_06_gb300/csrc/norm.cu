@@ -266,7 +266,8 @@ template <int WARPS, bool F32>
 constexpr int kCtas = WARPS >= 16 || F32 ? 1 : 2;
 
 template <int NV, int WARPS, bool F32, int AHEAD>
-__global__ void __launch_bounds__(kThreads<WARPS>, kCtas<WARPS, F32>) k_rms_norm_backward(const __grid_constant__ NormBackArgs p)
+__global__ void __launch_bounds__(kThreads<WARPS>, kCtas<WARPS, F32>)
+    k_rms_norm_backward(const __grid_constant__ NormBackArgs p)
 {
     extern __shared__ int4 ring[];
     pdl_wait();
