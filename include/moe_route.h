@@ -812,7 +812,8 @@ moe_status_t moe_expert_product(const uint16_t *a, int a_rows, const int32_t *ex
  *                (moe_dispatch, moe_dispatch_pack_permute; H a multiple of 512) instead of
  *                being quantized on the way.
  * One of y and record at least.  All arrays apart from each other but for residual_out.
- * H a multiple of 8, at most 32768; eps > 0.  A row whose mean square leaves fp32 is 0.
+ * H a multiple of 8, at most 32768; eps > 0 (the mean square is off by up to 2^-134, which matters only
+ * to an eps below 2^-100).  A row whose mean square leaves fp32 is 0.
  */
 moe_status_t moe_rms_norm(const uint16_t *x, const void *residual, int residual_type,
                           const void *weight, int weight_type, int64_t rows, int H, float eps,
@@ -940,7 +941,8 @@ moe_status_t moe_expert_product_backward(const uint16_t *d_y, const uint16_t *a,
  *   d_weight   [H] float32 out or NULL; sums in fp32 in a fixed order.
  *   ws         moe_rms_norm_backward_workspace_bytes(rows, H) bytes, 256-byte aligned, for
  *              d_weight.
- * All arrays apart from each other but for d_residual.  Sizes and eps as moe_rms_norm.
+ * All arrays apart from each other but for d_residual.  Sizes and eps as moe_rms_norm.  Of a row whose
+ * mean square leaves fp32 d_h is d_residual (NaN where the sum of q h leaves it too).
  */
 size_t moe_rms_norm_backward_workspace_bytes(int64_t rows, int H);
 moe_status_t moe_rms_norm_backward(const uint16_t *d_y, const void *h, int h_type, const void *weight,
