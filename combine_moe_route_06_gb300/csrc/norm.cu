@@ -267,11 +267,14 @@ __device__ __forceinline__ void copy_ahead(int4 *to, const int4 *from)
                  : "memory");
 }
 
-// CTAs that an SM has registers for.  Two of bf16 rows where teams are small (16,384 rows of 5,120: 104 us,
-// 111 with one).  One of fp32 rows: the rings of two leave L1 too little for the second halves of
-// sectors (266 us, 198 with one).
+// CTAs that an SM has registers for at least: two of bf16 rows in small teams (16,384 rows of 5,120: 104 us,
+// 111 with one).  Of fp32 rows there are as many as the registers come to, three in the forms of one vector, two
+// in small teams of two vectors, but one in teams of ten warps: the rings of two leave L1 too little for the
+// second halves of sectors (16,384 rows of 5,120: 266 us, 198 with one), which the grid sees to.
 template <int WARPS, bool F32>
 constexpr int kCtas = WARPS >= 16 || F32 ? 1 : 2;
+template <int WARPS, bool F32>
+constexpr bool kOneCta = F32 && WARPS == 10;
 
 template <int NV, int WARPS, bool F32, int AHEAD>
 __global__ void __launch_bounds__(kThreads<WARPS>, kCtas<WARPS, F32>)
@@ -467,6 +470,12 @@ cudaError_t norm_backward(const NormBackArgs &p, float *d_w, cudaStream_t st)
     if (err != cudaSuccess) return err;
     int64_t fit = resident_grid((const void *)kernel, kThreads<WARPS>, kSmem);
     if (fit <= 0 || fit > kMaxParts) fit = kMaxParts;
+    if (kOneCta<WARPS, F32>) {
+        DeviceInfo di;
+        err = device_info(&di);
+        if (err != cudaSuccess) return err;
+        if (fit > di.sm_count) fit = di.sm_count;
+    }
     const int64_t grid = want > fit ? fit : want;
     if (grid > 0) {
         MOE_TRACED_LAUNCH("k_rms_norm_backward", st,
