@@ -108,7 +108,6 @@ struct Args {
     int most;                        // rows of a tile of the B side: 256, 128 or 64
     __nv_bfloat16 *out, *keep;
     const __nv_bfloat16 *pre;
-    void *d_w;
     bool d_w_f32;
     float *partial;
     int32_t *arrivals;
@@ -1246,7 +1245,7 @@ cudaError_t launch_expert_product(const uint16_t *a, int a_rows, const int32_t *
     if (err == cudaSuccess) err = row_boxes(maps, a, a_rows, K, most);
     if (err != cudaSuccess) return err;
     const Args p{offsets, counts, block_rows, a_rows, E, N, K, rows_w, K, most, (__nv_bfloat16 *)y,
-                 (__nv_bfloat16 *)pre, nullptr, nullptr, false, nullptr, nullptr, dev_status};
+                 (__nv_bfloat16 *)pre, nullptr, false, nullptr, nullptr, dev_status};
     if (may_cut(K)) err = begin(ws, st);
     if (err != cudaSuccess) return err;
     return gated ? product<kGated>(maps, p, ctas, ws, st) : product<kPlain>(maps, p, ctas, ws, st);
@@ -1268,7 +1267,7 @@ cudaError_t launch_expert_product_backward(const uint16_t *d_y, const uint16_t *
     const int pairs = d_a && d_w ? ctas / 4 : ctas / 2;
     const int64_t tiles_n = (N + kTileRows - 1) / kTileRows, tiles_k = (K + kTileRows - 1) / kTileRows;
     Args p{offsets, counts, block_rows, a_rows, E, N, K, K, N, tile_rows(pairs, tiles_k, a_rows, a_rows < E ? a_rows : E),
-           (__nv_bfloat16 *)d_a, nullptr, (const __nv_bfloat16 *)pre, d_w, d_w_type == MOE_TYPE_F32, nullptr, nullptr,
+           (__nv_bfloat16 *)d_a, nullptr, (const __nv_bfloat16 *)pre, d_w_type == MOE_TYPE_F32, nullptr, nullptr,
            dev_status};
     Args p_w = p;
     p_w.most = tile_rows(pairs, E * tiles_n, K, 1);
