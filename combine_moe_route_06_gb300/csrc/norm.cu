@@ -16,9 +16,10 @@
 // rows' parts of d_w in registers, writes them to the workspace, and a second kernel
 // sums the CTAs' parts in their order.
 //
-// (16,384 rows of 5,120 with a residual's gradient: 104 us, 6.45 TB/s.)
+// (16,384 rows of 5,120 with a residual's gradient: 104.7 us, 6.4 TB/s; rows wider than 8,192 are far from that,
+// 1,500 of 30,000 208 us, 1.7 TB/s: no row is copied ahead, and 32 warps leave a thread too few registers.)
 //
-// Both are bound by HBM.
+// Both are bound by HBM, but for those.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -260,7 +261,7 @@ template <int NV, int WARPS>
 constexpr size_t kMergeBytes = kTeams<WARPS> > 1 ? (size_t)NV * 8 * kThreads<WARPS> * 4 : 0;
 
 // (By way of L1: the two halves of a thread's 32 bytes of fp32 are copies of their own, and past L1 each
-// fetches the whole sector.  16,384 rows of 5,120 in fp32: 198 us, 265 without; in bf16 104 and 113.)
+// fetches the whole sector.  16,384 rows of 5,120 in fp32: 198 us, 265 without; in bf16 105 and 113.)
 __device__ __forceinline__ void copy_ahead(int4 *to, const int4 *from)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
@@ -451,7 +452,7 @@ cudaError_t norm(const NormArgs &p, cudaStream_t st)
 template <int NV, int WARPS, bool F32>
 cudaError_t norm_backward(const NormBackArgs &p, float *d_w, cudaStream_t st)
 {
-    // Three rows in the ring where two CTAs of them fit an SM, else two (16,384 rows of 5,120: 104 us; past
+    // Three rows in the ring where two CTAs of them fit an SM, else two (16,384 rows of 5,120: 105 us; past
     // L1, 116 with three rows, 130 with two and 182 straight into registers).  Teams of sixteen warps have
     // an SM's registers to themselves, and take four rows or what its shared memory holds (9,000 rows of
     // 6,000 in fp32: 134 us, 201 straight into registers); with four vectors a thread too that is slower
